@@ -16,6 +16,13 @@ streams.
     vocab_shard / score_shard / merge_shards              -> vocabulary-parallel scoring
     correct(rollout, train, mask, ...)                    -> TIS/MIS weights, rejection
     align(hidden, input_ids, response_mask)               -> rows, targets, mask
+
+On rows of logits (logits.py, include/liblp_logits.h):
+
+    sample(logits, u, temperature, top_k, top_p, min_p)   -> token, logprob, processed, kept
+    top_logprobs(logits, k, temperature)                  -> ids, logits, logprobs
+    distill(logits, ids, teacher, ...)                    -> loss, differentiable
+    distill_forward / distill_backward / distill_step     -> its directions by hand
 """
 
 from __future__ import annotations
@@ -29,6 +36,8 @@ import torch
 from ._lib import (CORR_SEQ_DTYPE, EXPORTS, LP_OK, REJECT_K1, REJECT_K3,  # noqa: F401
                    REJECT_NONE, SEQ_STATS_DTYPE, TAIL_STATS_DTYPE, WORST_DTYPE, WORST_MAX, LpError,
                    lib, status_string)
+from .logits import (distill, distill_backward, distill_forward, distill_step, sample,  # noqa: F401
+                     top_logprobs)
 
 PAIRS = ("AB", "BC", "AC")
 

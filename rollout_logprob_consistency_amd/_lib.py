@@ -1,4 +1,4 @@
-"""ctypes declarations of the liblp C ABI (include/liblp.h).
+"""ctypes declarations of the liblp C ABI (include/liblp.h, include/liblp_logits.h).
 
 The shared library must have been built in-tree (build.py); importing the
 package without it raises, there is no fallback path.
@@ -24,6 +24,11 @@ EXPORTS = ("lp_status_string", "lp_score_workspace_bytes", "lp_score",
            "lp_correct", "lp_score_ex_workspace_bytes", "lp_score_ex",
            "lp_compare_tails_ex_workspace_bytes", "lp_compare_tails_ex",
            "lp_compare_quantiles", "lp_score_noalloc")
+
+# Names of every function include/liblp_logits.h declares.
+LOGITS_EXPORTS = ("lp_sample_workspace_bytes", "lp_sample", "lp_top_logprobs_workspace_bytes",
+                  "lp_top_logprobs", "lp_distill_workspace_bytes", "lp_distill_forward",
+                  "lp_distill_backward", "lp_distill_step")
 
 REJECT_NONE, REJECT_K1, REJECT_K3 = 0, 1, 3  # LP_REJECT_*
 
@@ -64,6 +69,10 @@ assert TAIL_STATS_DTYPE.itemsize == 64
 WORST_DTYPE = np.dtype([("abs_delta", "<f8"), ("seq", "<i4"), ("pos", "<i4")], align=True)
 assert WORST_DTYPE.itemsize == 16
 WORST_MAX = 4096  # LP_WORST_MAX
+SELECT_MAX_VOCAB = 1048576  # LP_SELECT_MAX_VOCAB
+TOP_MAX = 1024  # LP_TOP_MAX
+DISTILL_MAX_K = 1024  # LP_DISTILL_MAX_K
+DISTILL_LOGPROBS = 1  # LP_DISTILL_LOGPROBS
 NOALLOC_SCRATCH_BYTES = 32 << 20  # LP_NOALLOC_SCRATCH_BYTES
 
 
@@ -137,6 +146,22 @@ def lib() -> ctypes.CDLL:
     f64 = ctypes.c_double
     L.lp_correct.restype = ctypes.c_int
     L.lp_correct.argtypes = [vp, vp, vp, i64, i64, i64, f64, f64, f64, i32, f64, f64, vp, vp, vp]
+    sz = ctypes.c_size_t
+    for name in ("lp_sample_workspace_bytes", "lp_top_logprobs_workspace_bytes",
+                 "lp_distill_workspace_bytes"):
+        getattr(L, name).restype = sz
+        getattr(L, name).argtypes = [i64, i64, i32]
+    for name in ("lp_sample", "lp_top_logprobs", "lp_distill_forward", "lp_distill_backward",
+                 "lp_distill_step"):
+        getattr(L, name).restype = ctypes.c_int
+    rows = [vp, i64, i32, i64, i64]  # logits, ld, dtype, rows, V_true
+    L.lp_sample.argtypes = rows + [vp, vp, f32, vp, i32, vp, f32, vp, f32, vp, vp, vp, vp, vp,
+                                   vp, sz, vp]
+    L.lp_top_logprobs.argtypes = rows + [i32, f32, vp, vp, vp, vp, vp, vp, sz, vp]
+    L.lp_distill_forward.argtypes = rows + [vp, vp, i64, f32, u32, vp, vp, vp, vp, sz, vp]
+    L.lp_distill_backward.argtypes = rows + [i64, vp, vp, i64, f32, u32, vp, vp, vp, i64, vp]
+    L.lp_distill_step.argtypes = rows + [i64, vp, vp, i64, f32, u32, vp, vp, vp, i64, vp, vp, sz,
+                                         vp]
     _lib = L
     return L
 

@@ -1,0 +1,162 @@
+// Shared by the operators on rows of logits (include/liblp_logits.h):
+// element types, row loads, and the launch interface between the C-ABI host
+// code and the kernels.
+#pragma once
+
+#include <hip/hip_fp16.h>
+
+#include "liblp_logits.h"
+#include "lp_internal.h"
+
+namespace lp {
+
+// Element types of a row of logits. kVec elements make one 16-byte load.
+struct F32 {
+  using Raw = uint32_t;
+  static constexpr int kVec = 4;
+  static constexpr Raw kNegInf = 0xFF800000u;
+  static __device__ __forceinline__ float value(Raw r) { return __uint_as_float(r); }
+  static __device__ __forceinline__ Raw round(float v) { return __float_as_uint(v); }
+};
+
+struct BF16 {
+  using Raw = uint16_t;
+  static constexpr int kVec = 8;
+  static constexpr Raw kNegInf = 0xFF80u;
+  static __device__ __forceinline__ float value(Raw r) { return __uint_as_float((uint32_t)r << 16); }
+  // Nearest, ties to even; a NaN keeps its top bits and stays one.
+  static __device__ __forceinline__ Raw round(float v) {
+    const __bf16 b = (__bf16)v;
+    return __builtin_bit_cast(uint16_t, b);
+  }
+};
+
+struct F16 {
+  using Raw = uint16_t;
+  static constexpr int kVec = 8;
+  static constexpr Raw kNegInf = 0xFC00u;
+  static __device__ __forceinline__ float value(Raw r) {
+    return (float)__builtin_bit_cast(_Float16, r);
+  }
+  static __device__ __forceinline__ Raw round(float v) {
+    const _Float16 h = (_Float16)v;
+    return __builtin_bit_cast(uint16_t, h);
+  }
+};
+
+constexpr int64_t dtype_bytes(int32_t dtype) { return dtype == LP_F32 ? 4 : 2; }
+
+// One 16-byte group of a row: elements [i, i + kVec) of p. Groups are counted
+// from the row's start, never from an aligned address, so which elements a
+// lane holds does not depend on where the row lies (gfx950 takes global loads
+// and stores of 16 bytes at any alignment of the element type). A group that
+// reaches past `end` is loaded element by element and filled with -inf.
+template <class D>
+struct Group {
+  typename D::Raw r[D::kVec];
+};
+
+template <class D>
+__device__ __forceinline__ Group<D> load_group(const typename D::Raw* p, int64_t i, int64_t end) {
+  Group<D> g;
+  if (i + D::kVec <= end) {
+    __builtin_memcpy(&g, p + i, 16);
+  } else {
+#pragma unroll
+    for (int j = 0; j < D::kVec; ++j) g.r[j] = i + j < end ? p[i + j] : D::kNegInf;
+  }
+  return g;
+}
+
+template <class D>
+__device__ __forceinline__ void store_group(typename D::Raw* p, int64_t i, int64_t end,
+                                            const Group<D>& g) {
+  if (i + D::kVec <= end) {
+    __builtin_memcpy(p + i, &g, 16);
+  } else {
+#pragma unroll
+    for (int j = 0; j < D::kVec; ++j)
+      if (i + j < end) p[i + j] = g.r[j];
+  }
+}
+
+// ---- Distillation ---------------------------------------------------------
+
+// A row's vocabulary is cut into slices of equal length (a multiple of the
+// 16-byte group), one workgroup each. The cut depends on V_true and the dtype
+// only: a row's sums have the same order in every batch.
+constexpr int kDistillThreads = 256;
+constexpr int kDistillGroups = 8;  // 16-byte groups per thread and slice, at most
+
+struct DistillSlices {
+  int32_t n;    // slices per row
+  int64_t len;  // elements per slice
+};
+DistillSlices distill_slices(int64_t V_true, int32_t dtype);
+
+struct DistillArgs {
+  const void* logits;
+  int64_t ld;
+  int32_t dtype;
+  int64_t T, V_true, V_columns;
+  const int64_t* ids;      // [T, K]
+  const float* teacher;    // [T, K]
+  int32_t K;
+  bool logprobs;           // teacher entries are logprobs, taken as they are
+  double inv_tau;
+  float scale2;            // log2(e) / temperature
+  DistillSlices slices;
+  float* part_m;           // [T][n] slice maximum of z
+  double* part_s;          // [T][n] sum of exp((z - slice maximum) / tau)
+  float* out_loss;         // [T]
+  double* state;           // [T][4] or null
+  const double* state_in;  // [T][4] (backward)
+  const float* grad;       // [T] (backward)
+  void* out_grad;          // [T, ld_grad] (backward)
+  int64_t ld_grad;
+  int32_t* bad_rows;       // or null
+};
+
+struct DistillWorkspace {
+  size_t off_m, off_s, off_state, total;
+};
+DistillWorkspace distill_workspace_layout(int64_t T, int64_t V_true, int32_t dtype);
+
+hipError_t launch_distill_forward(const DistillArgs& a, hipStream_t stream);
+hipError_t launch_distill_backward(const DistillArgs& a, hipStream_t stream);
+// out_loss, state, grad and out_grad set; both directions.
+hipError_t launch_distill_step(const DistillArgs& a, hipStream_t stream);
+
+// ---- Selection (token draw and top logits) --------------------------------
+
+constexpr int kSelectThreads = 512;
+
+struct SelectArgs {
+  const void* logits;
+  int64_t ld;
+  int32_t dtype;
+  int64_t N;
+  int32_t V;
+  // Token draw. A null array means that the scalar beside it holds.
+  const float* u;
+  const float* temperatures;
+  const int32_t* top_ks;
+  const float* top_ps;
+  const float* min_ps;
+  float temperature, top_p, min_p;
+  int32_t top_k;           // token draw's scalar; the k of the top logits
+  int64_t* out_token;      // [N]
+  float* out_logprob;      // [N], or [N, k] for the top logits
+  float* out_processed;    // [N] or null
+  int32_t* out_kept;       // [N] or null
+  // Top logits.
+  int64_t* out_ids;        // [N, k]
+  float* out_logits;       // [N, k]
+  float* out_lse;          // [N] or null
+  int32_t* bad_rows;       // or null
+};
+
+hipError_t launch_sample(const SelectArgs& a, hipStream_t stream);
+hipError_t launch_top(const SelectArgs& a, hipStream_t stream);
+
+}  // namespace lp
