@@ -26,15 +26,20 @@ bool temperature_ok(float t) { return isfinite(t) && t > 0.0f; }
 constexpr int64_t kSelectMaxRows = 4194303;
 static_assert(kSelectMaxRows <= lp::kMaxDispatchItems / lp::kSelectThreads, "one dispatch");
 
-constexpr size_t kNoWorkspace = 256;
+size_t select_workspace_bytes(int64_t N, int64_t V_true, int32_t dtype) {
+  if (N < 0 || N > kSelectMaxRows || V_true < 1 || V_true > LP_SELECT_MAX_VOCAB ||
+      !dtype_ok(dtype))
+    return 0;
+  const size_t total = lp::select_workspace_layout(N, V_true, dtype).total;
+  return total < 256 ? 256 : (total + 255) / 256 * 256;
+}
 
 }  // namespace
 
 extern "C" {
 
 size_t lp_sample_workspace_bytes(int64_t N, int64_t V_true, int32_t dtype) {
-  if (N < 0 || V_true < 1 || !dtype_ok(dtype)) return 0;
-  return kNoWorkspace;
+  return select_workspace_bytes(N, V_true, dtype);
 }
 
 lp_status lp_sample(const void* logits, int64_t ld, int32_t dtype, int64_t N, int64_t V_true,
@@ -53,9 +58,9 @@ lp_status lp_sample(const void* logits, int64_t ld, int32_t dtype, int64_t N, in
       !aligned(out_token, 8) || !aligned(out_logprob, 4) || !aligned(out_processed, 4) ||
       !aligned(out_kept, 4) || !aligned(bad_rows, 4))
     return LP_EINVAL;
-  if (!aligned(workspace, 256) || workspace_bytes < lp_sample_workspace_bytes(N, V_true, dtype))
-    return LP_EINVAL;
   if (V_true > LP_SELECT_MAX_VOCAB || N > kSelectMaxRows) return LP_EUNSUPPORTED;
+  if (!aligned(workspace, 256) || workspace_bytes < select_workspace_bytes(N, V_true, dtype))
+    return LP_EINVAL;
   lp::SelectArgs a = {};
   a.logits = logits;
   a.ld = ld;
@@ -76,12 +81,11 @@ lp_status lp_sample(const void* logits, int64_t ld, int32_t dtype, int64_t N, in
   a.out_processed = out_processed;
   a.out_kept = out_kept;
   a.bad_rows = bad_rows;
-  return lp::launch_sample(a, stream) == hipSuccess ? LP_OK : LP_EHIP;
+  return lp::launch_select(a, workspace, stream) == hipSuccess ? LP_OK : LP_EHIP;
 }
 
 size_t lp_top_logprobs_workspace_bytes(int64_t N, int64_t V_true, int32_t dtype) {
-  if (N < 0 || V_true < 1 || !dtype_ok(dtype)) return 0;
-  return kNoWorkspace;
+  return select_workspace_bytes(N, V_true, dtype);
 }
 
 lp_status lp_top_logprobs(const void* logits, int64_t ld, int32_t dtype, int64_t N, int64_t V_true,
@@ -95,10 +99,9 @@ lp_status lp_top_logprobs(const void* logits, int64_t ld, int32_t dtype, int64_t
   if (!aligned(logits, size_of(dtype)) || !aligned(out_ids, 8) || !aligned(out_logits, 4) ||
       !aligned(out_logprob, 4) || !aligned(out_lse, 4) || !aligned(bad_rows, 4))
     return LP_EINVAL;
-  if (!aligned(workspace, 256) ||
-      workspace_bytes < lp_top_logprobs_workspace_bytes(N, V_true, dtype))
-    return LP_EINVAL;
   if (k > LP_TOP_MAX || V_true > LP_SELECT_MAX_VOCAB || N > kSelectMaxRows) return LP_EUNSUPPORTED;
+  if (!aligned(workspace, 256) || workspace_bytes < select_workspace_bytes(N, V_true, dtype))
+    return LP_EINVAL;
   lp::SelectArgs a = {};
   a.logits = logits;
   a.ld = ld;
@@ -112,7 +115,7 @@ lp_status lp_top_logprobs(const void* logits, int64_t ld, int32_t dtype, int64_t
   a.out_logprob = out_logprob;
   a.out_lse = out_lse;
   a.bad_rows = bad_rows;
-  return lp::launch_top(a, stream) == hipSuccess ? LP_OK : LP_EHIP;
+  return lp::launch_select(a, workspace, stream) == hipSuccess ? LP_OK : LP_EHIP;
 }
 
 size_t lp_distill_workspace_bytes(int64_t T, int64_t V_true, int32_t dtype) {

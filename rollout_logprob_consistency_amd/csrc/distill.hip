@@ -67,7 +67,7 @@ __global__ __launch_bounds__(kDistillThreads) void distill_partial_kernel(Distil
 #pragma unroll
   for (int j = 0; j < kDistillGroups; ++j)
 #pragma unroll
-    for (int i = 0; i < D::kVec; ++i) m = fmaxf(m, D::value(g[j].r[i]));
+    for (int i = 0; i < D::kVec; ++i) m = fmaxf(m, g[j].get(i));
   __shared__ float sh_m[kDistillThreads / 64];
   __shared__ double sh_s[kDistillThreads / 64];
   const float wm = (float)wave_max((double)m);
@@ -80,10 +80,12 @@ __global__ __launch_bounds__(kDistillThreads) void distill_partial_kernel(Distil
   const float base = m == -INFINITY ? 0.0f : m;
   float s = 0.0f;
 #pragma unroll
-  for (int j = 0; j < kDistillGroups; ++j)
+  for (int j = 0; j < kDistillGroups; ++j) {
+    g[j].fresh();
 #pragma unroll
     for (int i = 0; i < D::kVec; ++i)
-      s += __builtin_amdgcn_exp2f((D::value(g[j].r[i]) - base) * a.scale2);
+      s += __builtin_amdgcn_exp2f((g[j].get(i) - base) * a.scale2);
+  }
   const double ws = wave_sum((double)s);
   if ((tid & 63) == 0) sh_s[tid >> 6] = ws;
   __syncthreads();
@@ -198,7 +200,7 @@ __global__ __launch_bounds__(kDistillThreads) void distill_backward_kernel(Disti
   Group<D> g[kDistillGroups];
   if (grad == 0.0f || Q == 0.0) {
 #pragma unroll
-    for (int j = 0; j < D::kVec; ++j) g[0].r[j] = D::round(0.0f);
+    for (int j = 0; j < 4; ++j) g[0].w[j] = 0;
     for (int j = 0; j < kDistillGroups; ++j)
       store_group<D>(out, begin + (int64_t)(j * kDistillThreads + tid) * D::kVec, end, g[0]);
     return;
@@ -235,7 +237,7 @@ __global__ __launch_bounds__(kDistillThreads) void distill_backward_kernel(Disti
   for (int j = 0; j < kDistillGroups; ++j) {
 #pragma unroll
     for (int i = 0; i < D::kVec; ++i)
-      g[j].r[i] = D::round(c * __builtin_amdgcn_exp2f((D::value(g[j].r[i]) - m) * a.scale2));
+      g[j].set(i, D::round(c * __builtin_amdgcn_exp2f((g[j].get(i) - m) * a.scale2)));
     store_group<D>(out, begin + (int64_t)(j * kDistillThreads + tid) * D::kVec, end, g[j]);
   }
   __syncthreads();  // the dense values are in place before any is written again

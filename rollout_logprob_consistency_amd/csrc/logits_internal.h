@@ -51,9 +51,26 @@ constexpr int64_t dtype_bytes(int32_t dtype) { return dtype == LP_F32 ? 4 : 2; }
 // lane holds does not depend on where the row lies (gfx950 takes global loads
 // and stores of 16 bytes at any alignment of the element type). A group that
 // reaches past `end` is loaded element by element and filled with -inf.
+//
+// The group stays packed in four registers; elements are taken out where they
+// are used. fresh() makes the compiler forget what it has taken out, so that
+// two passes over a group do not hold its elements unpacked in between.
 template <class D>
 struct Group {
-  typename D::Raw r[D::kVec];
+  uint32_t w[4];
+
+  __device__ __forceinline__ float get(int i) const {
+    if constexpr (D::kVec == 4) return D::value(w[i]);
+    else return D::value((typename D::Raw)(w[i >> 1] >> ((i & 1) * 16)));
+  }
+  __device__ __forceinline__ void set(int i, typename D::Raw r) {
+    if constexpr (D::kVec == 4) w[i] = r;
+    else if (i & 1) w[i >> 1] = (w[i >> 1] & 0xFFFFu) | ((uint32_t)r << 16);
+    else w[i >> 1] = (w[i >> 1] & 0xFFFF0000u) | r;
+  }
+  __device__ __forceinline__ void fresh() {
+    asm volatile("" : "+v"(w[0]), "+v"(w[1]), "+v"(w[2]), "+v"(w[3]));
+  }
 };
 
 template <class D>
@@ -63,7 +80,9 @@ __device__ __forceinline__ Group<D> load_group(const typename D::Raw* p, int64_t
     __builtin_memcpy(&g, p + i, 16);
   } else {
 #pragma unroll
-    for (int j = 0; j < D::kVec; ++j) g.r[j] = i + j < end ? p[i + j] : D::kNegInf;
+    for (int j = 0; j < 4; ++j) g.w[j] = 0;
+#pragma unroll
+    for (int j = 0; j < D::kVec; ++j) g.set(j, i + j < end ? p[i + j] : D::kNegInf);
   }
   return g;
 }
@@ -76,7 +95,10 @@ __device__ __forceinline__ void store_group(typename D::Raw* p, int64_t i, int64
   } else {
 #pragma unroll
     for (int j = 0; j < D::kVec; ++j)
-      if (i + j < end) p[i + j] = g.r[j];
+      if (i + j < end) {
+        if constexpr (D::kVec == 4) p[i + j] = g.w[j];
+        else p[i + j] = (typename D::Raw)(g.w[j >> 1] >> ((j & 1) * 16));
+      }
   }
 }
 
@@ -131,6 +153,11 @@ hipError_t launch_distill_step(const DistillArgs& a, hipStream_t stream);
 
 constexpr int kSelectThreads = 512;
 
+// A wave's maximum m and sum of exp((z - m) / tau) over its part of a chunk.
+struct SelectPart {
+  float m, s;
+};
+
 struct SelectArgs {
   const void* logits;
   int64_t ld;
@@ -154,9 +181,19 @@ struct SelectArgs {
   float* out_logits;       // [N, k]
   float* out_lse;          // [N] or null
   int32_t* bad_rows;       // or null
+  // Set by launch_select.
+  int32_t slices;          // per row
+  uint32_t* counts;        // [N][slices] listed tokens
+  SelectPart* parts;       // [N][chunks][waves], where slices > 1
+  uint64_t* keys;          // [N][slices][LP_TOP_MAX], where slices > 1
 };
 
-hipError_t launch_sample(const SelectArgs& a, hipStream_t stream);
-hipError_t launch_top(const SelectArgs& a, hipStream_t stream);
+struct SelectWorkspace {
+  size_t off_counts, off_parts, off_keys, total;
+};
+SelectWorkspace select_workspace_layout(int64_t N, int64_t V, int32_t dtype);
+
+// The token draw, or the top logits where u is null.
+hipError_t launch_select(SelectArgs a, void* workspace, hipStream_t stream);
 
 }  // namespace lp
