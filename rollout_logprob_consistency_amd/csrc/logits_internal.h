@@ -186,10 +186,13 @@ struct SelectArgs {
   uint32_t* counts;        // [N][slices] listed tokens
   SelectPart* parts;       // [N][chunks][waves], where slices > 1
   uint64_t* keys;          // [N][slices][LP_TOP_MAX], where slices > 1
+  unsigned long long* masses;  // [N][buckets], where slices > 1; then, behind them,
+  uint32_t* bucket_counts;     // [N][buckets + 4]: counts and the row's facts
+  size_t bucket_bytes;         // of both
 };
 
 struct SelectWorkspace {
-  size_t off_counts, off_parts, off_keys, total;
+  size_t off_counts, off_parts, off_keys, off_masses, off_bucket_counts, total;
 };
 SelectWorkspace select_workspace_layout(int64_t N, int64_t V, int32_t dtype);
 

@@ -10,14 +10,16 @@
 // decided in it, with weights and sums in fp64. Where there are few rows, a
 // row is cut into slices, each leaves its list, and row_kernel joins them.
 //
-// By buckets (everything else, and rows whose list overflows): row_kernel
-// collects the weights w = exp(s - max s), s = z / tau, in 2 048 buckets of
-// 1/32 nat below the maximum: a count and a mass each. Inside bucket b a weight
-// is e^{-b/32} P with |ln P| <= 1/64; P is taken in fp64 and summed as an
-// integer in units of 2^-43, so a bucket's mass does not depend on the order
-// of its terms (LDS integer atomics). Prefix sums over the buckets find the
-// bucket in which a rank or a mass is reached; only that bucket's tokens are
-// then listed, sorted and summed.
+// By buckets (everything else, and rows whose list overflows): the weights are
+// collected in 2 048 buckets of 1/32 nat, a count and a mass each, placed so
+// that the maximum of the row's first chunk lies 24 nats below the top; a row
+// that rises further is collected again from its own maximum. Inside bucket b
+// a weight is the bucket's centre times P, |ln P| <= 1/64; P is taken in fp64
+// and summed as an integer in units of 2^-43, so a bucket's mass does not
+// depend on the order of its terms (integer atomics, in LDS and between
+// slices). Prefix sums over the buckets find the bucket in which a rank or a
+// mass is reached; only that bucket's tokens are then listed, sorted and
+// summed.
 #include <algorithm>
 
 #include "logits_internal.h"
@@ -27,12 +29,23 @@ namespace {
 
 constexpr int kThreads = kSelectThreads;
 constexpr int kWaves = kThreads / 64;
+constexpr int kGroups = 4;            // 16-byte groups per thread and chunk
 constexpr int kBuckets = 2048;        // of 1/32 nat; the last one: weight 0
 constexpr double kPerNat = 32.0;
+constexpr double kHead = 768.0;       // the anchor's place: 24 nats from the top
 constexpr int kPerThread = kBuckets / kThreads;
 constexpr int kList = 4096;           // tokens listed at once
-constexpr double kUnit = 8796093022208.0;  // 2^43: the mass unit's inverse
+constexpr int kListMax = LP_TOP_MAX;  // tokens that a slice leaves
+constexpr int kMaxSlices = 512;       // of a row
+constexpr uint32_t kOverflow = 0xFFFFFFFFu;    // a slice's count: take the buckets
+constexpr double kUnit = 8796093022208.0;      // 2^43: the mass unit's inverse
 constexpr double kMagic = 6755399441055744.0;  // 1.5 * 2^52: adding it rounds to an integer
+
+template <class D>
+constexpr int chunk_of() { return kThreads * kGroups * D::kVec; }
+constexpr int kMaxParts = LP_SELECT_MAX_VOCAB / chunk_of<F32>() * kWaves;
+
+using Part = SelectPart;
 
 // Tokens as distinct integers that ascend with (logit, then lower index):
 // the order of the selection is their descending order.
@@ -52,12 +65,17 @@ __device__ __forceinline__ float token_logit(uint64_t k) { return key_value((uin
 
 constexpr uint32_t kKeyNegInf = 0x007FFFFFu;  // key_of(-inf)
 
-constexpr int kGroups = 4;                     // 16-byte groups per thread and chunk
-constexpr int kMaxParts = LP_SELECT_MAX_VOCAB / (kThreads * kGroups * 4) * kWaves;
+
+// What the buckets of a row hold besides counts and masses.
+struct RowFacts {
+  uint32_t top;     // key of the largest logit
+  uint32_t odd;     // a NaN or +inf is there
+  uint32_t masked;  // -inf logits (in the last bucket's count), fill included
+};
 
 struct Shared {
   // Buckets: counts and masses while they are collected, then exclusive
-  // prefix sums (masses as doubles in units of the maximum's weight).
+  // prefix sums (masses as doubles in units of the anchor's weight).
   union {
     unsigned long long mass[kBuckets];
     double above[kBuckets + 1];
@@ -70,66 +88,90 @@ struct Shared {
       unsigned long long fmass[kBuckets];
       uint32_t fcnt[kBuckets];
     };
-    SelectPart parts[kMaxParts];
+    Part parts[kMaxParts];
   };
   unsigned long long wave_u64[kWaves];
   double wave_f64[kWaves], shared_f64;
   uint32_t wave_u32[kWaves];
   float wave_f32[kWaves];
-  uint32_t flags, n_list, found;
+  uint32_t n_list, found;
   uint32_t found_cnt;
   unsigned long long found_mass;
-  uint32_t bound[2];
+  float least[4];
+  RowFacts facts;
 };
 
-// A row and its scale. x(z) = 32 (max - z) / tau; the bucket is rint(x).
+// A row and its scale. x(z) = 32 (anchor - z) / tau + 768; the bucket is
+// rint(x), the last one from there on.
 template <class D>
 struct Row {
   const typename D::Raw* p;
   int V;
-  double zmax, inv;  // inv = 32 / tau
+  double anchor, inv;  // inv = 32 / tau
+  float zmax;
 
   __device__ __forceinline__ double x_of(float z) const {
-    return fmin((zmax - (double)z) * inv, (double)(kBuckets - 1));
+    return fmin(fma(anchor - (double)z, inv, kHead), (double)(kBuckets - 1));
   }
-  static __device__ __forceinline__ int bucket(double x) {
-    return (int)(uint32_t)__double_as_longlong(x + kMagic);
+  static __device__ __forceinline__ uint32_t bucket(double x) {
+    return min((uint32_t)__double_as_longlong(x + kMagic), (uint32_t)(kBuckets - 1));
   }
-  // exp((b - x) / 32) in units of 2^-43, by its Taylor series to degree 6
-  // (|d| <= 1/64: truncation 5e-17); the last bucket weighs 0.
+  // exp((b - x) / 32) in units of 2^-43, b = rint(x), by its Taylor series to
+  // degree 5 (|b - x| / 32 <= 1/64: truncation 2e-14 relative); the last term
+  // rounds to an integer.
   static __device__ __forceinline__ unsigned long long mass(double x) {
-    const double b = (x + kMagic) - kMagic;
-    const double d = (b - x) * (1.0 / kPerNat);
-    double p = 1.0 / 720.0;
-    p = fma(p, d, 1.0 / 120.0);
-    p = fma(p, d, 1.0 / 24.0);
-    p = fma(p, d, 1.0 / 6.0);
-    p = fma(p, d, 0.5);
-    p = fma(p, d, 1.0);
-    p = fma(p, d, 1.0);
-    const unsigned long long m =
-        (unsigned long long)__double_as_longlong(fma(p, kUnit, kMagic)) -
-        (unsigned long long)__double_as_longlong(kMagic);
-    return b < (double)(kBuckets - 1) ? m : 0ull;
+    const double y = ((x + kMagic) - kMagic) - x;
+    double p = kUnit / (120.0 * 33554432.0);       // 32^5 5!
+    p = fma(p, y, kUnit / (24.0 * 1048576.0));
+    p = fma(p, y, kUnit / (6.0 * 32768.0));
+    p = fma(p, y, kUnit / (2.0 * 1024.0));
+    p = fma(p, y, kUnit / 32.0);
+    const double m = fma(p, y, kUnit + kMagic);
+    return (unsigned long long)__double_as_longlong(m) -
+           (unsigned long long)__double_as_longlong(kMagic);
+  }
+  // A weight of mass m in bucket b, in units of the anchor's weight.
+  static __device__ __forceinline__ double unit(int b) {
+    return exp_f64((kHead - (double)b) / kPerNat) / kUnit;
+  }
+  __device__ __forceinline__ double max_weight() const {
+    return exp_f64(((double)zmax - anchor) * (inv / kPerNat));
   }
 
-  // f(logit, index) for every token, each thread its 16-byte groups.
+  __device__ __forceinline__ int chunks() const { return (V + chunk_of<D>() - 1) / chunk_of<D>(); }
+  __device__ __forceinline__ void load(Group<D> (&g)[kGroups], int c) const {
+#pragma unroll
+    for (int j = 0; j < kGroups; ++j)
+      g[j] = load_group<D>(
+          p, (int64_t)c * chunk_of<D>() + (j * kThreads + (int)threadIdx.x) * D::kVec, V);
+  }
+  static __device__ __forceinline__ int index(int c, int j, int i) {
+    return c * chunk_of<D>() + (j * kThreads + (int)threadIdx.x) * D::kVec + i;
+  }
+  // f(groups, chunk) for the chunks [c0, c1), the next one's loads in flight.
+  template <class F>
+  __device__ __forceinline__ void for_chunks(int c0, int c1, F f) const {
+    Group<D> g[kGroups], next[kGroups];
+    load(g, c0);
+    for (int c = c0; c < c1; ++c) {
+      if (c + 1 < c1) load(next, c + 1);
+      f(g, c);
+#pragma unroll
+      for (int j = 0; j < kGroups; ++j) g[j] = next[j];
+    }
+  }
+  // f(logit, index) for every token; places behind the row are -inf.
   template <class F>
   __device__ __forceinline__ void for_each(F f) const {
-    constexpr int kU = 4;
-    const int step = kThreads * D::kVec;
-    for (int i0 = (int)threadIdx.x * D::kVec; i0 < V; i0 += kU * step) {
-      Group<D> g[kU];
+    for_chunks(0, chunks(), [&](Group<D>(&g)[kGroups], int c) {
 #pragma unroll
-      for (int j = 0; j < kU; ++j) g[j] = load_group<D>(p, (int64_t)i0 + j * step, V);
-#pragma unroll
-      for (int j = 0; j < kU; ++j)
+      for (int j = 0; j < kGroups; ++j)
 #pragma unroll
         for (int i = 0; i < D::kVec; ++i) {
-          const int idx = i0 + j * step + i;
-          if (idx < V) f(g[j].get(i), idx);
+          f(g[j].get(i), index(c, j, i));
+          if (i % 4 == 3) __builtin_amdgcn_sched_barrier(0);  // bounds the registers in use
         }
-    }
+    });
   }
 };
 
@@ -171,14 +213,72 @@ __device__ __forceinline__ float block_max(float v, float* words) {
   return v;
 }
 
-// The list sorted descending (bitonic, padded with zeros to a power of two).
+
+// ---- Sorting the list -------------------------------------------------------
+
+template <int kJ>
+__device__ __forceinline__ uint64_t lane_xor(uint64_t v) {
+  if constexpr (kJ == 32) {
+    return __shfl_xor((unsigned long long)v, 32);
+  } else {
+    auto half = [](int x) {
+      if constexpr (kJ <= 2) return xlane<kJ>(x);  // quad permutations are true exchanges
+      else return __builtin_amdgcn_ds_swizzle(x, (kJ << 10) | 0x1F);
+    };
+    const uint32_t lo = (uint32_t)half((int)(uint32_t)v), hi = (uint32_t)half((int)(v >> 32));
+    return ((uint64_t)hi << 32) | lo;
+  }
+}
+
+// Compare and exchange at distance kJ < 64 inside a wave.
+template <int kJ>
+__device__ __forceinline__ void exchange(uint64_t& e, bool descending, int lane) {
+  const uint64_t o = lane_xor<kJ>(e);
+  const bool larger = ((lane & kJ) == 0) == descending;
+  e = larger == (e < o) ? o : e;
+}
+
+// The steps of distance kJ, kJ / 2, ..., 1 on both halves of 128 keys.
+template <int kJ>
+__device__ __forceinline__ void exchanges(uint64_t& e0, uint64_t& e1, bool d0, bool d1, int lane) {
+  exchange<kJ>(e0, d0, lane);
+  exchange<kJ>(e1, d1, lane);
+  if constexpr (kJ > 1) exchanges<kJ / 2>(e0, e1, d0, d1, lane);
+}
+__device__ __forceinline__ void exchange_halves(uint64_t& e0, uint64_t& e1, bool descending) {
+  const uint64_t hi = e0 > e1 ? e0 : e1, lo = e0 > e1 ? e1 : e0;
+  e0 = descending ? hi : lo;
+  e1 = descending ? lo : hi;
+}
+template <int kK>
+__device__ __forceinline__ void sort_wave(uint64_t& e0, uint64_t& e1, int lane) {
+  if constexpr (kK > 2) sort_wave<kK / 2>(e0, e1, lane);
+  const bool d = (lane & kK) == 0;  // (kK = 64: the first half descends, the second ascends)
+  exchanges<kK / 2>(e0, e1, kK == 64 ? true : d, kK == 64 ? false : d, lane);
+}
+
+// The list sorted descending: a bitonic network over a power of two of keys,
+// at least 128, padded with zeros. A wave holds 128 keys in registers for all
+// steps of distances up to 64; only longer ones go through LDS with a barrier
+// (the plain network's 45 barriers for 512 keys become 6).
 __device__ __forceinline__ void sort_list(uint64_t* list, uint32_t m) {
-  uint32_t n = 1;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  uint32_t n = 128;
   while (n < m) n <<= 1;
   for (uint32_t i = m + threadIdx.x; i < n; i += kThreads) list[i] = 0;
   __syncthreads();
-  for (uint32_t k = 2; k <= n; k <<= 1)
-    for (uint32_t j = k >> 1; j > 0; j >>= 1) {
+  for (uint32_t b = wave * 128; b < n; b += kWaves * 128) {
+    uint64_t e0 = list[b + lane], e1 = list[b + 64 + lane];
+    sort_wave<64>(e0, e1, lane);
+    const bool d = (b & 128) == 0;
+    exchange_halves(e0, e1, d);
+    exchanges<32>(e0, e1, d, d, lane);
+    list[b + lane] = e0;
+    list[b + 64 + lane] = e1;
+  }
+  __syncthreads();
+  for (uint32_t k = 256; k <= n; k <<= 1) {
+    for (uint32_t j = k >> 1; j >= 128; j >>= 1) {
       for (uint32_t t = threadIdx.x; t < n / 2; t += kThreads) {
         const uint32_t lo = 2 * t - (t & (j - 1)), hi = lo + j;
         const uint64_t a = list[lo], b = list[hi];
@@ -189,281 +289,17 @@ __device__ __forceinline__ void sort_list(uint64_t* list, uint32_t m) {
       }
       __syncthreads();
     }
-}
-
-// Tokens with keys in [lo, hi] appended to the list, in any order.
-template <class D>
-__device__ __forceinline__ uint32_t gather(const Row<D>& row, Shared& sh, uint64_t lo, uint64_t hi) {
-  __syncthreads();
-  if (threadIdx.x == 0) sh.n_list = 0;
-  __syncthreads();
-  row.for_each([&](float z, int idx) {
-    const uint64_t k = token_key(z, idx);
-    if (k >= lo && k <= hi) {
-      const uint32_t s = atomicAdd(&sh.n_list, 1u);
-      if (s < (uint32_t)kList) sh.list[s] = k;
-    }
-  });
-  __syncthreads();
-  return min(sh.n_list, (uint32_t)kList);
-}
-
-// Least key whose bucket is at most b (buckets fall as keys rise): a binary
-// search by one thread over the finite keys. All threads call it.
-template <class D>
-__device__ __forceinline__ uint32_t least_key(const Row<D>& row, Shared& sh, int b) {
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    uint32_t lo = kKeyNegInf + 1, hi = key_of((float)row.zmax);  // bucket(hi) = 0 <= b
-    while (lo < hi) {
-      const uint32_t mid = lo + (hi - lo) / 2;
-      if (Row<D>::bucket(row.x_of(key_value(mid))) <= b) hi = mid;
-      else lo = mid + 1;
-    }
-    sh.bound[0] = lo;
-  }
-  __syncthreads();
-  return sh.bound[0];
-}
-
-// Where a selection ends inside a bucket: the token, its rank there (from 0)
-// and the mass through it, in the bucket's units.
-struct Found {
-  uint64_t key;
-  uint32_t rank;
-  unsigned long long mass;
-};
-
-enum Mode { kByRank, kByMass, kByMassOver };
-
-// The first token, in order, of bucket b at which
-//   kByRank:     `rank` tokens of the bucket are reached (rank >= 1),
-//   kByMass:     the mass through it is >= want,
-//   kByMassOver: the mass through it is > want.
-// count is the bucket's. Where no token's mass gets there (want is rounded),
-// the last one.
-template <class D>
-__device__ Found select_in_bucket(const Row<D>& row, Shared& sh, int b, uint32_t count, Mode mode,
-                                  uint32_t rank, double want) {
-  uint64_t lo = (uint64_t)least_key(row, sh, b) << 32;
-  uint64_t hi = b == 0 ? (((uint64_t)key_of((float)row.zmax) << 32) | 0xFFFFFFFFull)
-                       : ((uint64_t)least_key(row, sh, b - 1) << 32) - 1;
-  uint32_t base_cnt = 0;
-  unsigned long long base_mass = 0;
-  auto reached = [&](uint32_t c, unsigned long long m) {
-    return mode == kByRank ? c >= rank : (mode == kByMass ? (double)m >= want : (double)m > want);
-  };
-  while (count > (uint32_t)kList) {
-    // Too many to list: 2 048 finer buckets of equal key ranges. The range
-    // shrinks 2 048-fold a turn, and keys are distinct, so this ends.
-    const uint64_t range = hi - lo;
-    const int bits = 64 - __clzll((long long)(range | 1));
-    const int shift = bits > 11 ? bits - 11 : 0;
-    __syncthreads();
-    for (int i = threadIdx.x; i < kBuckets; i += kThreads) {
-      sh.fmass[i] = 0;
-      sh.fcnt[i] = 0;
+    for (uint32_t b = wave * 128; b < n; b += kWaves * 128) {
+      uint64_t e0 = list[b + lane], e1 = list[b + 64 + lane];
+      const bool d = (b & k) == 0;
+      exchange_halves(e0, e1, d);
+      exchanges<32>(e0, e1, d, d, lane);
+      list[b + lane] = e0;
+      list[b + 64 + lane] = e1;
     }
     __syncthreads();
-    row.for_each([&](float z, int idx) {
-      const uint64_t k = token_key(z, idx);
-      if (k >= lo && k <= hi) {
-        const uint32_t f = (uint32_t)((hi - k) >> shift);
-        atomicAdd(&sh.fcnt[f], 1u);
-        atomicAdd(&sh.fmass[f], Row<D>::mass(row.x_of(z)));
-      }
-    });
-    __syncthreads();
-    uint32_t c = 0;
-    unsigned long long m = 0;
-    for (int i = 0; i < kPerThread; ++i) {
-      c += sh.fcnt[threadIdx.x * kPerThread + i];
-      m += sh.fmass[threadIdx.x * kPerThread + i];
-    }
-    uint32_t all_c;
-    unsigned long long all_m;
-    uint32_t cb = base_cnt + block_scan(c, sh.wave_u32, &all_c);
-    unsigned long long mb = base_mass + block_scan(m, sh.wave_u64, &all_m);
-    if (threadIdx.x == 0) sh.found = 0xFFFFFFFFu;
-    __syncthreads();
-    // First finer bucket through which the selection is reached; the last
-    // occupied one where rounding of `want` leaves none.
-    for (int i = 0; i < kPerThread; ++i) {
-      const int f = threadIdx.x * kPerThread + i;
-      const uint32_t c1 = cb + sh.fcnt[f];
-      const unsigned long long m1 = mb + sh.fmass[f];
-      const bool last = c1 == base_cnt + all_c;
-      if (sh.fcnt[f] != 0 && (reached(c1, m1) || last) && !(cb != base_cnt && reached(cb, mb))) {
-        sh.found = (uint32_t)f;
-        sh.found_cnt = cb;
-        sh.found_mass = mb;
-      }
-      cb = c1;
-      mb = m1;
-    }
-    __syncthreads();
-    const uint32_t f = sh.found;
-    base_cnt = sh.found_cnt;
-    base_mass = sh.found_mass;
-    count = sh.fcnt[f];
-    const uint64_t top = hi - ((uint64_t)f << shift);
-    const uint64_t width = (uint64_t)1 << shift;
-    lo = top - lo >= width ? top - width + 1 : lo;
-    hi = top;
-    __syncthreads();
   }
-
-  const uint32_t m = gather(row, sh, lo, hi);
-  sort_list(sh.list, m);
-  // Masses through every listed token, in order.
-  constexpr int kEach = kList / kThreads;
-  unsigned long long w[kEach], sum = 0;
-#pragma unroll
-  for (int i = 0; i < kEach; ++i) {
-    const uint32_t t = threadIdx.x * kEach + i;
-    w[i] = t < m ? Row<D>::mass(row.x_of(token_logit(sh.list[t]))) : 0ull;
-    sum += w[i];
-  }
-  unsigned long long all;
-  unsigned long long mb = base_mass + block_scan(sum, sh.wave_u64, &all);
-#pragma unroll
-  for (int i = 0; i < kEach; ++i) {
-    const uint32_t t = threadIdx.x * kEach + i;
-    const unsigned long long m1 = mb + w[i];
-    if (t < m) {
-      const uint32_t c1 = base_cnt + t + 1;
-      if ((reached(c1, m1) || t == m - 1) && !(t > 0 && reached(c1 - 1, mb))) {
-        sh.found = t;
-        sh.found_mass = m1;
-      }
-    }
-    mb = m1;
-  }
-  __syncthreads();
-  Found r;
-  r.key = sh.list[sh.found];
-  r.rank = base_cnt + sh.found;
-  r.mass = sh.found_mass;
-  __syncthreads();
-  return r;
 }
-
-// Row statistics: the maximum, then the buckets with their prefix sums.
-struct Totals {
-  bool bad;
-  uint32_t finite;
-  double mass;  // of all tokens, in units of the maximum's weight
-};
-
-template <class D>
-__device__ float row_max(const Row<D>& row, Shared& sh, bool* bad) {
-  float m = -INFINITY;
-  bool odd = false;
-  row.for_each([&](float z, int) {
-    m = fmaxf(m, z);
-    odd |= !(z < INFINITY);  // NaN or +inf
-  });
-  if (threadIdx.x == 0) sh.flags = 0;
-  m = block_max(m, sh.wave_f32);
-  if (odd) sh.flags = 1;
-  __syncthreads();
-  *bad = sh.flags != 0 || m == -INFINITY;
-  return m;
-}
-
-template <class D>
-__device__ Totals fill_buckets(const Row<D>& row, Shared& sh) {
-  for (int i = threadIdx.x; i < kBuckets; i += kThreads) {
-    sh.mass[i] = 0;
-    sh.cnt[i] = 0;
-  }
-  __syncthreads();
-  row.for_each([&](float z, int) {
-    if (z != -INFINITY) {
-      const double x = row.x_of(z);
-      const int b = Row<D>::bucket(x);
-      atomicAdd(&sh.cnt[b], 1u);
-      atomicAdd(&sh.mass[b], Row<D>::mass(x));
-    }
-  });
-  __syncthreads();
-  uint32_t c[kPerThread], cs = 0;
-  double m[kPerThread], ms = 0.0;
-#pragma unroll
-  for (int i = 0; i < kPerThread; ++i) {
-    const int b = threadIdx.x * kPerThread + i;
-    c[i] = sh.cnt[b];
-    m[i] = (double)sh.mass[b] * (exp_f64(-(double)b / kPerNat) / kUnit);
-    cs += c[i];
-    ms += m[i];
-  }
-  Totals t;
-  t.bad = false;
-  uint32_t cb = block_scan(cs, sh.wave_u32, &t.finite);
-  double mb = block_scan(ms, sh.wave_f64, &t.mass);  // (its barriers end the reads above)
-#pragma unroll
-  for (int i = 0; i < kPerThread; ++i) {
-    const int b = threadIdx.x * kPerThread + i;
-    sh.cnt[b] = cb;
-    sh.above[b] = mb;
-    cb += c[i];
-    mb += m[i];
-  }
-  if (threadIdx.x == kThreads - 1) {
-    sh.cnt[kBuckets] = t.finite;
-    sh.above[kBuckets] = mb;
-  }
-  __syncthreads();
-  t.mass = sh.above[kBuckets];
-  return t;
-}
-
-__device__ __forceinline__ double bucket_weight(int b) { return exp_f64(-(double)b / kPerNat); }
-
-// The bucket that holds the token of rank `k` (from 1).
-__device__ __forceinline__ int bucket_of_rank(Shared& sh, uint32_t k) {
-#pragma unroll
-  for (int i = 0; i < kPerThread; ++i) {
-    const int b = threadIdx.x * kPerThread + i;
-    if (sh.cnt[b] < k && k <= sh.cnt[b + 1]) sh.found = b;
-  }
-  __syncthreads();
-  const int b = (int)sh.found;
-  __syncthreads();
-  return b;
-}
-
-// The first occupied bucket through which the mass is >= want (> want with
-// `over`). Prefix sums of neighbouring threads may differ in the last bit, so
-// only a bucket's end is looked at; bucket 0 holds the maximum.
-__device__ __forceinline__ int bucket_of_mass(Shared& sh, double want, bool over) {
-  if (threadIdx.x == 0) sh.found = kBuckets;
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < kPerThread; ++i) {
-    const int b = threadIdx.x * kPerThread + i;
-    const double end = sh.above[b + 1];
-    if (sh.cnt[b + 1] != sh.cnt[b] && (over ? end > want : end >= want)) {
-      atomicMin(&sh.found, (uint32_t)b);
-      break;
-    }
-  }
-  __syncthreads();
-  const int b = sh.found < (uint32_t)kBuckets ? (int)sh.found : 0;
-  __syncthreads();
-  return b;
-}
-
-// ---- The short list ---------------------------------------------------------
-
-constexpr int kListMax = LP_TOP_MAX;           // tokens that a slice leaves
-constexpr uint32_t kOverflow = 0xFFFFFFFFu;    // a slice's count: take the buckets
-constexpr uint32_t kCrowded = 2048;            // a list is cut down from here on
-
-template <class D>
-constexpr int chunk_of() { return kThreads * kGroups * D::kVec; }
-
-using Part = SelectPart;
 
 __device__ __forceinline__ float wave_max_f32(float m) {
   m = fmaxf(m, __int_as_float(xlane<1>(__float_as_int(m))));
@@ -688,53 +524,131 @@ __device__ void finish_top(const SelectArgs& a, int64_t n, const uint64_t* list,
 }
 
 struct CollectShared {
-  uint64_t list[kList];
+  union {
+    uint64_t list[kList];
+    struct {  // a slice's buckets
+      unsigned long long mass[kBuckets];
+      uint32_t cnt[kBuckets];
+    };
+  };
   Part parts[kMaxParts];
   double wave_f64[kWaves], shared_f64;
   float wave_f32[kWaves];
   uint32_t n_list, found;
+  RowFacts facts;
 };
+
+// ---- Filling the buckets ----------------------------------------------------
+
+// The maximum of the first chunk that has a finite logit (or +inf): the
+// anchor of the buckets. -inf where there is none.
+template <class D>
+__device__ float anchor_of(const Row<D>& row, float* words) {
+  float m = -INFINITY;
+  for (int c = 0; c < row.chunks() && m == -INFINITY; ++c) {
+    Group<D> g[kGroups];
+    row.load(g, c);
+    float t = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < kGroups; ++j)
+#pragma unroll
+      for (int i = 0; i < D::kVec; ++i) t = fmaxf(t, g[j].get(i));
+    m = block_max(t, words);
+  }
+  return m;
+}
+
+// Counts and masses of the chunks [c0, c1) into LDS (cleared here), and their
+// facts. Logits above the first bucket land in the last one: the caller sees
+// by the maximum that there are some. No element is skipped: -inf goes to the
+// last bucket and is counted apart.
+template <class D, class S>
+__device__ void collect_buckets(const Row<D>& row, S& sh, int c0, int c1) {
+  for (int i = threadIdx.x; i < kBuckets; i += kThreads) {
+    sh.mass[i] = 0;
+    sh.cnt[i] = 0;
+  }
+  if (threadIdx.x == 0) sh.facts = {0u, 0u, 0u};
+  __syncthreads();
+  float top = -INFINITY;
+  bool odd = false;
+  uint32_t masked = 0;
+  row.for_chunks(c0, c1, [&](Group<D>(&g)[kGroups], int) {
+#pragma unroll
+    for (int j = 0; j < kGroups; ++j)
+#pragma unroll
+      for (int i = 0; i < D::kVec; ++i) {
+        const float z = g[j].get(i);
+        const double x = row.x_of(z);
+        const uint32_t b = Row<D>::bucket(x);
+        atomicAdd(&sh.cnt[b], 1u);
+        atomicAdd(&sh.mass[b], Row<D>::mass(x));
+        top = fmaxf(top, z);
+        odd |= __builtin_amdgcn_classf(z, 0x203);  // NaN, +inf
+        masked += (uint32_t)__popcll(__ballot(z == -INFINITY));
+        if (i % 4 == 3) __builtin_amdgcn_sched_barrier(0);  // bounds the registers in use
+      }
+  });
+  top = wave_max_f32(top);
+  const bool any = __ballot(odd) != 0;
+  if ((threadIdx.x & 63) == 0) {
+    atomicMax(&sh.facts.top, key_of(top));
+    if (any) atomicOr(&sh.facts.odd, 1u);
+    atomicAdd(&sh.facts.masked, masked);
+  }
+  __syncthreads();
+}
 
 // One slice of a row (the whole row where a.slices is 1).
 template <class D, bool kTop>
 __global__ __launch_bounds__(kThreads, 6) void collect_kernel(SelectArgs a) {
   __shared__ CollectShared sh;
-  constexpr int kChunk = chunk_of<D>();
   const int64_t n = blockIdx.x / (uint32_t)a.slices;
   const int slice = (int)(blockIdx.x - (uint32_t)n * (uint32_t)a.slices);
   const Settings st = settings_of(a, n);
   uint32_t* count = a.counts + n * a.slices;
-  if (st.kind == kBuckets_) {
-    if (slice == 0 && threadIdx.x == 0) count[0] = kOverflow;
-    return;
-  }
+  Row<D> row;
+  row.p = static_cast<const typename D::Raw*>(a.logits) + n * a.ld;
+  row.V = a.V;
+  const int chunks = row.chunks(), tid = threadIdx.x, wave = tid >> 6;
+  if constexpr (!kTop)
+    if (st.kind == kBuckets_) {
+      if (a.slices == 1 || st.bad) return;  // row_kernel collects by itself
+      const int c0 = chunks * slice / a.slices, c1 = chunks * (slice + 1) / a.slices;
+      row.anchor = (double)anchor_of(row, sh.wave_f32);
+      row.inv = kPerNat / (double)st.tau;
+      collect_buckets(row, sh, c0, c1);
+      unsigned long long* mass = a.masses + n * kBuckets;
+      uint32_t* cnt = a.bucket_counts + n * (kBuckets + 4);
+      for (int i = tid; i < kBuckets; i += kThreads)
+        if (sh.cnt[i]) {
+          atomicAdd(&cnt[i], sh.cnt[i]);
+          atomicAdd(&mass[i], sh.mass[i]);
+        }
+      if (tid == 0) {
+        atomicMax(&cnt[kBuckets], sh.facts.top);
+        atomicOr(&cnt[kBuckets + 1], sh.facts.odd);
+        atomicAdd(&cnt[kBuckets + 2], sh.facts.masked);
+      }
+      return;
+    }
   const int slices = slices_of(a, st);
   if (slice >= slices) return;
-  const int chunks = (a.V + kChunk - 1) / kChunk;
-  const int c0 = (int)((int64_t)chunks * slice / slices);
-  const int c1 = (int)((int64_t)chunks * (slice + 1) / slices);
-  const typename D::Raw* row = static_cast<const typename D::Raw*>(a.logits) + n * a.ld;
+  const int c0 = chunks * slice / slices, c1 = chunks * (slice + 1) / slices;
   const float scale2 = scale2_of(st.tau);
   const float depth = st.kind == kMinP ? depth_of(st) : 0.0f;
-  const int tid = threadIdx.x, wave = tid >> 6;
 
-  Group<D> g[kGroups], next[kGroups];
-  auto load = [&](Group<D>(&to)[kGroups], int c) {
-#pragma unroll
-    for (int j = 0; j < kGroups; ++j)
-      to[j] = load_group<D>(row, (int64_t)c * kChunk + (j * kThreads + tid) * D::kVec, a.V);
-  };
-  // Tokens from theta on enter the list. theta is a logit that `k` tokens
-  // reach (kTopK), or the depth below one (kMinP); never below the finite ones.
+  // Tokens from theta on enter the list. theta is a logit that k tokens reach
+  // (kTopK), or the depth below one (kMinP); never below the finite ones.
   float theta = 0.0f;
-  // Sorted down to what can still be needed; returns false where the list
-  // has lost tokens.
+  // The list sorted down to what can still be needed; false where it has lost
+  // tokens.
   auto cut = [&](bool always) {
     __syncthreads();
     const uint32_t m = sh.n_list;
     __syncthreads();
     if (m > (uint32_t)kList) return false;
-    if (!always && m < kCrowded) return true;
+    if (!always && m < (st.kind == kTopK ? 2 * st.k + 64 : 1024u)) return true;
     sort_list(sh.list, m);
     uint32_t keep = m;
     if (st.kind == kTopK) {
@@ -751,11 +665,21 @@ __global__ __launch_bounds__(kThreads, 6) void collect_kernel(SelectArgs a) {
     __syncthreads();
     return true;
   };
+  // The r-th largest of a wave's values, by taking the largest away r - 1 times.
+  auto rth_largest = [&](float v, uint32_t r) {
+    float m = wave_max_f32(v);
+    for (uint32_t i = 1; i < r; ++i) {
+      const uint64_t at = __ballot(v == m);
+      if (at == 0) break;  // nothing but masked tokens is left
+      if ((tid & 63) == __ffsll((long long)at) - 1) v = -INFINITY;
+      m = wave_max_f32(v);
+    }
+    return m;
+  };
 
-  load(g, c0);
   bool fits = true;
-  for (int c = c0; c < c1; ++c) {
-    if (c + 1 < c1) load(next, c + 1);
+  row.for_chunks(c0, c1, [&](Group<D>(&g)[kGroups], int c) {
+    if (!fits) return;
     float tm = -INFINITY, gm[kGroups];
 #pragma unroll
     for (int j = 0; j < kGroups; ++j) {
@@ -766,45 +690,53 @@ __global__ __launch_bounds__(kThreads, 6) void collect_kernel(SelectArgs a) {
     }
     const float m = wave_max_f32(tm);
     if (c == c0) {
-      // The k-th largest of the threads' (or their groups') maxima: k tokens
-      // of this chunk reach it.
+      // A first theta: with r = ceil(k / 8), the least of the eight waves'
+      // r-th largest thread maximum is reached by k tokens of this chunk
+      // (with more than 256 wanted, of the four groups' maxima apart).
       if (st.kind == kTopK) {
         const bool fine = st.k > 256;
+        float t;
         if (fine) {
+          const uint32_t r = (st.k + 4 * kWaves - 1) / (4 * kWaves);
+          t = rth_largest(gm[0], r);
 #pragma unroll
-          for (int j = 0; j < kGroups; ++j) sh.list[j * kThreads + tid] = token_key(gm[j], 0);
+          for (int j = 1; j < kGroups; ++j) t = fminf(t, rth_largest(gm[j], r));
         } else {
-          sh.list[tid] = token_key(tm, 0);
+          t = rth_largest(tm, (st.k + kWaves - 1) / kWaves);
         }
-        sort_list(sh.list, fine ? kGroups * kThreads : kThreads);
-        theta = bound(token_logit(sh.list[st.k - 1]));
+        theta = -block_max(-t, sh.wave_f32);
+        if (theta == -INFINITY) {  // a wave with too few: the k-th largest of all of them
+          if (fine) {
+#pragma unroll
+            for (int j = 0; j < kGroups; ++j) sh.list[j * kThreads + tid] = token_key(gm[j], 0);
+          } else {
+            sh.list[tid] = token_key(tm, 0);
+          }
+          sort_list(sh.list, fine ? kGroups * kThreads : kThreads);
+          theta = token_logit(sh.list[st.k - 1]);
+          __syncthreads();
+        }
+        theta = bound(theta);
       } else {
         theta = bound(block_max(tm, sh.wave_f32) - depth);
       }
-      __syncthreads();
       if (tid == 0) sh.n_list = 0;
       __syncthreads();
     }
     const Part p = part_of<D>(g, m, scale2, [&](float z, int j, int i) {
       if (z >= theta) {
         const uint32_t at = atomicAdd(&sh.n_list, 1u);
-        if (at < (uint32_t)kList)
-          sh.list[at] = token_key(z, c * kChunk + (j * kThreads + tid) * D::kVec + i);
+        if (at < (uint32_t)kList) sh.list[at] = token_key(z, Row<D>::index(c, j, i));
       }
     });
     if ((tid & 63) == 0) {
       if (a.slices == 1) sh.parts[c * kWaves + wave] = p;
       else a.parts[(n * chunks + c) * kWaves + wave] = p;
     }
-    // Cut at the 2nd, 4th, 8th, ... chunk, where a list has about doubled.
+    // Cut after the 1st, 2nd, 4th, 8th, ... chunk, where a list has doubled.
     const int done = c - c0 + 1;
-    if (c + 1 < c1 && done > 1 && (done & (done - 1)) == 0 && !cut(false)) {
-      fits = false;
-      break;
-    }
-#pragma unroll
-    for (int j = 0; j < kGroups; ++j) g[j] = next[j];
-  }
+    if (c + 1 < c1 && (done & (done - 1)) == 0) fits = cut(false);
+  });
   fits = fits && cut(true);
   const uint32_t m = fits ? sh.n_list : 0;
   if (!fits || m > (uint32_t)kListMax) {
@@ -831,97 +763,417 @@ __global__ __launch_bounds__(kThreads, 6) void collect_kernel(SelectArgs a) {
   }
 }
 
+__global__ __launch_bounds__(256) void clear_kernel(uint4* p, uint32_t n) {
+  const uint32_t i = blockIdx.x * 256 + threadIdx.x;
+  if (i < n) p[i] = make_uint4(0, 0, 0, 0);
+}
+
 // ---- By buckets -------------------------------------------------------------
 
-template <class D>
-__device__ void draw_by_buckets(const SelectArgs& a, const Settings& st, int64_t n, Shared& sh) {
-  const bool greedy = st.greedy;
-  const double tau = (double)st.tau;
-  Row<D> row;
-  row.p = static_cast<const typename D::Raw*>(a.logits) + n * a.ld;
-  row.V = a.V;
-  bool bad;
-  row.zmax = (double)row_max(row, sh, &bad);
-  if (bad || st.bad) {
-    if (threadIdx.x == 0) write_bad_draw(a, n);
-    return;
-  }
-  row.inv = kPerNat / tau;
-  const Totals all = fill_buckets(row, sh);
+// Prefix sums over the collected buckets.
+struct Totals {
+  uint32_t finite;
+  double mass;  // of all tokens, in units of the anchor's weight
+};
 
-  // Lengths of the kept prefix and its mass, filter by filter.
-  uint32_t kept = all.finite;
-  double mass = all.mass;
-  if (greedy) {
-    kept = 1;
-    mass = 1.0;
+template <class D>
+__device__ Totals sum_buckets(Shared& sh) {
+  uint32_t c[kPerThread], cs = 0;
+  double m[kPerThread], ms = 0.0;
+#pragma unroll
+  for (int i = 0; i < kPerThread; ++i) {
+    const int b = threadIdx.x * kPerThread + i;
+    const bool last = b == kBuckets - 1;
+    c[i] = sh.cnt[b] - (last ? sh.facts.masked : 0u);
+    m[i] = last ? 0.0 : (double)sh.mass[b] * Row<D>::unit(b);
+    cs += c[i];
+    ms += m[i];
+  }
+  Totals t;
+  uint32_t cb = block_scan(cs, sh.wave_u32, &t.finite);
+  double mb = block_scan(ms, sh.wave_f64, &t.mass);  // (its barriers end the reads above)
+#pragma unroll
+  for (int i = 0; i < kPerThread; ++i) {
+    const int b = threadIdx.x * kPerThread + i;
+    sh.cnt[b] = cb;
+    sh.above[b] = mb;
+    cb += c[i];
+    mb += m[i];
+  }
+  if (threadIdx.x == kThreads - 1) {
+    sh.cnt[kBuckets] = t.finite;
+    sh.above[kBuckets] = mb;
+  }
+  __syncthreads();
+  t.mass = sh.above[kBuckets];
+  return t;
+}
+
+// The buckets of a row: `anchor` and zmax set, `ready` where counts, masses
+// and facts are collected already. False for a row without a draw.
+template <class D>
+__device__ bool fill_buckets(Row<D>& row, Shared& sh, bool ready, Totals* all) {
+  if (!ready) collect_buckets(row, sh, 0, row.chunks());
+  row.zmax = key_value(sh.facts.top);
+  if (sh.facts.odd || row.zmax == -INFINITY) return false;
+  if (fma(row.anchor - (double)row.zmax, row.inv, kHead) < -0.5) {
+    // The maximum lies above the buckets: once more, from the maximum itself.
+    row.anchor = (double)row.zmax;
+    __syncthreads();
+    collect_buckets(row, sh, 0, row.chunks());
+  }
+  *all = sum_buckets<D>(sh);
+  return true;
+}
+
+// Least logit whose bucket is at most b0 .. b3, by wave 0 .. 3 into sh.least
+// (+inf where the maximum's bucket is beyond): a search over the finite keys, 64 at a time.
+template <class D>
+__device__ void least_logits(const Row<D>& row, Shared& sh, int b0, int b1, int b2, int b3) {
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  __syncthreads();
+  if (wave < 4) {
+    const int b = wave == 0 ? b0 : (wave == 1 ? b1 : (wave == 2 ? b2 : b3));
+    const bool some = b >= (int)Row<D>::bucket(row.x_of(row.zmax));
+    uint32_t lo = kKeyNegInf + 1, hi = key_of(row.zmax);  // hi is in a bucket <= b
+    if (some)
+      while (lo < hi) {
+        const uint32_t step = (hi - lo) / 64 + 1;
+        const uint32_t probe = min(hi, lo + (uint32_t)lane * step);  // lo + 63 step may pass hi
+        const uint64_t in = __ballot(Row<D>::bucket(row.x_of(key_value(probe))) <= (uint32_t)b);
+        const int f = in ? __ffsll((long long)in) - 1 : 64;
+        const uint32_t above = f < 64 ? min(hi, lo + (uint32_t)f * step) : hi;
+        if (f > 0) lo = min(hi, lo + (uint32_t)(f - 1) * step) + 1;
+        hi = above;
+      }
+    if (lane == 0) sh.least[wave] = some ? key_value(hi) : INFINITY;
+  }
+  __syncthreads();
+}
+
+// Tokens with lo0 <= z < hi0 or lo1 <= z < hi1 appended to the list, in any
+// order; returns their number (which may pass the list's size).
+template <class D>
+__device__ uint32_t gather(const Row<D>& row, Shared& sh, float lo0, float hi0, float lo1,
+                           float hi1) {
+  const float least = fminf(lo0, lo1);
+  __syncthreads();
+  if (threadIdx.x == 0) sh.n_list = 0;
+  __syncthreads();
+  row.for_each([&](float z, int idx) {
+    if (z >= least && ((z >= lo0 && z < hi0) || (z >= lo1 && z < hi1))) {
+      const uint32_t s = atomicAdd(&sh.n_list, 1u);
+      if (s < (uint32_t)kList) sh.list[s] = token_key(z, idx);
+    }
+  });
+  __syncthreads();
+  return sh.n_list;
+}
+
+// Where a selection ends inside a bucket: the token, its rank there (from 0)
+// and the mass through it, in the bucket's units.
+struct Found {
+  uint64_t key;
+  uint32_t rank;
+  unsigned long long mass;
+};
+
+enum Mode { kByRank, kByMass, kByMassOver };
+
+// The buckets whose tokens are listed and sorted: up to two ranges, the first
+// one nearer the top.
+struct Listed {
+  int lo0 = 1, hi0 = 0, lo1 = 1, hi1 = 0;
+};
+
+// The first token, in order, of bucket b at which
+//   kByRank:     `rank` tokens of the bucket are reached (rank >= 1),
+//   kByMass:     the mass through it is >= want,
+//   kByMassOver: the mass through it is > want.
+// Where no token's mass gets there (want is rounded), the last one.
+template <class D>
+__device__ Found select_in_bucket(const Row<D>& row, Shared& sh, Listed& listed, int b, Mode mode,
+                                  uint32_t rank, double want) {
+  uint32_t count = sh.cnt[b + 1] - sh.cnt[b];
+  uint32_t base_cnt = 0, at = 0, m = count;
+  unsigned long long base_mass = 0;
+  auto reached = [&](uint32_t c, unsigned long long s) {
+    return mode == kByRank ? c >= rank : (mode == kByMass ? (double)s >= want : (double)s > want);
+  };
+  if (b >= listed.lo0 && b <= listed.hi0) {
+    at = sh.cnt[b] - sh.cnt[listed.lo0];
+  } else if (b >= listed.lo1 && b <= listed.hi1) {
+    at = (listed.lo0 <= listed.hi0 ? sh.cnt[listed.hi0 + 1] - sh.cnt[listed.lo0] : 0) +
+         sh.cnt[b] - sh.cnt[listed.lo1];
   } else {
-    if (st.top_k > 0 && (uint32_t)st.top_k < kept) {
-      kept = (uint32_t)st.top_k;
-      const int b = bucket_of_rank(sh, kept);
-      if (b < kBuckets - 1) {
-        const Found f = select_in_bucket(row, sh, b, sh.cnt[b + 1] - sh.cnt[b], kByRank,
-                                         kept - sh.cnt[b], 0.0);
-        mass = sh.above[b] + (double)f.mass * (bucket_weight(b) / kUnit);
-      }
-    }
-    if (st.top_p < 1.0f) {
-      const double want = (double)st.top_p * mass;
-      if (want > 0.0) {
-        const int b = bucket_of_mass(sh, want, false);
-        const Found f = select_in_bucket(row, sh, b, sh.cnt[b + 1] - sh.cnt[b], kByMass, 0,
-                                         (want - sh.above[b]) * (kUnit / bucket_weight(b)));
-        const uint32_t m = sh.cnt[b] + f.rank + 1;
-        if (m < kept) {
-          kept = m;
-          mass = sh.above[b] + (double)f.mass * (bucket_weight(b) / kUnit);
+    least_logits(row, sh, b, b - 1, -1, -1);
+    float flo = sh.least[0], fhi = sh.least[1];
+    if (count > (uint32_t)kList) {
+      listed = Listed();
+      uint64_t lo = (uint64_t)key_of(flo) << 32;
+      uint64_t hi = fhi > row.zmax ? ((uint64_t)key_of(row.zmax) << 32) | 0xFFFFFFFFull
+                                             : ((uint64_t)key_of(fhi) << 32) - 1;
+      while (count > (uint32_t)kList) {
+        // Too many to list: 2 048 finer buckets of equal key ranges. The range
+        // shrinks 2 048-fold a turn, and keys are distinct, so this ends.
+        const uint64_t range = hi - lo;
+        const int bits = 64 - __clzll((long long)(range | 1));
+        const int shift = bits > 11 ? bits - 11 : 0;
+        __syncthreads();
+        for (int i = threadIdx.x; i < kBuckets; i += kThreads) {
+          sh.fmass[i] = 0;
+          sh.fcnt[i] = 0;
         }
-      } else {
-        kept = 1;
-        mass = 1.0;
-      }
-    }
-    if (st.min_p > 1.0f) {  // no weight reaches it: the first token alone
-      kept = 1;
-      mass = 1.0;
-    } else if (st.min_p > 0.0f) {
-      // w >= min_p where x = -32 ln w <= -32 ln min_p.
-      const double most = fmax(0.0, -log((double)st.min_p) * kPerNat);
-      const int b = Row<D>::bucket(fmin(most, (double)(kBuckets - 1)));
-      if (sh.cnt[b] < kept) {
-        uint32_t c = 0;
-        unsigned long long m = 0;
-        row.for_each([&](float z, int) {
-          if (z != -INFINITY) {
-            const double x = row.x_of(z);
-            if ((row.zmax - (double)z) * row.inv <= most && Row<D>::bucket(x) == b) {
-              ++c;
-              m += Row<D>::mass(x);
-            }
+        __syncthreads();
+        row.for_each([&](float z, int idx) {
+          const uint64_t k = token_key(z, idx);
+          if (k >= lo && k <= hi) {
+            const uint32_t f = (uint32_t)((hi - k) >> shift);
+            atomicAdd(&sh.fcnt[f], 1u);
+            atomicAdd(&sh.fmass[f], Row<D>::mass(row.x_of(z)));
           }
         });
-        uint32_t call;
-        unsigned long long mall;
-        block_scan(c, sh.wave_u32, &call);
-        block_scan(m, sh.wave_u64, &mall);
-        if (sh.cnt[b] + call < kept) {
-          kept = sh.cnt[b] + call;
-          mass = sh.above[b] + (double)mall * (bucket_weight(b) / kUnit);
+        __syncthreads();
+        uint32_t c = 0;
+        unsigned long long s = 0;
+        for (int i = 0; i < kPerThread; ++i) {
+          c += sh.fcnt[threadIdx.x * kPerThread + i];
+          s += sh.fmass[threadIdx.x * kPerThread + i];
         }
+        uint32_t all_c;
+        unsigned long long all_m;
+        uint32_t cb = base_cnt + block_scan(c, sh.wave_u32, &all_c);
+        unsigned long long mb = base_mass + block_scan(s, sh.wave_u64, &all_m);
+        // First finer bucket through which the selection is reached; the last
+        // occupied one where rounding of `want` leaves none.
+        for (int i = 0; i < kPerThread; ++i) {
+          const int f = threadIdx.x * kPerThread + i;
+          const uint32_t c1 = cb + sh.fcnt[f];
+          const unsigned long long m1 = mb + sh.fmass[f];
+          const bool last = c1 == base_cnt + all_c;
+          if (sh.fcnt[f] != 0 && (reached(c1, m1) || last) &&
+              !(cb != base_cnt && reached(cb, mb))) {
+            sh.found = (uint32_t)f;
+            sh.found_cnt = cb;
+            sh.found_mass = mb;
+          }
+          cb = c1;
+          mb = m1;
+        }
+        __syncthreads();
+        const uint32_t f = sh.found;
+        base_cnt = sh.found_cnt;
+        base_mass = sh.found_mass;
+        count = sh.fcnt[f];
+        const uint64_t top = hi - ((uint64_t)f << shift);
+        const uint64_t width = (uint64_t)1 << shift;
+        lo = top - lo >= width ? top - width + 1 : lo;
+        hi = top;
+        __syncthreads();
+      }
+      if (threadIdx.x == 0) sh.n_list = 0;
+      __syncthreads();
+      row.for_each([&](float z, int idx) {
+        const uint64_t k = token_key(z, idx);
+        if (k >= lo && k <= hi) {
+          const uint32_t s = atomicAdd(&sh.n_list, 1u);
+          if (s < (uint32_t)kList) sh.list[s] = k;
+        }
+      });
+      __syncthreads();
+    } else {
+      gather(row, sh, flo, fhi, INFINITY, INFINITY);
+      listed = Listed();
+      listed.lo0 = listed.hi0 = b;
+    }
+    m = min(sh.n_list, (uint32_t)kList);
+    __syncthreads();
+    sort_list(sh.list, m);
+  }
+
+  // Masses through every listed token of the bucket, in order.
+  constexpr int kEach = kList / kThreads;
+  unsigned long long w[kEach], sum = 0;
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const uint32_t t = threadIdx.x * kEach + i;
+    w[i] = t < m ? Row<D>::mass(row.x_of(token_logit(sh.list[at + t]))) : 0ull;
+    sum += w[i];
+  }
+  unsigned long long all;
+  unsigned long long mb = base_mass + block_scan(sum, sh.wave_u64, &all);
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const uint32_t t = threadIdx.x * kEach + i;
+    const unsigned long long m1 = mb + w[i];
+    if (t < m) {
+      const uint32_t c1 = base_cnt + t + 1;
+      if ((reached(c1, m1) || t == m - 1) && !(t > 0 && reached(c1 - 1, mb))) {
+        sh.found = t;
+        sh.found_mass = m1;
+      }
+    }
+    mb = m1;
+  }
+  __syncthreads();
+  Found r;
+  r.key = sh.list[at + sh.found];
+  r.rank = base_cnt + sh.found;
+  r.mass = sh.found_mass;
+  __syncthreads();
+  return r;
+}
+
+// The bucket that holds the token of rank `k` (from 1).
+__device__ __forceinline__ int bucket_of_rank(Shared& sh, uint32_t k) {
+#pragma unroll
+  for (int i = 0; i < kPerThread; ++i) {
+    const int b = threadIdx.x * kPerThread + i;
+    if (sh.cnt[b] < k && k <= sh.cnt[b + 1]) sh.found = b;
+  }
+  __syncthreads();
+  const int b = (int)sh.found;
+  __syncthreads();
+  return b;
+}
+
+// The first occupied bucket through which the mass is >= want (> want with
+// `over`). Prefix sums of neighbouring threads may differ in the last bit, so
+// only a bucket's end is looked at; where rounding leaves none, the last
+// occupied bucket that weighs.
+__device__ __forceinline__ int bucket_of_mass(Shared& sh, double want, bool over) {
+  if (threadIdx.x == 0) {
+    sh.found = kBuckets;
+    sh.found_cnt = 0;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kPerThread; ++i) {
+    const int b = threadIdx.x * kPerThread + i;
+    if (sh.cnt[b + 1] != sh.cnt[b] && b < kBuckets - 1) {
+      const double end = sh.above[b + 1];
+      if (over ? end > want : end >= want) {
+        atomicMin(&sh.found, (uint32_t)b);
+        break;
+      }
+      atomicMax(&sh.found_cnt, (uint32_t)b);
+    }
+  }
+  __syncthreads();
+  const int b = (int)(sh.found < (uint32_t)kBuckets ? sh.found : sh.found_cnt);
+  __syncthreads();
+  return b;
+}
+
+// A draw from filled buckets.
+template <class D>
+__device__ void draw_from_buckets(const SelectArgs& a, const Settings& st, int64_t n,
+                                  const Row<D>& row, const Totals& all, Shared& sh) {
+  const double tau = (double)st.tau;
+  const double u = fmin(fmax((double)st.u, 0.0), 1.0 - 0x1p-24);
+  Listed listed;
+  // Length of the kept prefix and its mass, filter by filter.
+  uint32_t kept = all.finite;
+  double mass = all.mass;
+  if (st.top_k > 0 && (uint32_t)st.top_k < kept) {
+    kept = (uint32_t)st.top_k;
+    const int b = bucket_of_rank(sh, kept);
+    if (b < kBuckets - 1) {
+      const Found f = select_in_bucket(row, sh, listed, b, kByRank, kept - sh.cnt[b], 0.0);
+      mass = sh.above[b] + (double)f.mass * Row<D>::unit(b);
+    }
+  }
+  if (st.top_p < 1.0f) {
+    const double want = (double)st.top_p * mass;
+    if (want > 0.0) {
+      const int b = bucket_of_mass(sh, want, false);
+      if (!(st.min_p > 0.0f)) {
+        // The kept mass lies between the bucket's ends, so the drawn token's
+        // bucket is known to one or a few: list both in one pass.
+        const int lo = bucket_of_mass(sh, u * sh.above[b], true);
+        const int hi = bucket_of_mass(sh, u * sh.above[b + 1], true);
+        Listed both;
+        both.lo0 = lo;
+        both.hi0 = hi >= b ? b : hi;
+        if (hi < b) both.lo1 = both.hi1 = b;
+        const uint32_t tokens = sh.cnt[both.hi0 + 1] - sh.cnt[lo] +
+                                (hi < b ? sh.cnt[b + 1] - sh.cnt[b] : 0u);
+        if (lo <= both.hi0 && tokens <= (uint32_t)kList) {
+          least_logits(row, sh, both.hi0, lo - 1, hi < b ? b : -1, hi < b ? b - 1 : -1);
+          const float l0 = sh.least[0], h0 = sh.least[1], l1 = sh.least[2], h1 = sh.least[3];
+          const uint32_t m = gather(row, sh, l0, h0, l1, h1);
+          __syncthreads();
+          sort_list(sh.list, m);
+          listed = both;
+        }
+      }
+      const Found f = select_in_bucket(row, sh, listed, b, kByMass, 0,
+                                       (want - sh.above[b]) / Row<D>::unit(b));
+      const uint32_t m = sh.cnt[b] + f.rank + 1;
+      if (m < kept) {
+        kept = m;
+        mass = sh.above[b] + (double)f.mass * Row<D>::unit(b);
+      }
+    } else {
+      kept = 1;
+      mass = row.max_weight();
+    }
+  }
+  if (st.min_p > 1.0f) {  // no weight reaches it: the first token alone
+    kept = 1;
+    mass = row.max_weight();
+  } else if (st.min_p > 0.0f) {
+    // w >= min_p where 32 (max - z) / tau <= -32 ln min_p. The bucket that
+    // this falls in is certain to one, so three are looked through.
+    const double most = fmax(0.0, -log((double)st.min_p) * kPerNat);
+    const double x0 = fma(row.anchor - (double)row.zmax, row.inv, kHead) + most;
+    const int mid = (int)Row<D>::bucket(fmin(fmax(x0, 0.0), (double)(kBuckets - 1)));
+    const int b0 = max(mid - 1, 0), b1 = min(mid + 1, kBuckets - 1);
+    if (sh.cnt[b0] < kept) {
+      uint32_t c[3] = {0, 0, 0};
+      unsigned long long w[3] = {0, 0, 0};
+      row.for_each([&](float z, int) {
+        const double x = row.x_of(z);
+        const int d = (int)Row<D>::bucket(x) - b0;
+        if (z != -INFINITY && d >= 0 && d <= b1 - b0 &&
+            (row.zmax - (double)z) * row.inv <= most) {
+#pragma unroll
+          for (int i = 0; i < 3; ++i)
+            if (d == i) {
+              ++c[i];
+              w[i] += b0 + i < kBuckets - 1 ? Row<D>::mass(x) : 0ull;
+            }
+        }
+      });
+      uint32_t m = sh.cnt[b0];
+      double s = sh.above[b0];
+#pragma unroll
+      for (int i = 0; i < 3; ++i) {
+        uint32_t call;
+        unsigned long long wall;
+        block_scan(c[i], sh.wave_u32, &call);
+        block_scan(w[i], sh.wave_u64, &wall);
+        m += call;
+        s += (double)wall * Row<D>::unit(b0 + i);
+      }
+      if (m < kept) {
+        kept = m;
+        mass = s;
       }
     }
   }
 
-  const double u = greedy ? 0.0 : fmin(fmax((double)st.u, 0.0), 1.0 - 0x1p-24);
   const double want = u * mass;
   const int b = bucket_of_mass(sh, want, true);
-  const Found f = select_in_bucket(row, sh, b, sh.cnt[b + 1] - sh.cnt[b], kByMassOver, 0,
-                                   (want - sh.above[b]) * (kUnit / bucket_weight(b)));
+  const Found f = select_in_bucket(row, sh, listed, b, kByMassOver, 0,
+                                   (want - sh.above[b]) / Row<D>::unit(b));
   if (threadIdx.x == 0) {
-    const double s = ((double)token_logit(f.key) - row.zmax) / tau;
+    const float z = token_logit(f.key);
+    // (z - anchor) / tau: the logarithms below are in the anchor's units.
+    const double s = ((double)z - row.anchor) / tau;
     a.out_token[n] = token_index(f.key);
     a.out_logprob[n] = (float)(s - log(all.mass));
-    if (a.out_processed) a.out_processed[n] = greedy ? 0.0f : (float)(s - log(mass));
+    if (a.out_processed) a.out_processed[n] = (float)(s - log(mass));
     if (a.out_kept) a.out_kept[n] = (int32_t)kept;
   }
 }
@@ -930,33 +1182,26 @@ __device__ void draw_by_buckets(const SelectArgs& a, const Settings& st, int64_t
 // their number.
 template <class D>
 __device__ int parts_of_row(const Row<D>& row, float tau, Shared& sh) {
-  constexpr int kChunk = chunk_of<D>();
-  const int tid = threadIdx.x, chunks = (row.V + kChunk - 1) / kChunk;
   const float scale2 = scale2_of(tau);
-  for (int c = 0; c < chunks; ++c) {
-    Group<D> g[kGroups];
+  row.for_chunks(0, row.chunks(), [&](Group<D>(&g)[kGroups], int c) {
     float m = -INFINITY;
 #pragma unroll
-    for (int j = 0; j < kGroups; ++j) {
-      g[j] = load_group<D>(row.p, (int64_t)c * kChunk + (j * kThreads + tid) * D::kVec, row.V);
+    for (int j = 0; j < kGroups; ++j)
 #pragma unroll
       for (int i = 0; i < D::kVec; ++i) m = fmaxf(m, g[j].get(i));
-    }
     const Part p = part_of<D>(g, wave_max_f32(m), scale2, [](float, int, int) {});
-    if ((tid & 63) == 0) sh.parts[c * kWaves + (tid >> 6)] = p;
-  }
+    if ((threadIdx.x & 63) == 0) sh.parts[c * kWaves + (threadIdx.x >> 6)] = p;
+  });
   __syncthreads();
-  return chunks * kWaves;
+  return row.chunks() * kWaves;
 }
 
 // A row of the short lists whose list overflowed: its tokens by selection,
 // then the same ending, so that its results do not depend on how the row was
 // cut. A row where min-p leaves more than kListMax goes by buckets for good.
 template <class D, bool kTop>
-__device__ void list_by_buckets(const SelectArgs& a, const Settings& st, int64_t n, Shared& sh) {
-  Row<D> row;
-  row.p = static_cast<const typename D::Raw*>(a.logits) + n * a.ld;
-  row.V = a.V;
+__device__ void list_by_buckets(const SelectArgs& a, const Settings& st, int64_t n, Row<D>& row,
+                                Shared& sh) {
   const int parts = parts_of_row(row, st.tau, sh);
   float zmax;
   const double sum =
@@ -966,69 +1211,114 @@ __device__ void list_by_buckets(const SelectArgs& a, const Settings& st, int64_t
     else if (threadIdx.x == 0) write_bad_draw(a, n);
     return;
   }
-  row.zmax = (double)zmax;
   row.inv = kPerNat / (double)st.tau;
-  if (st.kind == kMinP) {
-    gather(row, sh, (uint64_t)key_of(bound(zmax - depth_of(st))) << 32, ~0ull);
-    const uint32_t m = sh.n_list;
+  if (!kTop && st.kind == kMinP) {
+    const uint32_t m = gather(row, sh, bound(zmax - depth_of(st)), INFINITY, INFINITY, INFINITY);
     __syncthreads();
-    if (m > (uint32_t)kListMax) {
-      if constexpr (!kTop) draw_by_buckets<D>(a, st, n, sh);
+    if (m <= (uint32_t)kListMax) {
+      sort_list(sh.list, m);
+      if constexpr (!kTop) finish_draw(a, st, n, sh.list, m, zmax, sum, sh);
       return;
     }
-    sort_list(sh.list, m);
-    if constexpr (!kTop) finish_draw(a, st, n, sh.list, m, zmax, sum, sh);
-    return;
   }
-  const Totals all = fill_buckets(row, sh);
+  row.anchor = (double)anchor_of(row, sh.wave_f32);
+  Totals all;
+  if (!fill_buckets(row, sh, false, &all)) return;  // (a bad row has left above)
+  if constexpr (!kTop)
+    if (st.kind == kMinP) {
+      draw_from_buckets(a, st, n, row, all, sh);
+      return;
+    }
   const uint32_t want = min(st.k, all.finite);
   const int b = bucket_of_rank(sh, want);
-  uint64_t lo = b == kBuckets - 1 ? (uint64_t)(kKeyNegInf + 1) << 32
-                                  : (uint64_t)least_key(row, sh, b) << 32;
-  if (sh.cnt[b + 1] > (uint32_t)kList) {
-    // More than the list holds reach that bucket: the last token's own key.
-    const uint32_t before = sh.cnt[b];
-    lo = select_in_bucket(row, sh, b, sh.cnt[b + 1] - before, kByRank, want - before, 0.0).key;
+  uint32_t m = sh.cnt[b + 1];
+  if (m <= (uint32_t)kList) {
+    least_logits(row, sh, b, -1, -1, -1);
+    const float lo = sh.least[0];
+    m = gather(row, sh, lo, INFINITY, INFINITY, INFINITY);
+  } else {
+    // More than the list holds reach that bucket: up to the last token's key.
+    Listed none;
+    const uint64_t last =
+        select_in_bucket(row, sh, none, b, kByRank, want - sh.cnt[b], 0.0).key;
+    if (threadIdx.x == 0) sh.n_list = 0;
+    __syncthreads();
+    row.for_each([&](float z, int idx) {
+      const uint64_t k = token_key(z, idx);
+      if (k >= last && z != -INFINITY) {
+        const uint32_t s = atomicAdd(&sh.n_list, 1u);
+        if (s < (uint32_t)kList) sh.list[s] = k;
+      }
+    });
+    __syncthreads();
+    m = sh.n_list;
   }
-  sort_list(sh.list, gather(row, sh, lo, ~0ull));
+  __syncthreads();
+  sort_list(sh.list, m);
   if constexpr (kTop) finish_top(a, n, sh.list, want, (double)zmax, sum);
   else finish_draw(a, st, n, sh.list, want, zmax, sum, sh);
 }
 
-// One row: its slices' lists joined, or the buckets.
+// One row: its slices' lists or buckets joined, or the whole of it.
 template <class D, bool kTop>
-__global__ __launch_bounds__(kThreads, 4) void row_kernel(SelectArgs a) {
-  __shared__ Shared sh;
-  const int64_t n = blockIdx.x;
+__device__ void finish_row(const SelectArgs& a, int64_t n, Shared& sh) {
   const Settings st = settings_of(a, n);
-  const int slices = slices_of(a, st);
-  const uint32_t* count = a.counts + n * a.slices;
+  Row<D> row;
+  row.p = static_cast<const typename D::Raw*>(a.logits) + n * a.ld;
+  row.V = a.V;
   if constexpr (!kTop)
     if (st.kind == kBuckets_) {
-      draw_by_buckets<D>(a, st, n, sh);
+      if (st.bad) {
+        if (threadIdx.x == 0) write_bad_draw(a, n);
+        return;
+      }
+      row.inv = kPerNat / (double)st.tau;
+      row.anchor = (double)anchor_of(row, sh.wave_f32);
+      const bool ready = a.slices > 1;
+      if (ready) {
+        const unsigned long long* mass = a.masses + n * kBuckets;
+        const uint32_t* cnt = a.bucket_counts + n * (kBuckets + 4);
+#pragma unroll
+        for (int i = 0; i < kPerThread; ++i) {
+          const int b = threadIdx.x + i * kThreads;
+          sh.mass[b] = mass[b];
+          sh.cnt[b] = cnt[b];
+        }
+        if (threadIdx.x == 0)
+          sh.facts = {cnt[kBuckets], cnt[kBuckets + 1], cnt[kBuckets + 2]};
+        __syncthreads();
+      }
+      Totals all;
+      if (fill_buckets(row, sh, ready, &all)) draw_from_buckets(a, st, n, row, all, sh);
+      else if (threadIdx.x == 0) write_bad_draw(a, n);
       return;
     }
-  bool over = false;
-  uint32_t m = 0;
-  for (int i = 0; i < slices; ++i) {
-    const uint32_t c = count[i];
-    over |= c == kOverflow;
-    m += c;
-  }
-  if (over) {
-    list_by_buckets<D, kTop>(a, st, n, sh);
+  // The slices' counts, and where each list starts.
+  const int slices = slices_of(a, st);
+  const uint32_t c = (int)threadIdx.x < slices ? a.counts[n * a.slices + threadIdx.x] : 0u;
+  if (threadIdx.x == 0) sh.found = 0;
+  __syncthreads();
+  if (c == kOverflow) sh.found = 1;
+  uint32_t m;
+  const uint32_t at = block_scan(c, sh.wave_u32, &m);
+  if (sh.found) {
+    __syncthreads();
+    list_by_buckets<D, kTop>(a, st, n, row, sh);
     return;
   }
   if (a.slices == 1) return;  // collect_kernel has finished the row
-  uint32_t at = 0;
-  for (int i = 0; i < slices; ++i) {
-    const uint32_t c = count[i];
-    const uint64_t* keys = a.keys + (n * a.slices + i) * kListMax;
-    for (uint32_t j = threadIdx.x; j < c; j += kThreads) sh.list[at + j] = keys[j];
-    at += c;
+  if ((int)threadIdx.x < slices) {
+    sh.cnt[threadIdx.x] = at;
+    sh.cnt[kMaxSlices + threadIdx.x] = c;
   }
+  __syncthreads();
+  for (int i = threadIdx.x >> 6; i < slices; i += kWaves) {
+    const uint64_t* keys = a.keys + (n * a.slices + i) * kListMax;
+    const uint32_t to = sh.cnt[i], len = sh.cnt[kMaxSlices + i];
+    for (uint32_t j = threadIdx.x & 63; j < len; j += 64) sh.list[to + j] = keys[j];
+  }
+  __syncthreads();
   sort_list(sh.list, m);
-  const int chunks = (a.V + chunk_of<D>() - 1) / chunk_of<D>();
   if (st.kind == kTopK) {
     m = min(m, st.k);
   } else {
@@ -1038,13 +1328,14 @@ __global__ __launch_bounds__(kThreads, 4) void row_kernel(SelectArgs a) {
     m = first_index(&sh.found, m, base, kEach,
                     [&](int i) { return token_logit(sh.list[base + i]) < theta; });
     if (m > (uint32_t)kListMax) {
-      list_by_buckets<D, kTop>(a, st, n, sh);
+      list_by_buckets<D, kTop>(a, st, n, row, sh);
       return;
     }
   }
+  const int parts = row.chunks() * kWaves;
   float zmax;
-  const double all = join_parts(a.parts + n * chunks * kWaves, chunks * kWaves,
-                                1.0 / (double)st.tau, sh.wave_f32, sh.wave_f64, &zmax);
+  const double all = join_parts(a.parts + n * parts, parts, 1.0 / (double)st.tau, sh.wave_f32,
+                                sh.wave_f64, &zmax);
   if (!(all > 0.0) || zmax == -INFINITY) {
     if constexpr (kTop) write_bad_top(a, n);
     else if (threadIdx.x == 0) write_bad_draw(a, n);
@@ -1055,11 +1346,24 @@ __global__ __launch_bounds__(kThreads, 4) void row_kernel(SelectArgs a) {
 }
 
 template <class D, bool kTop>
-hipError_t launch(const SelectArgs& a, bool lists, hipStream_t stream) {
-  if (lists) {
+__global__ __launch_bounds__(kThreads, 4) void row_kernel(SelectArgs a) {
+  __shared__ Shared sh;
+  finish_row<D, kTop>(a, blockIdx.x, sh);
+}
+
+template <class D, bool kTop>
+hipError_t launch(const SelectArgs& a, bool lists, bool buckets, hipStream_t stream) {
+  hipError_t e;
+  if (buckets && a.slices > 1) {
+    // Counts, masses and facts of all rows, cleared (they lie side by side).
+    const uint32_t words = (uint32_t)(a.bucket_bytes / sizeof(uint4));
+    clear_kernel<<<dim3((words + 255) / 256), 256, 0, stream>>>(
+        reinterpret_cast<uint4*>(a.masses), words);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+  }
+  if (lists || (buckets && a.slices > 1)) {
     collect_kernel<D, kTop><<<dim3((uint32_t)(a.N * a.slices)), kThreads, 0, stream>>>(a);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
+    if ((e = hipGetLastError()) != hipSuccess) return e;
   }
   row_kernel<D, kTop><<<dim3((uint32_t)a.N), kThreads, 0, stream>>>(a);
   return hipGetLastError();
@@ -1067,24 +1371,28 @@ hipError_t launch(const SelectArgs& a, bool lists, hipStream_t stream) {
 
 }  // namespace
 
-int select_slices(int64_t N, int64_t V, int32_t dtype) {
+// Slices of a row. Rows that fill the card by themselves are not cut.
+static int select_slices(int64_t N, int64_t V, int32_t dtype) {
   const int64_t chunk = (int64_t)kThreads * kGroups * (16 / dtype_bytes(dtype));
   const int64_t chunks = (V + chunk - 1) / chunk;
-  // Rows that fill the card by themselves are not cut.
-  return (int)std::max<int64_t>(1, std::min<int64_t>(chunks, 512 / std::max<int64_t>(N, 1)));
+  const int64_t most = std::min<int64_t>(chunks, kMaxSlices);
+  return (int)std::max<int64_t>(1, std::min<int64_t>(most, 512 / std::max<int64_t>(N, 1)));
 }
 
 SelectWorkspace select_workspace_layout(int64_t N, int64_t V, int32_t dtype) {
   const int64_t chunk = (int64_t)kThreads * kGroups * (16 / dtype_bytes(dtype));
-  const int64_t chunks = (V + chunk - 1) / chunk;
-  const size_t lists = (size_t)N * (size_t)select_slices(N, V, dtype);
-  const bool cut = select_slices(N, V, dtype) > 1;
+  const size_t chunks = (size_t)((V + chunk - 1) / chunk);
+  const int slices = select_slices(N, V, dtype);
+  const size_t lists = (size_t)N * (size_t)slices;
+  const size_t cut = slices > 1 ? 1 : 0;  // what only cut rows need
   auto up = [](size_t b) { return (b + 255) / 256 * 256; };
   SelectWorkspace w;
   w.off_counts = 0;
   w.off_parts = up(lists * sizeof(uint32_t));
-  w.off_keys = w.off_parts + (cut ? up((size_t)N * chunks * kWaves * sizeof(Part)) : 0);
-  w.total = w.off_keys + (cut ? lists * kListMax * sizeof(uint64_t) : 0);
+  w.off_keys = w.off_parts + cut * up((size_t)N * chunks * kWaves * sizeof(Part));
+  w.off_masses = w.off_keys + cut * up(lists * kListMax * sizeof(uint64_t));
+  w.off_bucket_counts = w.off_masses + cut * (size_t)N * kBuckets * sizeof(unsigned long long);
+  w.total = w.off_bucket_counts + cut * up((size_t)N * (kBuckets + 4) * sizeof(uint32_t));
   return w;
 }
 
@@ -1095,15 +1403,26 @@ hipError_t launch_select(SelectArgs a, void* workspace, hipStream_t stream) {
   a.counts = reinterpret_cast<uint32_t*>(base + w.off_counts);
   a.parts = reinterpret_cast<SelectPart*>(base + w.off_parts);
   a.keys = reinterpret_cast<uint64_t*>(base + w.off_keys);
+  a.masses = reinterpret_cast<unsigned long long*>(base + w.off_masses);
+  a.bucket_counts = reinterpret_cast<uint32_t*>(base + w.off_bucket_counts);
+  a.bucket_bytes = w.total - w.off_masses;
   const bool top = a.u == nullptr;
-  // Settings that the host sees and that no row can take by lists.
-  const bool lists = top || a.temperatures || a.top_ks || a.top_ps || a.min_ps ||
-                     a.temperature == 0.0f || (a.top_k > 0 && a.top_k <= kListMax) ||
-                     (a.top_k <= 0 && a.top_p >= 1.0f && a.min_p > 0.0f && a.min_p <= 1.0f);
+  // Which ways the rows can take, as far as the host sees the settings.
+  const bool seen = !a.temperatures && !a.top_ks && !a.top_ps && !a.min_ps;
+  const bool short_list = a.temperature == 0.0f || (a.top_k > 0 && a.top_k <= kListMax) ||
+                          (a.top_k <= 0 && a.top_p >= 1.0f && a.min_p > 0.0f && a.min_p <= 1.0f);
+  const bool lists = top || !seen || short_list;
+  const bool buckets = !top && (!seen || !short_list);
   switch (a.dtype) {
-    case LP_F32: return top ? launch<F32, true>(a, lists, stream) : launch<F32, false>(a, lists, stream);
-    case LP_BF16: return top ? launch<BF16, true>(a, lists, stream) : launch<BF16, false>(a, lists, stream);
-    default: return top ? launch<F16, true>(a, lists, stream) : launch<F16, false>(a, lists, stream);
+    case LP_F32:
+      return top ? launch<F32, true>(a, lists, buckets, stream)
+                 : launch<F32, false>(a, lists, buckets, stream);
+    case LP_BF16:
+      return top ? launch<BF16, true>(a, lists, buckets, stream)
+                 : launch<BF16, false>(a, lists, buckets, stream);
+    default:
+      return top ? launch<F16, true>(a, lists, buckets, stream)
+                 : launch<F16, false>(a, lists, buckets, stream);
   }
 }
 
