@@ -48,6 +48,22 @@ __device__ __forceinline__ Place place_of(int64_t row0, int32_t n) {
   return {row0 + r, (int32_t)(b - r * (uint32_t)n)};
 }
 
+// A thread's groups of the slice [begin, end), -inf behind its end.
+template <class D>
+__device__ __forceinline__ void load_slice(Group<D> (&g)[kDistillGroups],
+                                           const typename D::Raw* row, int64_t begin,
+                                           int64_t end) {
+  const typename D::Raw* p = row + begin + threadIdx.x * D::kVec;
+  if (end - begin == (int64_t)kDistillGroups * kDistillThreads * D::kVec) {
+#pragma unroll
+    for (int j = 0; j < kDistillGroups; ++j) g[j] = load_whole<D>(p + j * kDistillThreads * D::kVec);
+  } else {
+#pragma unroll
+    for (int j = 0; j < kDistillGroups; ++j)
+      g[j] = load_group<D>(row, begin + (int64_t)(j * kDistillThreads + threadIdx.x) * D::kVec, end);
+  }
+}
+
 // One slice's maximum and sum. The slice is held in registers, so its
 // exponentials need no running maximum.
 template <class D>
@@ -60,9 +76,7 @@ __global__ __launch_bounds__(kDistillThreads) void distill_partial_kernel(Distil
   const int64_t end = min(begin + a.slices.len, a.V_true);
   const int tid = threadIdx.x;
   Group<D> g[kDistillGroups];
-#pragma unroll
-  for (int j = 0; j < kDistillGroups; ++j)
-    g[j] = load_group<D>(row, begin + (int64_t)(j * kDistillThreads + tid) * D::kVec, end);
+  load_slice<D>(g, row, begin, end);
   float m = -INFINITY;
 #pragma unroll
   for (int j = 0; j < kDistillGroups; ++j)
@@ -205,9 +219,7 @@ __global__ __launch_bounds__(kDistillThreads) void distill_backward_kernel(Disti
       store_group<D>(out, begin + (int64_t)(j * kDistillThreads + tid) * D::kVec, end, g[0]);
     return;
   }
-#pragma unroll
-  for (int j = 0; j < kDistillGroups; ++j)
-    g[j] = load_group<D>(row, begin + (int64_t)(j * kDistillThreads + tid) * D::kVec, end);
+  load_slice<D>(g, row, begin, end);
 
   // The teacher's entries of this slice, before anything is overwritten (the
   // output may be the logits' own buffer): offset in the slice or -1, and q.

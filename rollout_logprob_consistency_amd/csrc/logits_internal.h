@@ -73,33 +73,54 @@ struct Group {
   }
 };
 
+// Four words at any alignment of the element type, and the pointers to global
+// memory that rows are read and written through: a pointer whose address space
+// is lost in a struct would become flat accesses, which wait for LDS too.
+typedef uint32_t Words __attribute__((ext_vector_type(4), aligned(2)));
+template <class T>
+using Global = __attribute__((address_space(1))) T*;
+
+template <class T>
+__device__ __forceinline__ T read_global(const T* p, int64_t i) {
+  return ((Global<const T>)p)[i];
+}
+
+// The group that starts at p, whole.
+template <class D>
+__device__ __forceinline__ Group<D> load_whole(const typename D::Raw* p) {
+  const Words v = *(Global<const Words>)(const Words*)p;
+  return {{v.x, v.y, v.z, v.w}};
+}
+
 template <class D>
 __device__ __forceinline__ Group<D> load_group(const typename D::Raw* p, int64_t i, int64_t end) {
-  Group<D> g;
-  if (i + D::kVec <= end) {
-    __builtin_memcpy(&g, p + i, 16);
-  } else {
+  if (i + D::kVec <= end) return load_whole<D>(p + i);
+  Group<D> g = {{0, 0, 0, 0}};
+  const Global<const typename D::Raw> q = (Global<const typename D::Raw>)p;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) g.w[j] = 0;
-#pragma unroll
-    for (int j = 0; j < D::kVec; ++j) g.set(j, i + j < end ? p[i + j] : D::kNegInf);
-  }
+  for (int j = 0; j < D::kVec; ++j) g.set(j, i + j < end ? q[i + j] : D::kNegInf);
   return g;
+}
+
+template <class D>
+__device__ __forceinline__ void store_whole(typename D::Raw* p, const Group<D>& g) {
+  *(Global<Words>)(Words*)p = Words{g.w[0], g.w[1], g.w[2], g.w[3]};
 }
 
 template <class D>
 __device__ __forceinline__ void store_group(typename D::Raw* p, int64_t i, int64_t end,
                                             const Group<D>& g) {
   if (i + D::kVec <= end) {
-    __builtin_memcpy(p + i, &g, 16);
-  } else {
-#pragma unroll
-    for (int j = 0; j < D::kVec; ++j)
-      if (i + j < end) {
-        if constexpr (D::kVec == 4) p[i + j] = g.w[j];
-        else p[i + j] = (typename D::Raw)(g.w[j >> 1] >> ((j & 1) * 16));
-      }
+    store_whole<D>(p + i, g);
+    return;
   }
+  const Global<typename D::Raw> q = (Global<typename D::Raw>)p;
+#pragma unroll
+  for (int j = 0; j < D::kVec; ++j)
+    if (i + j < end) {
+      if constexpr (D::kVec == 4) q[i + j] = g.w[j];
+      else q[i + j] = (typename D::Raw)(g.w[j >> 1] >> ((j & 1) * 16));
+    }
 }
 
 // ---- Distillation ---------------------------------------------------------

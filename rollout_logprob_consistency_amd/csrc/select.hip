@@ -101,7 +101,8 @@ struct Shared {
   RowFacts facts;
 };
 
-// A row and its scale. x(z) = 32 (anchor - z) / tau + 768; the bucket is
+// A row and its scale. Functions that pass over a row copy it first: where the
+// compiler does not inline them, the copy stays in registers. x(z) = 32 (anchor - z) / tau + 768; the bucket is
 // rint(x), the last one from there on.
 template <class D>
 struct Row {
@@ -140,10 +141,14 @@ struct Row {
 
   __device__ __forceinline__ int chunks() const { return (V + chunk_of<D>() - 1) / chunk_of<D>(); }
   __device__ __forceinline__ void load(Group<D> (&g)[kGroups], int c) const {
+    const int first = c * chunk_of<D>() + (int)threadIdx.x * D::kVec;
+    if ((c + 1) * chunk_of<D>() <= V) {
 #pragma unroll
-    for (int j = 0; j < kGroups; ++j)
-      g[j] = load_group<D>(
-          p, (int64_t)c * chunk_of<D>() + (j * kThreads + (int)threadIdx.x) * D::kVec, V);
+      for (int j = 0; j < kGroups; ++j) g[j] = load_whole<D>(p + first + j * kThreads * D::kVec);
+    } else {
+#pragma unroll
+      for (int j = 0; j < kGroups; ++j) g[j] = load_group<D>(p, first + j * kThreads * D::kVec, V);
+    }
   }
   static __device__ __forceinline__ int index(int c, int j, int i) {
     return c * chunk_of<D>() + (j * kThreads + (int)threadIdx.x) * D::kVec + i;
@@ -355,11 +360,11 @@ __device__ __forceinline__ Settings settings_of(const SelectArgs& a, int64_t n) 
     s = {a.temperature, 1.0f, 0.0f, 0.0f, a.top_k, false, false, kTopK, (uint32_t)a.top_k};
     return s;
   }
-  s.tau = a.temperatures ? a.temperatures[n] : a.temperature;
-  s.top_p = a.top_ps ? a.top_ps[n] : a.top_p;
-  s.min_p = a.min_ps ? a.min_ps[n] : a.min_p;
-  s.top_k = a.top_ks ? a.top_ks[n] : a.top_k;
-  s.u = a.u[n];
+  s.tau = a.temperatures ? read_global(a.temperatures, n) : a.temperature;
+  s.top_p = a.top_ps ? read_global(a.top_ps, n) : a.top_p;
+  s.min_p = a.min_ps ? read_global(a.min_ps, n) : a.min_p;
+  s.top_k = a.top_ks ? read_global(a.top_ks, n) : a.top_k;
+  s.u = read_global(a.u, n);
   s.greedy = s.tau == 0.0f;
   s.bad = !(s.tau >= 0.0f) || isnan(s.u) || isnan(s.top_p) || isnan(s.min_p);
   if (s.greedy) s.tau = 1.0f;
@@ -414,14 +419,15 @@ __device__ void write_bad_top(const SelectArgs& a, int64_t n) {
 // The row's maximum and the mass of all its tokens in units of the maximum's
 // weight, from its parts: fixed order, each part scaled in fp64. A NaN or
 // +inf logit leaves a NaN.
-__device__ __forceinline__ double join_parts(const Part* parts, int n, double inv_tau, float* words,
+template <class P>  // parts in LDS or in global memory
+__device__ __forceinline__ double join_parts(P parts, int n, double inv_tau, float* words,
                                              double* words64, float* zmax) {
   float m = -INFINITY;
   for (int i = threadIdx.x; i < n; i += kThreads) m = fmaxf(m, parts[i].m);
   m = block_max(m, words);
   double s = 0.0;
   for (int i = threadIdx.x; i < n; i += kThreads) {
-    const Part p = parts[i];
+    const Part p = {parts[i].m, parts[i].s};
     // m = -inf: nothing but masked tokens (0), or a NaN among them.
     s += p.m == -INFINITY ? (double)p.s
                           : (double)p.s * exp_f64(((double)p.m - (double)m) * inv_tau);
@@ -543,7 +549,8 @@ struct CollectShared {
 // The maximum of the first chunk that has a finite logit (or +inf): the
 // anchor of the buckets. -inf where there is none.
 template <class D>
-__device__ float anchor_of(const Row<D>& row, float* words) {
+__device__ float anchor_of(const Row<D>& row_in, float* words) {
+  const Row<D> row = row_in;
   float m = -INFINITY;
   for (int c = 0; c < row.chunks() && m == -INFINITY; ++c) {
     Group<D> g[kGroups];
@@ -563,7 +570,8 @@ __device__ float anchor_of(const Row<D>& row, float* words) {
 // by the maximum that there are some. No element is skipped: -inf goes to the
 // last bucket and is counted apart.
 template <class D, class S>
-__device__ void collect_buckets(const Row<D>& row, S& sh, int c0, int c1) {
+__device__ void collect_buckets(const Row<D>& row_in, S& sh, int c0, int c1) {
+  const Row<D> row = row_in;
   for (int i = threadIdx.x; i < kBuckets; i += kThreads) {
     sh.mass[i] = 0;
     sh.cnt[i] = 0;
@@ -571,7 +579,7 @@ __device__ void collect_buckets(const Row<D>& row, S& sh, int c0, int c1) {
   if (threadIdx.x == 0) sh.facts = {0u, 0u, 0u};
   __syncthreads();
   float top = -INFINITY;
-  bool odd = false;
+  uint64_t odd = 0;  // by lane
   uint32_t masked = 0;
   row.for_chunks(c0, c1, [&](Group<D>(&g)[kGroups], int) {
 #pragma unroll
@@ -584,16 +592,15 @@ __device__ void collect_buckets(const Row<D>& row, S& sh, int c0, int c1) {
         atomicAdd(&sh.cnt[b], 1u);
         atomicAdd(&sh.mass[b], Row<D>::mass(x));
         top = fmaxf(top, z);
-        odd |= __builtin_amdgcn_classf(z, 0x203);  // NaN, +inf
+        odd |= __ballot(__builtin_amdgcn_classf(z, 0x203));  // NaN, +inf
         masked += (uint32_t)__popcll(__ballot(z == -INFINITY));
         if (i % 4 == 3) __builtin_amdgcn_sched_barrier(0);  // bounds the registers in use
       }
   });
   top = wave_max_f32(top);
-  const bool any = __ballot(odd) != 0;
   if ((threadIdx.x & 63) == 0) {
     atomicMax(&sh.facts.top, key_of(top));
-    if (any) atomicOr(&sh.facts.odd, 1u);
+    if (odd) atomicOr(&sh.facts.odd, 1u);
     atomicAdd(&sh.facts.masked, masked);
   }
   __syncthreads();
@@ -829,7 +836,8 @@ __device__ bool fill_buckets(Row<D>& row, Shared& sh, bool ready, Totals* all) {
 // Least logit whose bucket is at most b0 .. b3, by wave 0 .. 3 into sh.least
 // (+inf where the maximum's bucket is beyond): a search over the finite keys, 64 at a time.
 template <class D>
-__device__ void least_logits(const Row<D>& row, Shared& sh, int b0, int b1, int b2, int b3) {
+__device__ void least_logits(const Row<D>& row_in, Shared& sh, int b0, int b1, int b2, int b3) {
+  const Row<D> row = row_in;
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   __syncthreads();
   if (wave < 4) {
@@ -854,8 +862,9 @@ __device__ void least_logits(const Row<D>& row, Shared& sh, int b0, int b1, int 
 // Tokens with lo0 <= z < hi0 or lo1 <= z < hi1 appended to the list, in any
 // order; returns their number (which may pass the list's size).
 template <class D>
-__device__ uint32_t gather(const Row<D>& row, Shared& sh, float lo0, float hi0, float lo1,
+__device__ uint32_t gather(const Row<D>& row_in, Shared& sh, float lo0, float hi0, float lo1,
                            float hi1) {
+  const Row<D> row = row_in;
   const float least = fminf(lo0, lo1);
   __syncthreads();
   if (threadIdx.x == 0) sh.n_list = 0;
@@ -892,8 +901,9 @@ struct Listed {
 //   kByMassOver: the mass through it is > want.
 // Where no token's mass gets there (want is rounded), the last one.
 template <class D>
-__device__ Found select_in_bucket(const Row<D>& row, Shared& sh, Listed& listed, int b, Mode mode,
+__device__ Found select_in_bucket(const Row<D>& row_in, Shared& sh, Listed& listed, int b, Mode mode,
                                   uint32_t rank, double want) {
+  const Row<D> row = row_in;
   uint32_t count = sh.cnt[b + 1] - sh.cnt[b];
   uint32_t base_cnt = 0, at = 0, m = count;
   unsigned long long base_mass = 0;
@@ -1068,7 +1078,8 @@ __device__ __forceinline__ int bucket_of_mass(Shared& sh, double want, bool over
 // A draw from filled buckets.
 template <class D>
 __device__ void draw_from_buckets(const SelectArgs& a, const Settings& st, int64_t n,
-                                  const Row<D>& row, const Totals& all, Shared& sh) {
+                                  const Row<D>& row_in, const Totals& all, Shared& sh) {
+  const Row<D> row = row_in;
   const double tau = (double)st.tau;
   const double u = fmin(fmax((double)st.u, 0.0), 1.0 - 0x1p-24);
   Listed listed;
@@ -1181,7 +1192,8 @@ __device__ void draw_from_buckets(const SelectArgs& a, const Settings& st, int64
 // The parts of a row as collect_kernel forms them, into sh.parts; returns
 // their number.
 template <class D>
-__device__ int parts_of_row(const Row<D>& row, float tau, Shared& sh) {
+__device__ int parts_of_row(const Row<D>& row_in, float tau, Shared& sh) {
+  const Row<D> row = row_in;
   const float scale2 = scale2_of(tau);
   row.for_chunks(0, row.chunks(), [&](Group<D>(&g)[kGroups], int c) {
     float m = -INFINITY;
@@ -1281,8 +1293,8 @@ __device__ void finish_row(const SelectArgs& a, int64_t n, Shared& sh) {
 #pragma unroll
         for (int i = 0; i < kPerThread; ++i) {
           const int b = threadIdx.x + i * kThreads;
-          sh.mass[b] = mass[b];
-          sh.cnt[b] = cnt[b];
+          sh.mass[b] = read_global(mass, b);
+          sh.cnt[b] = read_global(cnt, b);
         }
         if (threadIdx.x == 0)
           sh.facts = {cnt[kBuckets], cnt[kBuckets + 1], cnt[kBuckets + 2]};
@@ -1295,7 +1307,7 @@ __device__ void finish_row(const SelectArgs& a, int64_t n, Shared& sh) {
     }
   // The slices' counts, and where each list starts.
   const int slices = slices_of(a, st);
-  const uint32_t c = (int)threadIdx.x < slices ? a.counts[n * a.slices + threadIdx.x] : 0u;
+  const uint32_t c = (int)threadIdx.x < slices ? read_global(a.counts, n * a.slices + threadIdx.x) : 0u;
   if (threadIdx.x == 0) sh.found = 0;
   __syncthreads();
   if (c == kOverflow) sh.found = 1;
@@ -1315,7 +1327,7 @@ __device__ void finish_row(const SelectArgs& a, int64_t n, Shared& sh) {
   for (int i = threadIdx.x >> 6; i < slices; i += kWaves) {
     const uint64_t* keys = a.keys + (n * a.slices + i) * kListMax;
     const uint32_t to = sh.cnt[i], len = sh.cnt[kMaxSlices + i];
-    for (uint32_t j = threadIdx.x & 63; j < len; j += 64) sh.list[to + j] = keys[j];
+    for (uint32_t j = threadIdx.x & 63; j < len; j += 64) sh.list[to + j] = read_global(keys, j);
   }
   __syncthreads();
   sort_list(sh.list, m);
@@ -1334,7 +1346,7 @@ __device__ void finish_row(const SelectArgs& a, int64_t n, Shared& sh) {
   }
   const int parts = row.chunks() * kWaves;
   float zmax;
-  const double all = join_parts(a.parts + n * parts, parts, 1.0 / (double)st.tau, sh.wave_f32,
+  const double all = join_parts((Global<const Part>)(a.parts + n * parts), parts, 1.0 / (double)st.tau, sh.wave_f32,
                                 sh.wave_f64, &zmax);
   if (!(all > 0.0) || zmax == -INFINITY) {
     if constexpr (kTop) write_bad_top(a, n);
