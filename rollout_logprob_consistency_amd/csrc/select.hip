@@ -325,23 +325,102 @@ __device__ __forceinline__ float wave_sum_f32(float s) {
          __int_as_float(lane_value(__float_as_int(s), 32));
 }
 
-// The part of a wave whose lanes hold these groups: the same terms in the
-// same order wherever it is formed. f(z, j, i) sees every logit.
+// The log2 offset that a part of base m counts from: the integer next to m c
+// where that is small enough to be one, else m c itself. c = log2(e) / tau as
+// a float; it stands for the temperature wherever parts are used, so that its
+// rounding scales differences of logits and not the logits.
+__device__ __forceinline__ bool near_offset(float m, float c) { return fabsf(m * c) < 0x1p40f; }
+__device__ __forceinline__ double offset_of(float m, float c) {
+  return near_offset(m, c) ? (double)rintf(m * c) : (double)m * (double)c;
+}
+
+// Sum over a wave's groups of 2^(z c - offset(m)), f(z, j, i) seeing every logit.
 template <class D, class F>
-__device__ __forceinline__ Part part_of(Group<D> (&g)[kGroups], float m, float scale2, F f) {
-  const float base = m == -INFINITY ? 0.0f : m;  // masked tokens sum to 0, a NaN stays one
+__device__ __forceinline__ float sum_of(Group<D> (&g)[kGroups], float m, float c, F f) {
   float s = 0.0f;
+  if (near_offset(m, c)) {
+    const float b = rintf(m * c);
 #pragma unroll
-  for (int j = 0; j < kGroups; ++j) {
-    g[j].fresh();
+    for (int j = 0; j < kGroups; ++j) {
+      g[j].fresh();
 #pragma unroll
-    for (int i = 0; i < D::kVec; ++i) {
-      const float z = g[j].get(i);
-      s += __builtin_amdgcn_exp2f((z - base) * scale2);
-      f(z, j, i);
+      for (int i = 0; i < D::kVec; ++i) {
+        const float z = g[j].get(i);
+        s += __builtin_amdgcn_exp2f(fmaf(z, c, -b));
+        f(z, j, i);
+      }
+    }
+  } else {
+    const float base = m == -INFINITY ? 0.0f : m;  // masked tokens sum to 0, a NaN stays one
+#pragma unroll
+    for (int j = 0; j < kGroups; ++j)
+#pragma unroll
+      for (int i = 0; i < D::kVec; ++i) {
+        const float z = g[j].get(i);
+        s += __builtin_amdgcn_exp2f((z - base) * c);
+        f(z, j, i);
+      }
+  }
+  return wave_sum_f32(s);
+}
+
+// The part of a wave whose lanes hold these groups: the same terms in the same
+// order wherever it is formed. Its base is the maximum of the first groups
+// alone, which spares most of a pass; where a sum gets out of 2^32, or is none,
+// it is formed again from the maximum of all.
+template <class D, class F>
+__device__ __forceinline__ Part part_of(Group<D> (&g)[kGroups], float c, F f) {
+  float m = g[0].get(0);
+#pragma unroll
+  for (int i = 1; i < D::kVec; ++i) m = fmaxf(m, g[0].get(i));
+  m = wave_max_f32(m);
+  float s = sum_of<D>(g, m, c, f);
+  if (!(s < 0x1p32f) || !near_offset(m, c)) {
+#pragma unroll
+    for (int j = 0; j < kGroups; ++j) {
+      g[j].fresh();
+#pragma unroll
+      for (int i = 0; i < D::kVec; ++i) m = fmaxf(m, g[j].get(i));
+    }
+    m = wave_max_f32(m);
+    s = sum_of<D>(g, m, c, [](float, int, int) {});
+  }
+  return {m, s};
+}
+
+// Tokens that hit(z) appended to the list, in any order. The lanes' hits of up
+// to 16 places are gathered as masks first, so that a wave asks for its places
+// in the list once and not per hit.
+template <class D, class F>
+__device__ __forceinline__ void append(const Group<D> (&g)[kGroups], int index0, uint64_t* list,
+                                       uint32_t* n_list, F hit) {
+  constexpr int kBatch = 16 / D::kVec;  // groups
+#pragma unroll
+  for (int j0 = 0; j0 < kGroups; j0 += kBatch) {
+    uint64_t masks[16], any = 0;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      masks[e] = __ballot(hit(g[j0 + e / D::kVec].get(e % D::kVec)));
+      any |= masks[e];
+    }
+    if (any == 0) continue;
+    uint32_t total = 0;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) total += (uint32_t)__popcll(masks[e]);
+    uint32_t at = 0;
+    if ((threadIdx.x & 63) == 0) at = atomicAdd(n_list, total);
+    at = __builtin_amdgcn_readfirstlane(at);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      if (masks[e] == 0) continue;
+      const uint32_t to = at + lanes_below(masks[e]);
+      if ((masks[e] >> (threadIdx.x & 63) & 1) && to < (uint32_t)kList) {
+        const int j = j0 + e / D::kVec, i = e % D::kVec;
+        list[to] = token_key(g[j].get(i), index0 + j * kThreads * D::kVec + i);
+      }
+      at += (uint32_t)__popcll(masks[e]);
     }
   }
-  return {m, wave_sum_f32(s)};
 }
 
 enum Kind { kBuckets_, kTopK, kMinP };
@@ -416,26 +495,40 @@ __device__ void write_bad_top(const SelectArgs& a, int64_t n) {
   }
 }
 
-// The row's maximum and the mass of all its tokens in units of the maximum's
-// weight, from its parts: fixed order, each part scaled in fp64. A NaN or
-// +inf logit leaves a NaN.
+// log2 of the sum of all 2^(z c) as top + rest: top alone may be as large as
+// the logits, and the two are subtracted from a logit's z c one after the other.
+// rest is NaN where a NaN or +inf logit is, -inf where all are masked.
+struct Log2Sum {
+  double top, rest;
+};
+
+// The sum from a row's parts: fixed order, each part scaled in fp64.
 template <class P>  // parts in LDS or in global memory
-__device__ __forceinline__ double join_parts(P parts, int n, double inv_tau, float* words,
-                                             double* words64, float* zmax) {
-  float m = -INFINITY;
-  for (int i = threadIdx.x; i < n; i += kThreads) m = fmaxf(m, parts[i].m);
-  m = block_max(m, words);
+__device__ __forceinline__ Log2Sum join_parts(P parts, int n, float c, double* words) {
+  double top = -INFINITY;
+  for (int i = threadIdx.x; i < n; i += kThreads) top = fmax(top, offset_of(parts[i].m, c));
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) top = fmax(top, __shfl_xor(top, d));
+  if ((threadIdx.x & 63) == 0) words[threadIdx.x >> 6] = top;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) top = fmax(top, words[w]);
+  __syncthreads();
   double s = 0.0;
   for (int i = threadIdx.x; i < n; i += kThreads) {
-    const Part p = {parts[i].m, parts[i].s};
-    // m = -inf: nothing but masked tokens (0), or a NaN among them.
-    s += p.m == -INFINITY ? (double)p.s
-                          : (double)p.s * exp_f64(((double)p.m - (double)m) * inv_tau);
+    const float m = parts[i].m, t = parts[i].s;
+    s += m == -INFINITY ? (double)t
+                        : (double)t * exp_f64((offset_of(m, c) - top) * 0.69314718055994531);
   }
   double all;
-  block_scan(s, words64, &all);
-  *zmax = m;
-  return all;
+  block_scan(s, words, &all);
+  if (top == -INFINITY) return {0.0, all == 0.0 ? -INFINITY : NAN};
+  return {top, log2(all)};
+}
+
+// The score of a logit under the whole vocabulary, from the sum's log2.
+__device__ __forceinline__ float score_of(float z, float c, const Log2Sum& all) {
+  return (float)(((double)z * (double)c - all.top - all.rest) * 0.69314718055994531);
 }
 
 // First index (of each thread's, then of all) with hit; n where there is none.
@@ -459,9 +552,9 @@ __device__ __forceinline__ uint32_t first_index(uint32_t* word, uint32_t n, uint
 // The draw from a sorted list that holds every token that can be kept.
 template <class Words>
 __device__ void finish_draw(const SelectArgs& a, const Settings& st, int64_t n, const uint64_t* list,
-                            uint32_t m, float zmax, double all, Words& w) {
+                            uint32_t m, const Log2Sum& all, Words& w) {
   constexpr int kEach = kList / kThreads;
-  const double tau = (double)st.tau, top = (double)zmax;
+  const double tau = (double)st.tau, top = (double)token_logit(list[0]);
   const uint32_t base = threadIdx.x * kEach;
   double x[kEach], c[kEach], sum = 0.0;  // -ln weight; sums through each token
 #pragma unroll
@@ -507,7 +600,7 @@ __device__ void finish_draw(const SelectArgs& a, const Settings& st, int64_t n, 
     const uint64_t t = list[rank];
     const double s = ((double)token_logit(t) - top) / tau;
     a.out_token[n] = token_index(t);
-    a.out_logprob[n] = (float)(s - log(all));
+    a.out_logprob[n] = score_of(token_logit(t), scale2_of(st.tau), all);
     if (a.out_processed) a.out_processed[n] = st.greedy ? 0.0f : (float)(s - log(mass));
     if (a.out_kept) a.out_kept[n] = (int32_t)kept;
   }
@@ -515,8 +608,8 @@ __device__ void finish_draw(const SelectArgs& a, const Settings& st, int64_t n, 
 
 // The first k tokens from a sorted list of m.
 __device__ void finish_top(const SelectArgs& a, int64_t n, const uint64_t* list, uint32_t m,
-                           double zmax, double all) {
-  const double tau = (double)a.temperature, ln_mass = log(all);
+                           const Log2Sum& all) {
+  const float c = scale2_of(a.temperature);
   for (uint32_t i = threadIdx.x; i < (uint32_t)a.top_k; i += kThreads) {
     const bool there = i < m;
     const uint64_t t = there ? list[i] : 0;
@@ -524,9 +617,9 @@ __device__ void finish_top(const SelectArgs& a, int64_t n, const uint64_t* list,
     const int64_t o = n * a.top_k + i;
     a.out_ids[o] = there ? token_index(t) : -1;
     a.out_logits[o] = z;
-    a.out_logprob[o] = (float)(((double)z - zmax) / tau - ln_mass);
+    a.out_logprob[o] = score_of(z, c, all);
   }
-  if (threadIdx.x == 0 && a.out_lse) a.out_lse[n] = (float)(zmax / tau + ln_mass);
+  if (threadIdx.x == 0 && a.out_lse) a.out_lse[n] = -score_of(0.0f, c, all);
 }
 
 struct CollectShared {
@@ -687,16 +780,15 @@ __global__ __launch_bounds__(kThreads, 6) void collect_kernel(SelectArgs a) {
   bool fits = true;
   row.for_chunks(c0, c1, [&](Group<D>(&g)[kGroups], int c) {
     if (!fits) return;
-    float tm = -INFINITY, gm[kGroups];
-#pragma unroll
-    for (int j = 0; j < kGroups; ++j) {
-      gm[j] = -INFINITY;
-#pragma unroll
-      for (int i = 0; i < D::kVec; ++i) gm[j] = fmaxf(gm[j], g[j].get(i));
-      tm = fmaxf(tm, gm[j]);
-    }
-    const float m = wave_max_f32(tm);
     if (c == c0) {
+      float tm = -INFINITY, gm[kGroups];
+#pragma unroll
+      for (int j = 0; j < kGroups; ++j) {
+        gm[j] = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < D::kVec; ++i) gm[j] = fmaxf(gm[j], g[j].get(i));
+        tm = fmaxf(tm, gm[j]);
+      }
       // A first theta: with r = ceil(k / 8), the least of the eight waves'
       // r-th largest thread maximum is reached by k tokens of this chunk
       // (with more than 256 wanted, of the four groups' maxima apart).
@@ -730,12 +822,8 @@ __global__ __launch_bounds__(kThreads, 6) void collect_kernel(SelectArgs a) {
       if (tid == 0) sh.n_list = 0;
       __syncthreads();
     }
-    const Part p = part_of<D>(g, m, scale2, [&](float z, int j, int i) {
-      if (z >= theta) {
-        const uint32_t at = atomicAdd(&sh.n_list, 1u);
-        if (at < (uint32_t)kList) sh.list[at] = token_key(z, Row<D>::index(c, j, i));
-      }
-    });
+    const Part p = part_of<D>(g, scale2, [](float, int, int) {});
+    append<D>(g, Row<D>::index(c, 0, 0), sh.list, &sh.n_list, [&](float z) { return z >= theta; });
     if ((tid & 63) == 0) {
       if (a.slices == 1) sh.parts[c * kWaves + wave] = p;
       else a.parts[(n * chunks + c) * kWaves + wave] = p;
@@ -756,17 +844,15 @@ __global__ __launch_bounds__(kThreads, 6) void collect_kernel(SelectArgs a) {
     if (tid == 0) count[slice] = m;
     return;
   }
-  float zmax;
-  const double all =
-      join_parts(sh.parts, chunks * kWaves, 1.0 / (double)st.tau, sh.wave_f32, sh.wave_f64, &zmax);
+  const Log2Sum log2_all = join_parts(sh.parts, chunks * kWaves, scale2, sh.wave_f64);
   if (tid == 0) count[0] = 0;
-  if (!(all > 0.0) || zmax == -INFINITY) {
+  if (m == 0 || isnan(log2_all.rest)) {
     if (kTop) write_bad_top(a, n);
     else if (tid == 0) write_bad_draw(a, n);
   } else if (kTop) {
-    finish_top(a, n, sh.list, m, (double)zmax, all);
+    finish_top(a, n, sh.list, m, log2_all);
   } else {
-    finish_draw(a, st, n, sh.list, m, zmax, all, sh);
+    finish_draw(a, st, n, sh.list, m, log2_all, sh);
   }
 }
 
@@ -865,15 +951,13 @@ template <class D>
 __device__ uint32_t gather(const Row<D>& row_in, Shared& sh, float lo0, float hi0, float lo1,
                            float hi1) {
   const Row<D> row = row_in;
-  const float least = fminf(lo0, lo1);
   __syncthreads();
   if (threadIdx.x == 0) sh.n_list = 0;
   __syncthreads();
-  row.for_each([&](float z, int idx) {
-    if (z >= least && ((z >= lo0 && z < hi0) || (z >= lo1 && z < hi1))) {
-      const uint32_t s = atomicAdd(&sh.n_list, 1u);
-      if (s < (uint32_t)kList) sh.list[s] = token_key(z, idx);
-    }
+  row.for_chunks(0, row.chunks(), [&](Group<D>(&g)[kGroups], int c) {
+    append<D>(g, Row<D>::index(c, 0, 0), sh.list, &sh.n_list, [&](float z) {
+      return (z >= lo0 && z < hi0) || (z >= lo1 && z < hi1);
+    });
   });
   __syncthreads();
   return sh.n_list;
@@ -1052,27 +1136,32 @@ __device__ __forceinline__ int bucket_of_rank(Shared& sh, uint32_t k) {
 // only a bucket's end is looked at; where rounding leaves none, the last
 // occupied bucket that weighs.
 __device__ __forceinline__ int bucket_of_mass(Shared& sh, double want, bool over) {
-  if (threadIdx.x == 0) {
-    sh.found = kBuckets;
-    sh.found_cnt = 0;
-  }
-  __syncthreads();
+  int first = kBuckets, last = -1;
 #pragma unroll
-  for (int i = 0; i < kPerThread; ++i) {
+  for (int i = kPerThread - 1; i >= 0; --i) {
     const int b = threadIdx.x * kPerThread + i;
-    if (sh.cnt[b + 1] != sh.cnt[b] && b < kBuckets - 1) {
-      const double end = sh.above[b + 1];
-      if (over ? end > want : end >= want) {
-        atomicMin(&sh.found, (uint32_t)b);
-        break;
-      }
-      atomicMax(&sh.found_cnt, (uint32_t)b);
-    }
+    const double end = sh.above[b + 1];
+    const bool occupied = sh.cnt[b + 1] != sh.cnt[b] && b < kBuckets - 1;
+    if (occupied && last < 0) last = b;
+    if (occupied && (over ? end > want : end >= want)) first = b;
+  }
+  // Buckets ascend with lanes: the first lane that has one, the last occupied.
+  const uint64_t hit = __ballot(first < kBuckets), some = __ballot(last >= 0);
+  const int f = hit ? __builtin_amdgcn_readlane(first, __ffsll((long long)hit) - 1) : kBuckets;
+  const int l = some ? __builtin_amdgcn_readlane(last, 63 - __clzll((long long)some)) : 0;
+  if ((threadIdx.x & 63) == 0) {
+    sh.wave_u32[threadIdx.x >> 6] = (uint32_t)f;
+    sh.wave_u64[threadIdx.x >> 6] = (uint64_t)l;
   }
   __syncthreads();
-  const int b = (int)(sh.found < (uint32_t)kBuckets ? sh.found : sh.found_cnt);
+  int b = kBuckets, e = 0;
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) {
+    b = min(b, (int)sh.wave_u32[w]);
+    e = max(e, (int)sh.wave_u64[w]);
+  }
   __syncthreads();
-  return b;
+  return b < kBuckets ? b : e;
 }
 
 // A draw from filled buckets.
@@ -1196,16 +1285,19 @@ __device__ int parts_of_row(const Row<D>& row_in, float tau, Shared& sh) {
   const Row<D> row = row_in;
   const float scale2 = scale2_of(tau);
   row.for_chunks(0, row.chunks(), [&](Group<D>(&g)[kGroups], int c) {
-    float m = -INFINITY;
-#pragma unroll
-    for (int j = 0; j < kGroups; ++j)
-#pragma unroll
-      for (int i = 0; i < D::kVec; ++i) m = fmaxf(m, g[j].get(i));
-    const Part p = part_of<D>(g, wave_max_f32(m), scale2, [](float, int, int) {});
+    const Part p = part_of<D>(g, scale2, [](float, int, int) {});
     if ((threadIdx.x & 63) == 0) sh.parts[c * kWaves + (threadIdx.x >> 6)] = p;
   });
   __syncthreads();
   return row.chunks() * kWaves;
+}
+
+template <class D>
+__device__ float max_of(const Row<D>& row_in, Shared& sh) {
+  const Row<D> row = row_in;
+  float m = -INFINITY;
+  row.for_each([&](float z, int) { m = fmaxf(m, z); });
+  return block_max(m, sh.wave_f32);
 }
 
 // A row of the short lists whose list overflowed: its tokens by selection,
@@ -1215,21 +1307,20 @@ template <class D, bool kTop>
 __device__ void list_by_buckets(const SelectArgs& a, const Settings& st, int64_t n, Row<D>& row,
                                 Shared& sh) {
   const int parts = parts_of_row(row, st.tau, sh);
-  float zmax;
-  const double sum =
-      join_parts(sh.parts, parts, 1.0 / (double)st.tau, sh.wave_f32, sh.wave_f64, &zmax);
-  if (!(sum > 0.0) || zmax == -INFINITY) {
+  const Log2Sum log2_all = join_parts(sh.parts, parts, scale2_of(st.tau), sh.wave_f64);
+  if (!isfinite(log2_all.rest)) {
     if constexpr (kTop) write_bad_top(a, n);
     else if (threadIdx.x == 0) write_bad_draw(a, n);
     return;
   }
   row.inv = kPerNat / (double)st.tau;
   if (!kTop && st.kind == kMinP) {
-    const uint32_t m = gather(row, sh, bound(zmax - depth_of(st)), INFINITY, INFINITY, INFINITY);
+    const float lo = bound(max_of(row, sh) - depth_of(st));
+    const uint32_t m = gather(row, sh, lo, INFINITY, INFINITY, INFINITY);
     __syncthreads();
     if (m <= (uint32_t)kListMax) {
       sort_list(sh.list, m);
-      if constexpr (!kTop) finish_draw(a, st, n, sh.list, m, zmax, sum, sh);
+      if constexpr (!kTop) finish_draw(a, st, n, sh.list, m, log2_all, sh);
       return;
     }
   }
@@ -1267,8 +1358,8 @@ __device__ void list_by_buckets(const SelectArgs& a, const Settings& st, int64_t
   }
   __syncthreads();
   sort_list(sh.list, m);
-  if constexpr (kTop) finish_top(a, n, sh.list, want, (double)zmax, sum);
-  else finish_draw(a, st, n, sh.list, want, zmax, sum, sh);
+  if constexpr (kTop) finish_top(a, n, sh.list, want, log2_all);
+  else finish_draw(a, st, n, sh.list, want, log2_all, sh);
 }
 
 // One row: its slices' lists or buckets joined, or the whole of it.
@@ -1345,16 +1436,15 @@ __device__ void finish_row(const SelectArgs& a, int64_t n, Shared& sh) {
     }
   }
   const int parts = row.chunks() * kWaves;
-  float zmax;
-  const double all = join_parts((Global<const Part>)(a.parts + n * parts), parts, 1.0 / (double)st.tau, sh.wave_f32,
-                                sh.wave_f64, &zmax);
-  if (!(all > 0.0) || zmax == -INFINITY) {
+  const Log2Sum log2_all = join_parts((Global<const Part>)(a.parts + n * parts), parts,
+                                     scale2_of(st.tau), sh.wave_f64);
+  if (m == 0 || isnan(log2_all.rest)) {
     if constexpr (kTop) write_bad_top(a, n);
     else if (threadIdx.x == 0) write_bad_draw(a, n);
     return;
   }
-  if constexpr (kTop) finish_top(a, n, sh.list, m, (double)zmax, all);
-  else finish_draw(a, st, n, sh.list, m, zmax, all, sh);
+  if constexpr (kTop) finish_top(a, n, sh.list, m, log2_all);
+  else finish_draw(a, st, n, sh.list, m, log2_all, sh);
 }
 
 template <class D, bool kTop>

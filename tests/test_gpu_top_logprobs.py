@@ -1,6 +1,6 @@
 """lp_top_logprobs against the fp64 oracle. Ids and logits are exact; logprobs
-and lse are rounded to fp32 once (2^-24 relative), and their log-sum-exp has
-the error of the token draw's raw score (75 * 2^-24 absolute, derived there)."""
+and lse are rounded to fp32 once (2^-24 relative) and have the error of the
+token draw's raw score, derived there (86 * 2^-24 absolute, 2^-24 relative)."""
 
 import numpy as np
 import pytest
@@ -27,7 +27,7 @@ def check(t, z, k, temperature=1.0, v_true=None):
     for g, r in ((logp, r_lp), (lse.cpu().numpy(), r_lse)):
         finite = np.isfinite(r)
         assert np.array_equal(g[~finite], r[~finite].astype(np.float32), equal_nan=True)
-        assert np.all(np.abs(g[finite] - r[finite]) <= 2.0 ** -24 * np.abs(r[finite]) + 75 * 2.0 ** -24)
+        assert np.all(np.abs(g[finite] - r[finite]) <= 2.0 ** -23 * np.abs(r[finite]) + 86 * 2.0 ** -24)
     return got
 
 
