@@ -24,6 +24,10 @@
 
 #include "logits_internal.h"
 
+// Lambdas here capture by reference; one that is not inlined would put what it
+// captures into scratch memory, whose loads wait for the row's.
+#define LP_INLINE __attribute__((always_inline))
+
 namespace lp {
 namespace {
 
@@ -101,8 +105,7 @@ struct Shared {
   RowFacts facts;
 };
 
-// A row and its scale. Functions that pass over a row copy it first: where the
-// compiler does not inline them, the copy stays in registers. x(z) = 32 (anchor - z) / tau + 768; the bucket is
+// A row and its scale. x(z) = 32 (anchor - z) / tau + 768; the bucket is
 // rint(x), the last one from there on.
 template <class D>
 struct Row {
@@ -168,7 +171,7 @@ struct Row {
   // f(logit, index) for every token; places behind the row are -inf.
   template <class F>
   __device__ __forceinline__ void for_each(F f) const {
-    for_chunks(0, chunks(), [&](Group<D>(&g)[kGroups], int c) {
+    for_chunks(0, chunks(), [&](Group<D>(&g)[kGroups], int c) LP_INLINE {
 #pragma unroll
       for (int j = 0; j < kGroups; ++j)
 #pragma unroll
@@ -226,7 +229,7 @@ __device__ __forceinline__ uint64_t lane_xor(uint64_t v) {
   if constexpr (kJ == 32) {
     return __shfl_xor((unsigned long long)v, 32);
   } else {
-    auto half = [](int x) {
+    auto half = [](int x) LP_INLINE {
       if constexpr (kJ <= 2) return xlane<kJ>(x);  // quad permutations are true exchanges
       else return __builtin_amdgcn_ds_swizzle(x, (kJ << 10) | 0x1F);
     };
@@ -383,7 +386,7 @@ __device__ __forceinline__ Part part_of(Group<D> (&g)[kGroups], float c, F f) {
       for (int i = 0; i < D::kVec; ++i) m = fmaxf(m, g[j].get(i));
     }
     m = wave_max_f32(m);
-    s = sum_of<D>(g, m, c, [](float, int, int) {});
+    s = sum_of<D>(g, m, c, [](float, int, int) LP_INLINE {});
   }
   return {m, s};
 }
@@ -483,7 +486,7 @@ __device__ __forceinline__ void write_bad_draw(const SelectArgs& a, int64_t n) {
 }
 
 // A row without a valid draw or list: -1 and NaN.
-__device__ void write_bad_top(const SelectArgs& a, int64_t n) {
+__device__ __forceinline__ void write_bad_top(const SelectArgs& a, int64_t n) {
   for (int i = threadIdx.x; i < a.top_k; i += kThreads) {
     a.out_ids[n * a.top_k + i] = -1;
     a.out_logits[n * a.top_k + i] = NAN;
@@ -551,7 +554,7 @@ __device__ __forceinline__ uint32_t first_index(uint32_t* word, uint32_t n, uint
 
 // The draw from a sorted list that holds every token that can be kept.
 template <class Words>
-__device__ void finish_draw(const SelectArgs& a, const Settings& st, int64_t n, const uint64_t* list,
+__device__ __forceinline__ void finish_draw(const SelectArgs& a, const Settings& st, int64_t n, const uint64_t* list,
                             uint32_t m, const Log2Sum& all, Words& w) {
   constexpr int kEach = kList / kThreads;
   const double tau = (double)st.tau, top = (double)token_logit(list[0]);
@@ -568,7 +571,7 @@ __device__ void finish_draw(const SelectArgs& a, const Settings& st, int64_t n, 
 #pragma unroll
   for (int i = 0; i < kEach; ++i) c[i] += before;
   // The sum through token t (from 0) for every thread.
-  auto mass_through = [&](uint32_t t) {
+  auto mass_through = [&](uint32_t t) LP_INLINE {
 #pragma unroll
     for (int i = 0; i < kEach; ++i)
       if (base + i == t) w.shared_f64 = c[i];
@@ -580,7 +583,7 @@ __device__ void finish_draw(const SelectArgs& a, const Settings& st, int64_t n, 
   uint32_t kept = st.kind == kTopK ? min(st.k, m) : m;
   if (st.kind == kMinP || (st.min_p > 0.0f && !st.greedy)) {
     const double most = fmax(0.0, -log((double)st.min_p));
-    kept = min(kept, st.min_p > 1.0f ? 1u : first_index(&w.found, m, base, kEach, [&](int i) {
+    kept = min(kept, st.min_p > 1.0f ? 1u : first_index(&w.found, m, base, kEach, [&](int i) LP_INLINE {
                  return x[i] > most;
                }));
   }
@@ -588,14 +591,14 @@ __device__ void finish_draw(const SelectArgs& a, const Settings& st, int64_t n, 
     // The nucleus is of what top-k left, whatever min-p drops.
     const double want = (double)st.top_p * mass_through(min(st.k, m) - 1);
     const uint32_t p = want > 0.0 ? first_index(&w.found, m, base, kEach,
-                                                [&](int i) { return c[i] >= want; }) + 1
+                                                [&](int i) LP_INLINE { return c[i] >= want; }) + 1
                                   : 1u;
     kept = min(kept, p);
   }
   const double mass = mass_through(kept - 1);
   const double u = st.greedy ? 0.0 : fmin(fmax((double)st.u, 0.0), 1.0 - 0x1p-24);
   const uint32_t rank =
-      min(kept - 1, first_index(&w.found, kept, base, kEach, [&](int i) { return c[i] > u * mass; }));
+      min(kept - 1, first_index(&w.found, kept, base, kEach, [&](int i) LP_INLINE { return c[i] > u * mass; }));
   if (threadIdx.x == 0) {
     const uint64_t t = list[rank];
     const double s = ((double)token_logit(t) - top) / tau;
@@ -607,7 +610,7 @@ __device__ void finish_draw(const SelectArgs& a, const Settings& st, int64_t n, 
 }
 
 // The first k tokens from a sorted list of m.
-__device__ void finish_top(const SelectArgs& a, int64_t n, const uint64_t* list, uint32_t m,
+__device__ __forceinline__ void finish_top(const SelectArgs& a, int64_t n, const uint64_t* list, uint32_t m,
                            const Log2Sum& all) {
   const float c = scale2_of(a.temperature);
   for (uint32_t i = threadIdx.x; i < (uint32_t)a.top_k; i += kThreads) {
@@ -642,8 +645,7 @@ struct CollectShared {
 // The maximum of the first chunk that has a finite logit (or +inf): the
 // anchor of the buckets. -inf where there is none.
 template <class D>
-__device__ float anchor_of(const Row<D>& row_in, float* words) {
-  const Row<D> row = row_in;
+__device__ __forceinline__ float anchor_of(const Row<D>& row, float* words) {
   float m = -INFINITY;
   for (int c = 0; c < row.chunks() && m == -INFINITY; ++c) {
     Group<D> g[kGroups];
@@ -663,8 +665,7 @@ __device__ float anchor_of(const Row<D>& row_in, float* words) {
 // by the maximum that there are some. No element is skipped: -inf goes to the
 // last bucket and is counted apart.
 template <class D, class S>
-__device__ void collect_buckets(const Row<D>& row_in, S& sh, int c0, int c1) {
-  const Row<D> row = row_in;
+__device__ __forceinline__ void collect_buckets(const Row<D>& row, S& sh, int c0, int c1) {
   for (int i = threadIdx.x; i < kBuckets; i += kThreads) {
     sh.mass[i] = 0;
     sh.cnt[i] = 0;
@@ -674,7 +675,7 @@ __device__ void collect_buckets(const Row<D>& row_in, S& sh, int c0, int c1) {
   float top = -INFINITY;
   uint64_t odd = 0;  // by lane
   uint32_t masked = 0;
-  row.for_chunks(c0, c1, [&](Group<D>(&g)[kGroups], int) {
+  row.for_chunks(c0, c1, [&](Group<D>(&g)[kGroups], int) LP_INLINE {
 #pragma unroll
     for (int j = 0; j < kGroups; ++j)
 #pragma unroll
@@ -743,7 +744,7 @@ __global__ __launch_bounds__(kThreads, 6) void collect_kernel(SelectArgs a) {
   float theta = 0.0f;
   // The list sorted down to what can still be needed; false where it has lost
   // tokens.
-  auto cut = [&](bool always) {
+  auto cut = [&](bool always) LP_INLINE {
     __syncthreads();
     const uint32_t m = sh.n_list;
     __syncthreads();
@@ -758,7 +759,7 @@ __global__ __launch_bounds__(kThreads, 6) void collect_kernel(SelectArgs a) {
       theta = bound(token_logit(sh.list[0]) - depth);
       constexpr int kEach = kList / kThreads;
       keep = first_index(&sh.found, m, tid * kEach, kEach,
-                         [&](int i) { return token_logit(sh.list[tid * kEach + i]) < theta; });
+                         [&](int i) LP_INLINE { return token_logit(sh.list[tid * kEach + i]) < theta; });
     }
     __syncthreads();
     if (tid == 0) sh.n_list = keep;
@@ -766,7 +767,7 @@ __global__ __launch_bounds__(kThreads, 6) void collect_kernel(SelectArgs a) {
     return true;
   };
   // The r-th largest of a wave's values, by taking the largest away r - 1 times.
-  auto rth_largest = [&](float v, uint32_t r) {
+  auto rth_largest = [&](float v, uint32_t r) LP_INLINE {
     float m = wave_max_f32(v);
     for (uint32_t i = 1; i < r; ++i) {
       const uint64_t at = __ballot(v == m);
@@ -778,7 +779,7 @@ __global__ __launch_bounds__(kThreads, 6) void collect_kernel(SelectArgs a) {
   };
 
   bool fits = true;
-  row.for_chunks(c0, c1, [&](Group<D>(&g)[kGroups], int c) {
+  row.for_chunks(c0, c1, [&](Group<D>(&g)[kGroups], int c) LP_INLINE {
     if (!fits) return;
     if (c == c0) {
       float tm = -INFINITY, gm[kGroups];
@@ -822,8 +823,8 @@ __global__ __launch_bounds__(kThreads, 6) void collect_kernel(SelectArgs a) {
       if (tid == 0) sh.n_list = 0;
       __syncthreads();
     }
-    const Part p = part_of<D>(g, scale2, [](float, int, int) {});
-    append<D>(g, Row<D>::index(c, 0, 0), sh.list, &sh.n_list, [&](float z) { return z >= theta; });
+    const Part p = part_of<D>(g, scale2, [](float, int, int) LP_INLINE {});
+    append<D>(g, Row<D>::index(c, 0, 0), sh.list, &sh.n_list, [&](float z) LP_INLINE { return z >= theta; });
     if ((tid & 63) == 0) {
       if (a.slices == 1) sh.parts[c * kWaves + wave] = p;
       else a.parts[(n * chunks + c) * kWaves + wave] = p;
@@ -870,7 +871,7 @@ struct Totals {
 };
 
 template <class D>
-__device__ Totals sum_buckets(Shared& sh) {
+__device__ __forceinline__ Totals sum_buckets(Shared& sh) {
   uint32_t c[kPerThread], cs = 0;
   double m[kPerThread], ms = 0.0;
 #pragma unroll
@@ -905,7 +906,7 @@ __device__ Totals sum_buckets(Shared& sh) {
 // The buckets of a row: `anchor` and zmax set, `ready` where counts, masses
 // and facts are collected already. False for a row without a draw.
 template <class D>
-__device__ bool fill_buckets(Row<D>& row, Shared& sh, bool ready, Totals* all) {
+__device__ __forceinline__ bool fill_buckets(Row<D>& row, Shared& sh, bool ready, Totals* all) {
   if (!ready) collect_buckets(row, sh, 0, row.chunks());
   row.zmax = key_value(sh.facts.top);
   if (sh.facts.odd || row.zmax == -INFINITY) return false;
@@ -922,8 +923,7 @@ __device__ bool fill_buckets(Row<D>& row, Shared& sh, bool ready, Totals* all) {
 // Least logit whose bucket is at most b0 .. b3, by wave 0 .. 3 into sh.least
 // (+inf where the maximum's bucket is beyond): a search over the finite keys, 64 at a time.
 template <class D>
-__device__ void least_logits(const Row<D>& row_in, Shared& sh, int b0, int b1, int b2, int b3) {
-  const Row<D> row = row_in;
+__device__ __forceinline__ void least_logits(const Row<D>& row, Shared& sh, int b0, int b1, int b2, int b3) {
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   __syncthreads();
   if (wave < 4) {
@@ -948,14 +948,13 @@ __device__ void least_logits(const Row<D>& row_in, Shared& sh, int b0, int b1, i
 // Tokens with lo0 <= z < hi0 or lo1 <= z < hi1 appended to the list, in any
 // order; returns their number (which may pass the list's size).
 template <class D>
-__device__ uint32_t gather(const Row<D>& row_in, Shared& sh, float lo0, float hi0, float lo1,
+__device__ __forceinline__ uint32_t gather(const Row<D>& row, Shared& sh, float lo0, float hi0, float lo1,
                            float hi1) {
-  const Row<D> row = row_in;
   __syncthreads();
   if (threadIdx.x == 0) sh.n_list = 0;
   __syncthreads();
-  row.for_chunks(0, row.chunks(), [&](Group<D>(&g)[kGroups], int c) {
-    append<D>(g, Row<D>::index(c, 0, 0), sh.list, &sh.n_list, [&](float z) {
+  row.for_chunks(0, row.chunks(), [&](Group<D>(&g)[kGroups], int c) LP_INLINE {
+    append<D>(g, Row<D>::index(c, 0, 0), sh.list, &sh.n_list, [&](float z) LP_INLINE {
       return (z >= lo0 && z < hi0) || (z >= lo1 && z < hi1);
     });
   });
@@ -985,13 +984,12 @@ struct Listed {
 //   kByMassOver: the mass through it is > want.
 // Where no token's mass gets there (want is rounded), the last one.
 template <class D>
-__device__ Found select_in_bucket(const Row<D>& row_in, Shared& sh, Listed& listed, int b, Mode mode,
+__device__ __forceinline__ Found select_in_bucket(const Row<D>& row, Shared& sh, Listed& listed, int b, Mode mode,
                                   uint32_t rank, double want) {
-  const Row<D> row = row_in;
   uint32_t count = sh.cnt[b + 1] - sh.cnt[b];
   uint32_t base_cnt = 0, at = 0, m = count;
   unsigned long long base_mass = 0;
-  auto reached = [&](uint32_t c, unsigned long long s) {
+  auto reached = [&](uint32_t c, unsigned long long s) LP_INLINE {
     return mode == kByRank ? c >= rank : (mode == kByMass ? (double)s >= want : (double)s > want);
   };
   if (b >= listed.lo0 && b <= listed.hi0) {
@@ -1019,7 +1017,7 @@ __device__ Found select_in_bucket(const Row<D>& row_in, Shared& sh, Listed& list
           sh.fcnt[i] = 0;
         }
         __syncthreads();
-        row.for_each([&](float z, int idx) {
+        row.for_each([&](float z, int idx) LP_INLINE {
           const uint64_t k = token_key(z, idx);
           if (k >= lo && k <= hi) {
             const uint32_t f = (uint32_t)((hi - k) >> shift);
@@ -1067,7 +1065,7 @@ __device__ Found select_in_bucket(const Row<D>& row_in, Shared& sh, Listed& list
       }
       if (threadIdx.x == 0) sh.n_list = 0;
       __syncthreads();
-      row.for_each([&](float z, int idx) {
+      row.for_each([&](float z, int idx) LP_INLINE {
         const uint64_t k = token_key(z, idx);
         if (k >= lo && k <= hi) {
           const uint32_t s = atomicAdd(&sh.n_list, 1u);
@@ -1166,9 +1164,8 @@ __device__ __forceinline__ int bucket_of_mass(Shared& sh, double want, bool over
 
 // A draw from filled buckets.
 template <class D>
-__device__ void draw_from_buckets(const SelectArgs& a, const Settings& st, int64_t n,
-                                  const Row<D>& row_in, const Totals& all, Shared& sh) {
-  const Row<D> row = row_in;
+__device__ __forceinline__ void draw_from_buckets(const SelectArgs& a, const Settings& st, int64_t n,
+                                  const Row<D>& row, const Totals& all, Shared& sh) {
   const double tau = (double)st.tau;
   const double u = fmin(fmax((double)st.u, 0.0), 1.0 - 0x1p-24);
   Listed listed;
@@ -1232,7 +1229,7 @@ __device__ void draw_from_buckets(const SelectArgs& a, const Settings& st, int64
     if (sh.cnt[b0] < kept) {
       uint32_t c[3] = {0, 0, 0};
       unsigned long long w[3] = {0, 0, 0};
-      row.for_each([&](float z, int) {
+      row.for_each([&](float z, int) LP_INLINE {
         const double x = row.x_of(z);
         const int d = (int)Row<D>::bucket(x) - b0;
         if (z != -INFINITY && d >= 0 && d <= b1 - b0 &&
@@ -1281,11 +1278,10 @@ __device__ void draw_from_buckets(const SelectArgs& a, const Settings& st, int64
 // The parts of a row as collect_kernel forms them, into sh.parts; returns
 // their number.
 template <class D>
-__device__ int parts_of_row(const Row<D>& row_in, float tau, Shared& sh) {
-  const Row<D> row = row_in;
+__device__ __forceinline__ int parts_of_row(const Row<D>& row, float tau, Shared& sh) {
   const float scale2 = scale2_of(tau);
-  row.for_chunks(0, row.chunks(), [&](Group<D>(&g)[kGroups], int c) {
-    const Part p = part_of<D>(g, scale2, [](float, int, int) {});
+  row.for_chunks(0, row.chunks(), [&](Group<D>(&g)[kGroups], int c) LP_INLINE {
+    const Part p = part_of<D>(g, scale2, [](float, int, int) LP_INLINE {});
     if ((threadIdx.x & 63) == 0) sh.parts[c * kWaves + (threadIdx.x >> 6)] = p;
   });
   __syncthreads();
@@ -1293,10 +1289,9 @@ __device__ int parts_of_row(const Row<D>& row_in, float tau, Shared& sh) {
 }
 
 template <class D>
-__device__ float max_of(const Row<D>& row_in, Shared& sh) {
-  const Row<D> row = row_in;
+__device__ __forceinline__ float max_of(const Row<D>& row, Shared& sh) {
   float m = -INFINITY;
-  row.for_each([&](float z, int) { m = fmaxf(m, z); });
+  row.for_each([&](float z, int) LP_INLINE { m = fmaxf(m, z); });
   return block_max(m, sh.wave_f32);
 }
 
@@ -1304,8 +1299,8 @@ __device__ float max_of(const Row<D>& row_in, Shared& sh) {
 // then the same ending, so that its results do not depend on how the row was
 // cut. A row where min-p leaves more than kListMax goes by buckets for good.
 template <class D, bool kTop>
-__device__ void list_by_buckets(const SelectArgs& a, const Settings& st, int64_t n, Row<D>& row,
-                                Shared& sh) {
+__device__ __noinline__ void list_by_buckets(SelectArgs a, Settings st, int64_t n, Row<D> row,
+                                             Shared& sh) {
   const int parts = parts_of_row(row, st.tau, sh);
   const Log2Sum log2_all = join_parts(sh.parts, parts, scale2_of(st.tau), sh.wave_f64);
   if (!isfinite(log2_all.rest)) {
@@ -1346,7 +1341,7 @@ __device__ void list_by_buckets(const SelectArgs& a, const Settings& st, int64_t
         select_in_bucket(row, sh, none, b, kByRank, want - sh.cnt[b], 0.0).key;
     if (threadIdx.x == 0) sh.n_list = 0;
     __syncthreads();
-    row.for_each([&](float z, int idx) {
+    row.for_each([&](float z, int idx) LP_INLINE {
       const uint64_t k = token_key(z, idx);
       if (k >= last && z != -INFINITY) {
         const uint32_t s = atomicAdd(&sh.n_list, 1u);
@@ -1364,7 +1359,7 @@ __device__ void list_by_buckets(const SelectArgs& a, const Settings& st, int64_t
 
 // One row: its slices' lists or buckets joined, or the whole of it.
 template <class D, bool kTop>
-__device__ void finish_row(const SelectArgs& a, int64_t n, Shared& sh) {
+__device__ __forceinline__ void finish_row(const SelectArgs& a, int64_t n, Shared& sh) {
   const Settings st = settings_of(a, n);
   Row<D> row;
   row.p = static_cast<const typename D::Raw*>(a.logits) + n * a.ld;
@@ -1429,7 +1424,7 @@ __device__ void finish_row(const SelectArgs& a, int64_t n, Shared& sh) {
     const uint32_t base = threadIdx.x * kEach;
     const float theta = m > 0 ? bound(token_logit(sh.list[0]) - depth_of(st)) : 0.0f;
     m = first_index(&sh.found, m, base, kEach,
-                    [&](int i) { return token_logit(sh.list[base + i]) < theta; });
+                    [&](int i) LP_INLINE { return token_logit(sh.list[base + i]) < theta; });
     if (m > (uint32_t)kListMax) {
       list_by_buckets<D, kTop>(a, st, n, row, sh);
       return;
@@ -1487,7 +1482,7 @@ SelectWorkspace select_workspace_layout(int64_t N, int64_t V, int32_t dtype) {
   const int slices = select_slices(N, V, dtype);
   const size_t lists = (size_t)N * (size_t)slices;
   const size_t cut = slices > 1 ? 1 : 0;  // what only cut rows need
-  auto up = [](size_t b) { return (b + 255) / 256 * 256; };
+  auto up = [](size_t b) LP_INLINE { return (b + 255) / 256 * 256; };
   SelectWorkspace w;
   w.off_counts = 0;
   w.off_parts = up(lists * sizeof(uint32_t));
