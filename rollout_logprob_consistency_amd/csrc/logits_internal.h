@@ -95,7 +95,9 @@ __device__ __forceinline__ Group<D> load_whole(const typename D::Raw* p) {
 template <class D>
 __device__ __forceinline__ Group<D> load_group(const typename D::Raw* p, int64_t i, int64_t end) {
   if (i + D::kVec <= end) return load_whole<D>(p + i);
-  Group<D> g = {{0, 0, 0, 0}};
+  constexpr uint32_t kFill = D::kVec == 4 ? (uint32_t)D::kNegInf : D::kNegInf * 0x10001u;
+  Group<D> g = {{kFill, kFill, kFill, kFill}};
+  if (i >= end) return g;
   const Global<const typename D::Raw> q = (Global<const typename D::Raw>)p;
 #pragma unroll
   for (int j = 0; j < D::kVec; ++j) g.set(j, i + j < end ? q[i + j] : D::kNegInf);

@@ -39,6 +39,8 @@ constexpr double kPerNat = 32.0;
 constexpr double kHead = 768.0;       // the anchor's place: 24 nats from the top
 constexpr int kPerThread = kBuckets / kThreads;
 constexpr int kList = 4096;           // tokens listed at once
+constexpr int kShort = 2048;          // ... by a workgroup of collect_kernel
+constexpr int kShortTop = 512;        // largest top_k that goes by short lists
 constexpr int kListMax = LP_TOP_MAX;  // tokens that a slice leaves
 constexpr int kMaxSlices = 512;       // of a row
 constexpr uint32_t kOverflow = 0xFFFFFFFFu;    // a slice's count: take the buckets
@@ -391,37 +393,51 @@ __device__ __forceinline__ Part part_of(Group<D> (&g)[kGroups], float c, F f) {
   return {m, s};
 }
 
-// Tokens that hit(z) appended to the list, in any order. The lanes' hits of up
-// to 16 places are gathered as masks first, so that a wave asks for its places
-// in the list once and not per hit.
-template <class D, class F>
-__device__ __forceinline__ void append(const Group<D> (&g)[kGroups], int index0, uint64_t* list,
-                                       uint32_t* n_list, F hit) {
-  constexpr int kBatch = 16 / D::kVec;  // groups
+// Which lanes' logits of a chunk are wanted, place by place, and in which
+// blocks of eight places there are any.
+template <class D>
+struct Hits {
+  static constexpr int kPlaces = kGroups * D::kVec, kBlocks = kPlaces / 8;
+  uint64_t masks[kPlaces], any[kBlocks];
+
+  __device__ __forceinline__ void set(int e, bool hit) {
+    masks[e] = __ballot(hit);
+    any[e / 8] = e % 8 == 0 ? masks[e] : any[e / 8] | masks[e];
+  }
+};
+
+// These tokens appended to the list, in any order. A wave asks for its places
+// in the list once a chunk, and passes over blocks without a hit.
+template <class D>
+__device__ __forceinline__ void append(const Group<D> (&g)[kGroups], const Hits<D>& hits,
+                                       int index0, uint64_t* list, uint32_t size,
+                                       uint32_t* n_list) {
+  uint64_t all = 0;
 #pragma unroll
-  for (int j0 = 0; j0 < kGroups; j0 += kBatch) {
-    uint64_t masks[16], any = 0;
+  for (int k = 0; k < Hits<D>::kBlocks; ++k) all |= hits.any[k];
+  if (all == 0) return;
+  uint32_t total = 0;
 #pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      masks[e] = __ballot(hit(g[j0 + e / D::kVec].get(e % D::kVec)));
-      any |= masks[e];
-    }
-    if (any == 0) continue;
-    uint32_t total = 0;
+  for (int k = 0; k < Hits<D>::kBlocks; ++k)
+    if (hits.any[k])
 #pragma unroll
-    for (int e = 0; e < 16; ++e) total += (uint32_t)__popcll(masks[e]);
-    uint32_t at = 0;
-    if ((threadIdx.x & 63) == 0) at = atomicAdd(n_list, total);
-    at = __builtin_amdgcn_readfirstlane(at);
+      for (int e = k * 8; e < k * 8 + 8; ++e) total += (uint32_t)__popcll(hits.masks[e]);
+  uint32_t at = 0;
+  if ((threadIdx.x & 63) == 0) at = atomicAdd(n_list, total);
+  at = __builtin_amdgcn_readfirstlane(at);
 #pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      if (masks[e] == 0) continue;
-      const uint32_t to = at + lanes_below(masks[e]);
-      if ((masks[e] >> (threadIdx.x & 63) & 1) && to < (uint32_t)kList) {
-        const int j = j0 + e / D::kVec, i = e % D::kVec;
+  for (int k = 0; k < Hits<D>::kBlocks; ++k) {
+    if (hits.any[k] == 0) continue;
+#pragma unroll
+    for (int e = k * 8; e < k * 8 + 8; ++e) {
+      const uint64_t mask = hits.masks[e];
+      if (mask == 0) continue;
+      const uint32_t to = at + lanes_below(mask);
+      if ((mask >> (threadIdx.x & 63) & 1) && to < size) {
+        const int j = e / D::kVec, i = e % D::kVec;
         list[to] = token_key(g[j].get(i), index0 + j * kThreads * D::kVec + i);
       }
-      at += (uint32_t)__popcll(masks[e]);
+      at += (uint32_t)__popcll(mask);
     }
   }
 }
@@ -453,7 +469,7 @@ __device__ __forceinline__ Settings settings_of(const SelectArgs& a, int64_t n) 
   s.k = s.greedy ? 1u : (uint32_t)max(s.top_k, 0);
   s.kind = kBuckets_;
   if (!s.bad && isfinite(s.tau)) {
-    if (s.greedy || (s.top_k > 0 && s.top_k <= kListMax)) s.kind = kTopK;
+    if (s.greedy || (s.top_k > 0 && s.top_k <= kShortTop)) s.kind = kTopK;
     else if (s.top_k <= 0 && s.top_p >= 1.0f && s.min_p > 0.0f && s.min_p <= 1.0f) s.kind = kMinP;
   }
   return s;
@@ -556,7 +572,8 @@ __device__ __forceinline__ uint32_t first_index(uint32_t* word, uint32_t n, uint
 template <class Words>
 __device__ __forceinline__ void finish_draw(const SelectArgs& a, const Settings& st, int64_t n, const uint64_t* list,
                             uint32_t m, const Log2Sum& all, Words& w) {
-  constexpr int kEach = kList / kThreads;
+  // Lists are no longer than kListMax here.
+  constexpr int kEach = kListMax / kThreads;
   const double tau = (double)st.tau, top = (double)token_logit(list[0]);
   const uint32_t base = threadIdx.x * kEach;
   double x[kEach], c[kEach], sum = 0.0;  // -ln weight; sums through each token
@@ -627,7 +644,7 @@ __device__ __forceinline__ void finish_top(const SelectArgs& a, int64_t n, const
 
 struct CollectShared {
   union {
-    uint64_t list[kList];
+    uint64_t list[kShort];
     struct {  // a slice's buckets
       unsigned long long mass[kBuckets];
       uint32_t cnt[kBuckets];
@@ -742,45 +759,25 @@ __global__ __launch_bounds__(kThreads, 6) void collect_kernel(SelectArgs a) {
   // Tokens from theta on enter the list. theta is a logit that k tokens reach
   // (kTopK), or the depth below one (kMinP); never below the finite ones.
   float theta = 0.0f;
-  // The list sorted down to what can still be needed; false where it has lost
-  // tokens.
-  auto cut = [&](bool always) LP_INLINE {
-    __syncthreads();
-    const uint32_t m = sh.n_list;
-    __syncthreads();
-    if (m > (uint32_t)kList) return false;
-    if (!always && m < (st.kind == kTopK ? 2 * st.k + 64 : 1024u)) return true;
-    sort_list(sh.list, m);
-    uint32_t keep = m;
-    if (st.kind == kTopK) {
-      keep = min(m, st.k);
-      if (m >= st.k) theta = token_logit(sh.list[st.k - 1]);
-    } else if (m > 0) {
-      theta = bound(token_logit(sh.list[0]) - depth);
-      constexpr int kEach = kList / kThreads;
-      keep = first_index(&sh.found, m, tid * kEach, kEach,
-                         [&](int i) LP_INLINE { return token_logit(sh.list[tid * kEach + i]) < theta; });
-    }
-    __syncthreads();
-    if (tid == 0) sh.n_list = keep;
-    __syncthreads();
-    return true;
-  };
   // The r-th largest of a wave's values, by taking the largest away r - 1 times.
   auto rth_largest = [&](float v, uint32_t r) LP_INLINE {
     float m = wave_max_f32(v);
     for (uint32_t i = 1; i < r; ++i) {
       const uint64_t at = __ballot(v == m);
-      if (at == 0) break;  // nothing but masked tokens is left
       if ((tid & 63) == __ffsll((long long)at) - 1) v = -INFINITY;
       m = wave_max_f32(v);
     }
     return m;
   };
 
-  bool fits = true;
-  row.for_chunks(c0, c1, [&](Group<D>(&g)[kGroups], int c) LP_INLINE {
-    if (!fits) return;
+  // Loads are not taken ahead: with 64 registers four workgroups of 8 waves
+  // share a CU, and their loads overlap each other's arithmetic (with the next
+  // chunk in registers and two or three workgroups, 2 304 rows of 151 936 took
+  // FIGURE).
+  bool fits = !kTop || st.k <= (uint32_t)kShortTop;
+  for (int c = c0; c < c1 && fits; ++c) {
+    Group<D> g[kGroups];
+    row.load(g, c);
     if (c == c0) {
       float tm = -INFINITY, gm[kGroups];
 #pragma unroll
@@ -790,50 +787,61 @@ __global__ __launch_bounds__(kThreads, 6) void collect_kernel(SelectArgs a) {
         for (int i = 0; i < D::kVec; ++i) gm[j] = fmaxf(gm[j], g[j].get(i));
         tm = fmaxf(tm, gm[j]);
       }
-      // A first theta: with r = ceil(k / 8), the least of the eight waves'
-      // r-th largest thread maximum is reached by k tokens of this chunk
-      // (with more than 256 wanted, of the four groups' maxima apart).
       if (st.kind == kTopK) {
-        const bool fine = st.k > 256;
-        float t;
-        if (fine) {
+        // A first theta: with r = ceil(k / 8), the least of the eight waves'
+        // r-th largest thread maximum is reached by k tokens of this chunk
+        // (with more than 256 wanted, of the four groups' maxima apart).
+        if (st.k > 256) {
           const uint32_t r = (st.k + 4 * kWaves - 1) / (4 * kWaves);
-          t = rth_largest(gm[0], r);
+          tm = rth_largest(gm[0], r);
 #pragma unroll
-          for (int j = 1; j < kGroups; ++j) t = fminf(t, rth_largest(gm[j], r));
+          for (int j = 1; j < kGroups; ++j) tm = fminf(tm, rth_largest(gm[j], r));
         } else {
-          t = rth_largest(tm, (st.k + kWaves - 1) / kWaves);
+          tm = rth_largest(tm, (st.k + kWaves - 1) / kWaves);
         }
-        theta = -block_max(-t, sh.wave_f32);
-        if (theta == -INFINITY) {  // a wave with too few: the k-th largest of all of them
-          if (fine) {
-#pragma unroll
-            for (int j = 0; j < kGroups; ++j) sh.list[j * kThreads + tid] = token_key(gm[j], 0);
-          } else {
-            sh.list[tid] = token_key(tm, 0);
-          }
-          sort_list(sh.list, fine ? kGroups * kThreads : kThreads);
-          theta = token_logit(sh.list[st.k - 1]);
-          __syncthreads();
-        }
-        theta = bound(theta);
+        theta = bound(-block_max(-tm, sh.wave_f32));
       } else {
         theta = bound(block_max(tm, sh.wave_f32) - depth);
       }
       if (tid == 0) sh.n_list = 0;
       __syncthreads();
     }
-    const Part p = part_of<D>(g, scale2, [](float, int, int) LP_INLINE {});
-    append<D>(g, Row<D>::index(c, 0, 0), sh.list, &sh.n_list, [&](float z) LP_INLINE { return z >= theta; });
+    Hits<D> hits;
+    const Part p = part_of<D>(g, scale2, [&](float z, int j, int i) LP_INLINE {
+      hits.set(j * D::kVec + i, z >= theta);
+    });
+    append<D>(g, hits, Row<D>::index(c, 0, 0), sh.list, kShort, &sh.n_list);
     if ((tid & 63) == 0) {
       if (a.slices == 1) sh.parts[c * kWaves + wave] = p;
       else a.parts[(n * chunks + c) * kWaves + wave] = p;
     }
-    // Cut after the 1st, 2nd, 4th, 8th, ... chunk, where a list has doubled.
+    // After the 1st, 2nd, 4th, 8th, ... chunk, where a list has doubled, and
+    // the last one: a list that has grown is sorted down to what can still be
+    // needed. One that has lost tokens is given up.
     const int done = c - c0 + 1;
-    if (c + 1 < c1 && (done & (done - 1)) == 0) fits = cut(false);
-  });
-  fits = fits && cut(true);
+    const bool last = c + 1 == c1;
+    if (!last && (done & (done - 1)) != 0) continue;
+    __syncthreads();
+    const uint32_t m = sh.n_list;
+    __syncthreads();
+    fits = m <= (uint32_t)kShort;
+    if (!fits || (!last && m < (st.kind == kTopK ? 2 * st.k + 128 : 1024u))) continue;
+    sort_list(sh.list, m);
+    uint32_t keep = m;
+    if (st.kind == kTopK) {
+      keep = min(m, st.k);
+      if (m >= st.k) theta = token_logit(sh.list[st.k - 1]);
+    } else if (m > 0) {
+      theta = bound(token_logit(sh.list[0]) - depth);
+      constexpr int kEach = kShort / kThreads;
+      keep = first_index(&sh.found, m, tid * kEach, kEach, [&](int i) LP_INLINE {
+        return token_logit(sh.list[tid * kEach + i]) < theta;
+      });
+    }
+    __syncthreads();
+    if (tid == 0) sh.n_list = keep;
+    __syncthreads();
+  }
   const uint32_t m = fits ? sh.n_list : 0;
   if (!fits || m > (uint32_t)kListMax) {
     if (tid == 0) count[slice] = kOverflow;
@@ -954,9 +962,13 @@ __device__ __forceinline__ uint32_t gather(const Row<D>& row, Shared& sh, float 
   if (threadIdx.x == 0) sh.n_list = 0;
   __syncthreads();
   row.for_chunks(0, row.chunks(), [&](Group<D>(&g)[kGroups], int c) LP_INLINE {
-    append<D>(g, Row<D>::index(c, 0, 0), sh.list, &sh.n_list, [&](float z) LP_INLINE {
-      return (z >= lo0 && z < hi0) || (z >= lo1 && z < hi1);
-    });
+    Hits<D> hits;
+#pragma unroll
+    for (int e = 0; e < Hits<D>::kPlaces; ++e) {
+      const float z = g[e / D::kVec].get(e % D::kVec);
+      hits.set(e, (z >= lo0 && z < hi0) || (z >= lo1 && z < hi1));
+    }
+    append<D>(g, hits, Row<D>::index(c, 0, 0), sh.list, kList, &sh.n_list);
   });
   __syncthreads();
   return sh.n_list;
@@ -1448,6 +1460,27 @@ __global__ __launch_bounds__(kThreads, 4) void row_kernel(SelectArgs a) {
   finish_row<D, kTop>(a, blockIdx.x, sh);
 }
 
+// The rows of the top logits whose list overflowed, where collect_kernel has
+// finished all others (a.slices == 1): kCheckRows rows a workgroup.
+constexpr int kCheckRows = 8;
+template <class D>
+__global__ __launch_bounds__(kThreads, 4) void overflow_kernel(SelectArgs a) {
+  __shared__ Shared sh;
+  const int64_t n0 = (int64_t)blockIdx.x * kCheckRows;
+  const int64_t mine = n0 + (threadIdx.x & 63);
+  uint64_t over = __ballot((threadIdx.x & 63) < kCheckRows && mine < a.N &&
+                           read_global(a.counts, min(mine, a.N - 1)) == kOverflow);
+  while (over) {
+    const int64_t n = n0 + __ffsll((long long)over) - 1;
+    over &= over - 1;
+    Row<D> row;
+    row.p = static_cast<const typename D::Raw*>(a.logits) + n * a.ld;
+    row.V = a.V;
+    list_by_buckets<D, true>(a, settings_of(a, n), n, row, sh);
+    __syncthreads();
+  }
+}
+
 template <class D, bool kTop>
 hipError_t launch(const SelectArgs& a, bool lists, bool buckets, hipStream_t stream) {
   hipError_t e;
@@ -1462,7 +1495,11 @@ hipError_t launch(const SelectArgs& a, bool lists, bool buckets, hipStream_t str
     collect_kernel<D, kTop><<<dim3((uint32_t)(a.N * a.slices)), kThreads, 0, stream>>>(a);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
-  row_kernel<D, kTop><<<dim3((uint32_t)a.N), kThreads, 0, stream>>>(a);
+  if (kTop && a.slices == 1)
+    overflow_kernel<D><<<dim3((uint32_t)((a.N + kCheckRows - 1) / kCheckRows)), kThreads, 0,
+                         stream>>>(a);
+  else
+    row_kernel<D, kTop><<<dim3((uint32_t)a.N), kThreads, 0, stream>>>(a);
   return hipGetLastError();
 }
 
@@ -1506,7 +1543,7 @@ hipError_t launch_select(SelectArgs a, void* workspace, hipStream_t stream) {
   const bool top = a.u == nullptr;
   // Which ways the rows can take, as far as the host sees the settings.
   const bool seen = !a.temperatures && !a.top_ks && !a.top_ps && !a.min_ps;
-  const bool short_list = a.temperature == 0.0f || (a.top_k > 0 && a.top_k <= kListMax) ||
+  const bool short_list = a.temperature == 0.0f || (a.top_k > 0 && a.top_k <= kShortTop) ||
                           (a.top_k <= 0 && a.top_p >= 1.0f && a.min_p > 0.0f && a.min_p <= 1.0f);
   const bool lists = top || !seen || short_list;
   const bool buckets = !top && (!seen || !short_list);
