@@ -311,25 +311,6 @@ __device__ __forceinline__ void sort_list(uint64_t* list, uint32_t m) {
   }
 }
 
-__device__ __forceinline__ float wave_max_f32(float m) {
-  m = fmaxf(m, __int_as_float(xlane<1>(__float_as_int(m))));
-  m = fmaxf(m, __int_as_float(xlane<2>(__float_as_int(m))));
-  m = fmaxf(m, __int_as_float(xlane<4>(__float_as_int(m))));
-  m = fmaxf(m, __int_as_float(xlane<8>(__float_as_int(m))));
-  m = fmaxf(m, __int_as_float(xlane<16>(__float_as_int(m))));
-  return fmaxf(__int_as_float(lane_value(__float_as_int(m), 0)),
-               __int_as_float(lane_value(__float_as_int(m), 32)));
-}
-__device__ __forceinline__ float wave_sum_f32(float s) {
-  s += __int_as_float(xlane<1>(__float_as_int(s)));
-  s += __int_as_float(xlane<2>(__float_as_int(s)));
-  s += __int_as_float(xlane<4>(__float_as_int(s)));
-  s += __int_as_float(xlane<8>(__float_as_int(s)));
-  s += __int_as_float(xlane<16>(__float_as_int(s)));
-  return __int_as_float(lane_value(__float_as_int(s), 0)) +
-         __int_as_float(lane_value(__float_as_int(s), 32));
-}
-
 // The log2 offset that a part of base m counts from: the integer next to m c
 // where that is small enough to be one, else m c itself. c = log2(e) / tau as
 // a float; it stands for the temperature wherever parts are used, so that its

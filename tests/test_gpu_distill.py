@@ -54,7 +54,7 @@ def compare(z, ids, x, tau, renorm, loss, grad=None, weight=None, dtype="fp32"):
     assert np.array_equal(loss[inf], r_loss[inf])
     ok = np.isfinite(r_loss)
     tol = S_ERR * q + 2.0 ** -24 * np.abs(r_loss) + 1e-12
-    err = np.abs(loss - r_loss)
+    err = np.abs(np.where(inf, 0.0, loss) - np.where(inf, 0.0, r_loss))
     print("loss error / tolerance", np.max((err / tol)[ok], initial=0.0))
     assert np.all(err[ok] <= tol[ok])
     if grad is None:
@@ -240,6 +240,47 @@ def test_batch_invariance_and_alignment():
     for i in (0, 13, 39):
         l1, g1 = lp.distill_step(t2[i:i + 1], di[i:i + 1], dx[i:i + 1], w[i:i + 1])
         assert torch.equal(loss[i:i + 1], l1) and torch.equal(grad[i:i + 1], g1)
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16", "fp16"])
+@pytest.mark.parametrize("v,pad,lead", [(5, 0, 0), (4099, 5, 1), (40007, 0, 3)])
+def test_many_rows_give_the_bits_of_few(dtype, v, pad, lead):
+    """300 rows (one workgroup each) and the same rows in batches of 100
+    (slices): forward, backward and step, also over the logits' own buffer."""
+    T = 300
+    t, z = rows(17, T, v, dtype, pad=pad, lead=lead, masked=0.1)
+    z[5] = -np.inf
+    z[6, v // 2] = np.nan
+    t, z = place(z, dtype, pad, lead)
+    ids, x = teacher(5, z, min(v, 70))
+    ids[7] = -1
+    ids[8, 0] = v
+    ids[9, :] = ids[9, 0]
+    w = np.random.default_rng(3).normal(size=T).astype(np.float32)
+    w[10:40] = 0
+    di, dx, dw = dev(ids, torch.int64), dev(x, torch.float32), dev(w, torch.float32)
+    vt = max(1, v - 3)
+    di[di >= vt] = -1
+    bad, bad2 = (torch.zeros(1, dtype=torch.int32, device=DEV) for _ in range(2))
+    loss, state = lp.distill_forward(t, di, dx, v_true=vt, bad_rows=bad)
+    grad = lp.distill_backward(t, di, dx, state, dw, v_true=vt)
+    loss2, grad2 = lp.distill_step(t, di, dx, dw, v_true=vt, bad_rows=bad2)
+    parts = []
+    for a in range(0, T, 100):
+        b = slice(a, a + 100)
+        parts.append(lp.distill_step(t[b], di[b], dx[b], dw[b], v_true=vt))
+    loss3, grad3 = (torch.cat(p) for p in zip(*parts))
+    loss4, grad4 = lp.distill_step(t, di, dx, dw, v_true=vt, out=t)
+    assert grad4.data_ptr() == t.data_ptr() and torch.equal(bad, bad2)
+
+    def same(a, b):
+        return torch.equal(a.contiguous().view(torch.uint8), b.contiguous().view(torch.uint8))
+    for other in (loss2, loss3, loss4):
+        assert torch.equal(loss.nan_to_num(-9.0), other.nan_to_num(-9.0))
+    for other in (grad2, grad3, grad4):
+        assert torch.equal(grad.isnan(), other.isnan())
+        assert same(grad.nan_to_num(0.0), other.nan_to_num(0.0))
+    assert not grad[:, vt:].any() and not grad[10:40].any()
 
 
 def test_many_rows():
