@@ -204,7 +204,15 @@ hipError_t launch_distill_step(const DistillArgs& a, hipStream_t stream);
 
 constexpr int kSelectThreads = 512;
 
-// A wave's maximum m and sum of exp((z - m) / tau) over its part of a chunk.
+// What the buckets of a row, or of a slice of it, hold besides counts and masses.
+struct RowFacts {
+  uint32_t top;     // key of the largest logit
+  uint32_t odd;     // a NaN or +inf is there
+  uint32_t masked;  // -inf logits (in the last bucket's count), fill included
+  uint32_t unused;
+};
+
+// A base m and the sum of 2^(z c - offset(m)) over a wave's part of a chunk.
 struct SelectPart {
   float m, s;
 };
@@ -237,13 +245,14 @@ struct SelectArgs {
   uint32_t* counts;        // [N][slices] listed tokens
   SelectPart* parts;       // [N][chunks][waves], where slices > 1
   uint64_t* keys;          // [N][slices][LP_TOP_MAX], where slices > 1
-  unsigned long long* masses;  // [N][buckets], where slices > 1; then, behind them,
-  uint32_t* bucket_counts;     // [N][buckets + 4]: counts and the row's facts
-  size_t bucket_bytes;         // of both
+  // Of a slice that goes by buckets, where slices > 1.
+  unsigned long long* masses;  // [N][slices][buckets]
+  uint32_t* bucket_counts;     // [N][slices][buckets]
+  RowFacts* facts;             // [N][slices]
 };
 
 struct SelectWorkspace {
-  size_t off_counts, off_parts, off_keys, off_masses, off_bucket_counts, total;
+  size_t off_counts, off_parts, off_keys, off_masses, off_bucket_counts, off_facts, total;
 };
 SelectWorkspace select_workspace_layout(int64_t N, int64_t V, int32_t dtype);
 

@@ -72,13 +72,6 @@ __device__ __forceinline__ float token_logit(uint64_t k) { return key_value((uin
 constexpr uint32_t kKeyNegInf = 0x007FFFFFu;  // key_of(-inf)
 
 
-// What the buckets of a row hold besides counts and masses.
-struct RowFacts {
-  uint32_t top;     // key of the largest logit
-  uint32_t odd;     // a NaN or +inf is there
-  uint32_t masked;  // -inf logits (in the last bucket's count), fill included
-};
-
 struct Shared {
   // Buckets: counts and masses while they are collected, then exclusive
   // prefix sums (masses as doubles in units of the anchor's weight).
@@ -320,48 +313,37 @@ __device__ __forceinline__ double offset_of(float m, float c) {
   return near_offset(m, c) ? (double)rintf(m * c) : (double)m * (double)c;
 }
 
-// Sum over a wave's groups of 2^(z c - offset(m)), f(z, j, i) seeing every logit.
-template <class D, class F>
-__device__ __forceinline__ float sum_of(Group<D> (&g)[kGroups], float m, float c, F f) {
-  float s = 0.0f;
-  if (near_offset(m, c)) {
-    const float b = rintf(m * c);
-#pragma unroll
-    for (int j = 0; j < kGroups; ++j) {
-      g[j].fresh();
-#pragma unroll
-      for (int i = 0; i < D::kVec; ++i) {
-        const float z = g[j].get(i);
-        s += __builtin_amdgcn_exp2f(fmaf(z, c, -b));
-        f(z, j, i);
-      }
-    }
-  } else {
-    const float base = m == -INFINITY ? 0.0f : m;  // masked tokens sum to 0, a NaN stays one
-#pragma unroll
-    for (int j = 0; j < kGroups; ++j)
-#pragma unroll
-      for (int i = 0; i < D::kVec; ++i) {
-        const float z = g[j].get(i);
-        s += __builtin_amdgcn_exp2f((z - base) * c);
-        f(z, j, i);
-      }
-  }
-  return wave_sum_f32(s);
-}
+// A chunk is gone through in blocks of eight places.
+template <class D>
+constexpr int kBlocks = kGroups * D::kVec / 8;
 
 // The part of a wave whose lanes hold these groups: the same terms in the same
 // order wherever it is formed. Its base is the maximum of the first groups
-// alone, which spares most of a pass; where a sum gets out of 2^32, or is none,
-// it is formed again from the maximum of all.
-template <class D, class F>
-__device__ __forceinline__ Part part_of(Group<D> (&g)[kGroups], float c, F f) {
+// alone, which spares most of a pass; where the sum gets out of 2^32, or is
+// none, it is formed again from the maximum of all. logit(z, e) sees the logit
+// of every place e of a block, block(k) the block's end.
+template <class D, class F, class B>
+__device__ __forceinline__ Part part_of(Group<D> (&g)[kGroups], float c, F logit, B block) {
   float m = g[0].get(0);
 #pragma unroll
   for (int i = 1; i < D::kVec; ++i) m = fmaxf(m, g[0].get(i));
   m = wave_max_f32(m);
-  float s = sum_of<D>(g, m, c, f);
-  if (!(s < 0x1p32f) || !near_offset(m, c)) {
+  bool near = near_offset(m, c);
+  float b = near ? rintf(m * c) : 0.0f, s = 0.0f;
+#pragma unroll
+  for (int k = 0; k < kBlocks<D>; ++k) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int j = (k * 8 + e) / D::kVec, i = (k * 8 + e) % D::kVec;
+      if (i == 0) g[j].fresh();
+      const float z = g[j].get(i);
+      s += __builtin_amdgcn_exp2f(fmaf(z, c, -b));
+      logit(z, e);
+    }
+    block(k);
+  }
+  s = wave_sum_f32(s);
+  if (!(s < 0x1p32f) || !near) {
 #pragma unroll
     for (int j = 0; j < kGroups; ++j) {
       g[j].fresh();
@@ -369,57 +351,55 @@ __device__ __forceinline__ Part part_of(Group<D> (&g)[kGroups], float c, F f) {
       for (int i = 0; i < D::kVec; ++i) m = fmaxf(m, g[j].get(i));
     }
     m = wave_max_f32(m);
-    s = sum_of<D>(g, m, c, [](float, int, int) LP_INLINE {});
+    near = near_offset(m, c);
+    b = near ? rintf(m * c) : 0.0f;
+    const float base = near || m == -INFINITY ? 0.0f : m;  // masked tokens sum to 0
+    s = 0.0f;
+#pragma unroll
+    for (int j = 0; j < kGroups; ++j) {
+      g[j].fresh();
+#pragma unroll
+      for (int i = 0; i < D::kVec; ++i)
+        s += __builtin_amdgcn_exp2f(fmaf(g[j].get(i) - base, c, -b));
+    }
+    s = wave_sum_f32(s);
   }
   return {m, s};
 }
 
-// Which lanes' logits of a chunk are wanted, place by place, and in which
-// blocks of eight places there are any.
-template <class D>
+// Which lanes' logits of a block are wanted, place by place. (Masks of a whole
+// chunk would not fit the scalar registers.)
 struct Hits {
-  static constexpr int kPlaces = kGroups * D::kVec, kBlocks = kPlaces / 8;
-  uint64_t masks[kPlaces], any[kBlocks];
-
-  __device__ __forceinline__ void set(int e, bool hit) {
-    masks[e] = __ballot(hit);
-    any[e / 8] = e % 8 == 0 ? masks[e] : any[e / 8] | masks[e];
-  }
+  uint64_t masks[8];
+  __device__ __forceinline__ void set(int e, bool hit) { masks[e] = __ballot(hit); }
 };
 
 // These tokens appended to the list, in any order. A wave asks for its places
-// in the list once a chunk, and passes over blocks without a hit.
+// in the list once a block.
 template <class D>
-__device__ __forceinline__ void append(const Group<D> (&g)[kGroups], const Hits<D>& hits,
+__device__ __forceinline__ void append(const Group<D> (&g)[kGroups], int k, const Hits& hits,
                                        int index0, uint64_t* list, uint32_t size,
                                        uint32_t* n_list) {
-  uint64_t all = 0;
+  uint64_t any = 0;
 #pragma unroll
-  for (int k = 0; k < Hits<D>::kBlocks; ++k) all |= hits.any[k];
-  if (all == 0) return;
+  for (int e = 0; e < 8; ++e) any |= hits.masks[e];
+  if (any == 0) return;
   uint32_t total = 0;
 #pragma unroll
-  for (int k = 0; k < Hits<D>::kBlocks; ++k)
-    if (hits.any[k])
-#pragma unroll
-      for (int e = k * 8; e < k * 8 + 8; ++e) total += (uint32_t)__popcll(hits.masks[e]);
+  for (int e = 0; e < 8; ++e) total += (uint32_t)__popcll(hits.masks[e]);
   uint32_t at = 0;
   if ((threadIdx.x & 63) == 0) at = atomicAdd(n_list, total);
   at = __builtin_amdgcn_readfirstlane(at);
 #pragma unroll
-  for (int k = 0; k < Hits<D>::kBlocks; ++k) {
-    if (hits.any[k] == 0) continue;
-#pragma unroll
-    for (int e = k * 8; e < k * 8 + 8; ++e) {
-      const uint64_t mask = hits.masks[e];
-      if (mask == 0) continue;
-      const uint32_t to = at + lanes_below(mask);
-      if ((mask >> (threadIdx.x & 63) & 1) && to < size) {
-        const int j = e / D::kVec, i = e % D::kVec;
-        list[to] = token_key(g[j].get(i), index0 + j * kThreads * D::kVec + i);
-      }
-      at += (uint32_t)__popcll(mask);
+  for (int e = 0; e < 8; ++e) {
+    const uint64_t mask = hits.masks[e];
+    if (mask == 0) continue;
+    const uint32_t to = at + lanes_below(mask);
+    if ((mask >> (threadIdx.x & 63) & 1) && to < size) {
+      const int j = (k * 8 + e) / D::kVec, i = (k * 8 + e) % D::kVec;
+      list[to] = token_key(g[j].get(i), index0 + j * kThreads * D::kVec + i);
     }
+    at += (uint32_t)__popcll(mask);
   }
 }
 
@@ -668,7 +648,7 @@ __device__ __forceinline__ void collect_buckets(const Row<D>& row, S& sh, int c0
     sh.mass[i] = 0;
     sh.cnt[i] = 0;
   }
-  if (threadIdx.x == 0) sh.facts = {0u, 0u, 0u};
+  if (threadIdx.x == 0) sh.facts = {0u, 0u, 0u, 0u};
   __syncthreads();
   float top = -INFINITY;
   uint64_t odd = 0;  // by lane
@@ -717,18 +697,17 @@ __global__ __launch_bounds__(kThreads, 6) void collect_kernel(SelectArgs a) {
       row.anchor = (double)anchor_of(row, sh.wave_f32);
       row.inv = kPerNat / (double)st.tau;
       collect_buckets(row, sh, c0, c1);
-      unsigned long long* mass = a.masses + n * kBuckets;
-      uint32_t* cnt = a.bucket_counts + n * (kBuckets + 4);
-      for (int i = tid; i < kBuckets; i += kThreads)
-        if (sh.cnt[i]) {
-          atomicAdd(&cnt[i], sh.cnt[i]);
-          atomicAdd(&mass[i], sh.mass[i]);
-        }
-      if (tid == 0) {
-        atomicMax(&cnt[kBuckets], sh.facts.top);
-        atomicOr(&cnt[kBuckets + 1], sh.facts.odd);
-        atomicAdd(&cnt[kBuckets + 2], sh.facts.masked);
+      // Left for row_kernel as they are. (Added up by global atomics, cut rows
+      // of a batch of 64 took 50 us instead of FIGURE: eight dies' caches have no
+      // common place for them.)
+      const int64_t at = n * a.slices + slice;
+      unsigned long long* mass = a.masses + at * kBuckets;
+      uint32_t* cnt = a.bucket_counts + at * kBuckets;
+      for (int i = tid; i < kBuckets; i += kThreads) {
+        mass[i] = sh.mass[i];
+        cnt[i] = sh.cnt[i];
       }
+      if (tid == 0) a.facts[at] = sh.facts;
       return;
     }
   const int slices = slices_of(a, st);
@@ -787,11 +766,12 @@ __global__ __launch_bounds__(kThreads, 6) void collect_kernel(SelectArgs a) {
       if (tid == 0) sh.n_list = 0;
       __syncthreads();
     }
-    Hits<D> hits;
-    const Part p = part_of<D>(g, scale2, [&](float z, int j, int i) LP_INLINE {
-      hits.set(j * D::kVec + i, z >= theta);
-    });
-    append<D>(g, hits, Row<D>::index(c, 0, 0), sh.list, kShort, &sh.n_list);
+    Hits hits;
+    const Part p = part_of<D>(
+        g, scale2, [&](float z, int e) LP_INLINE { hits.set(e, z >= theta); },
+        [&](int k) LP_INLINE {
+          append<D>(g, k, hits, Row<D>::index(c, 0, 0), sh.list, kShort, &sh.n_list);
+        });
     if ((tid & 63) == 0) {
       if (a.slices == 1) sh.parts[c * kWaves + wave] = p;
       else a.parts[(n * chunks + c) * kWaves + wave] = p;
@@ -844,11 +824,6 @@ __global__ __launch_bounds__(kThreads, 6) void collect_kernel(SelectArgs a) {
   } else {
     finish_draw(a, st, n, sh.list, m, log2_all, sh);
   }
-}
-
-__global__ __launch_bounds__(256) void clear_kernel(uint4* p, uint32_t n) {
-  const uint32_t i = blockIdx.x * 256 + threadIdx.x;
-  if (i < n) p[i] = make_uint4(0, 0, 0, 0);
 }
 
 // ---- By buckets -------------------------------------------------------------
@@ -943,13 +918,16 @@ __device__ __forceinline__ uint32_t gather(const Row<D>& row, Shared& sh, float 
   if (threadIdx.x == 0) sh.n_list = 0;
   __syncthreads();
   row.for_chunks(0, row.chunks(), [&](Group<D>(&g)[kGroups], int c) LP_INLINE {
-    Hits<D> hits;
 #pragma unroll
-    for (int e = 0; e < Hits<D>::kPlaces; ++e) {
-      const float z = g[e / D::kVec].get(e % D::kVec);
-      hits.set(e, (z >= lo0 && z < hi0) || (z >= lo1 && z < hi1));
+    for (int k = 0; k < kBlocks<D>; ++k) {
+      Hits hits;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float z = g[(k * 8 + e) / D::kVec].get((k * 8 + e) % D::kVec);
+        hits.set(e, (z >= lo0 && z < hi0) || (z >= lo1 && z < hi1));
+      }
+      append<D>(g, k, hits, Row<D>::index(c, 0, 0), sh.list, kList, &sh.n_list);
     }
-    append<D>(g, hits, Row<D>::index(c, 0, 0), sh.list, kList, &sh.n_list);
   });
   __syncthreads();
   return sh.n_list;
@@ -970,6 +948,95 @@ enum Mode { kByRank, kByMass, kByMassOver };
 struct Listed {
   int lo0 = 1, hi0 = 0, lo1 = 1, hi1 = 0;
 };
+
+// Part of a bucket of more tokens than can be listed: 2 048 finer buckets of
+// equal key ranges, turn by turn, until the one in which the selection ends can
+// be. Its tokens are listed; returns what lies before them. Out of line: only
+// rows of many equal or near logits come here.
+struct Refined {
+  uint32_t cnt;
+  unsigned long long mass;
+};
+template <class D>
+__device__ __noinline__ Refined refine(Row<D> row, Shared& sh, float flo, float fhi,
+                                       uint32_t count, Mode mode, uint32_t rank, double want) {
+  uint32_t base_cnt = 0;
+  unsigned long long base_mass = 0;
+  auto reached = [&](uint32_t c, unsigned long long s) LP_INLINE {
+    return mode == kByRank ? c >= rank : (mode == kByMass ? (double)s >= want : (double)s > want);
+  };
+  uint64_t lo = (uint64_t)key_of(flo) << 32;
+  uint64_t hi = fhi > row.zmax ? ((uint64_t)key_of(row.zmax) << 32) | 0xFFFFFFFFull
+                                         : ((uint64_t)key_of(fhi) << 32) - 1;
+  while (count > (uint32_t)kList) {
+    // The range shrinks 2 048-fold a turn, and keys are distinct, so this ends.
+    const uint64_t range = hi - lo;
+    const int bits = 64 - __clzll((long long)(range | 1));
+    const int shift = bits > 11 ? bits - 11 : 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < kBuckets; i += kThreads) {
+      sh.fmass[i] = 0;
+      sh.fcnt[i] = 0;
+    }
+    __syncthreads();
+    row.for_each([&](float z, int idx) LP_INLINE {
+      const uint64_t k = token_key(z, idx);
+      if (k >= lo && k <= hi) {
+        const uint32_t f = (uint32_t)((hi - k) >> shift);
+        atomicAdd(&sh.fcnt[f], 1u);
+        atomicAdd(&sh.fmass[f], Row<D>::mass(row.x_of(z)));
+      }
+    });
+    __syncthreads();
+    uint32_t c = 0;
+    unsigned long long s = 0;
+    for (int i = 0; i < kPerThread; ++i) {
+      c += sh.fcnt[threadIdx.x * kPerThread + i];
+      s += sh.fmass[threadIdx.x * kPerThread + i];
+    }
+    uint32_t all_c;
+    unsigned long long all_m;
+    uint32_t cb = base_cnt + block_scan(c, sh.wave_u32, &all_c);
+    unsigned long long mb = base_mass + block_scan(s, sh.wave_u64, &all_m);
+    // First finer bucket through which the selection is reached; the last
+    // occupied one where rounding of `want` leaves none.
+    for (int i = 0; i < kPerThread; ++i) {
+      const int f = threadIdx.x * kPerThread + i;
+      const uint32_t c1 = cb + sh.fcnt[f];
+      const unsigned long long m1 = mb + sh.fmass[f];
+      const bool last = c1 == base_cnt + all_c;
+      if (sh.fcnt[f] != 0 && (reached(c1, m1) || last) &&
+          !(cb != base_cnt && reached(cb, mb))) {
+        sh.found = (uint32_t)f;
+        sh.found_cnt = cb;
+        sh.found_mass = mb;
+      }
+      cb = c1;
+      mb = m1;
+    }
+    __syncthreads();
+    const uint32_t f = sh.found;
+    base_cnt = sh.found_cnt;
+    base_mass = sh.found_mass;
+    count = sh.fcnt[f];
+    const uint64_t top = hi - ((uint64_t)f << shift);
+    const uint64_t width = (uint64_t)1 << shift;
+    lo = top - lo >= width ? top - width + 1 : lo;
+    hi = top;
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) sh.n_list = 0;
+  __syncthreads();
+  row.for_each([&](float z, int idx) LP_INLINE {
+    const uint64_t k = token_key(z, idx);
+    if (k >= lo && k <= hi) {
+      const uint32_t s = atomicAdd(&sh.n_list, 1u);
+      if (s < (uint32_t)kList) sh.list[s] = k;
+    }
+  });
+  __syncthreads();
+  return {base_cnt, base_mass};
+}
 
 // The first token, in order, of bucket b at which
 //   kByRank:     `rank` tokens of the bucket are reached (rank >= 1),
@@ -995,77 +1062,9 @@ __device__ __forceinline__ Found select_in_bucket(const Row<D>& row, Shared& sh,
     float flo = sh.least[0], fhi = sh.least[1];
     if (count > (uint32_t)kList) {
       listed = Listed();
-      uint64_t lo = (uint64_t)key_of(flo) << 32;
-      uint64_t hi = fhi > row.zmax ? ((uint64_t)key_of(row.zmax) << 32) | 0xFFFFFFFFull
-                                             : ((uint64_t)key_of(fhi) << 32) - 1;
-      while (count > (uint32_t)kList) {
-        // Too many to list: 2 048 finer buckets of equal key ranges. The range
-        // shrinks 2 048-fold a turn, and keys are distinct, so this ends.
-        const uint64_t range = hi - lo;
-        const int bits = 64 - __clzll((long long)(range | 1));
-        const int shift = bits > 11 ? bits - 11 : 0;
-        __syncthreads();
-        for (int i = threadIdx.x; i < kBuckets; i += kThreads) {
-          sh.fmass[i] = 0;
-          sh.fcnt[i] = 0;
-        }
-        __syncthreads();
-        row.for_each([&](float z, int idx) LP_INLINE {
-          const uint64_t k = token_key(z, idx);
-          if (k >= lo && k <= hi) {
-            const uint32_t f = (uint32_t)((hi - k) >> shift);
-            atomicAdd(&sh.fcnt[f], 1u);
-            atomicAdd(&sh.fmass[f], Row<D>::mass(row.x_of(z)));
-          }
-        });
-        __syncthreads();
-        uint32_t c = 0;
-        unsigned long long s = 0;
-        for (int i = 0; i < kPerThread; ++i) {
-          c += sh.fcnt[threadIdx.x * kPerThread + i];
-          s += sh.fmass[threadIdx.x * kPerThread + i];
-        }
-        uint32_t all_c;
-        unsigned long long all_m;
-        uint32_t cb = base_cnt + block_scan(c, sh.wave_u32, &all_c);
-        unsigned long long mb = base_mass + block_scan(s, sh.wave_u64, &all_m);
-        // First finer bucket through which the selection is reached; the last
-        // occupied one where rounding of `want` leaves none.
-        for (int i = 0; i < kPerThread; ++i) {
-          const int f = threadIdx.x * kPerThread + i;
-          const uint32_t c1 = cb + sh.fcnt[f];
-          const unsigned long long m1 = mb + sh.fmass[f];
-          const bool last = c1 == base_cnt + all_c;
-          if (sh.fcnt[f] != 0 && (reached(c1, m1) || last) &&
-              !(cb != base_cnt && reached(cb, mb))) {
-            sh.found = (uint32_t)f;
-            sh.found_cnt = cb;
-            sh.found_mass = mb;
-          }
-          cb = c1;
-          mb = m1;
-        }
-        __syncthreads();
-        const uint32_t f = sh.found;
-        base_cnt = sh.found_cnt;
-        base_mass = sh.found_mass;
-        count = sh.fcnt[f];
-        const uint64_t top = hi - ((uint64_t)f << shift);
-        const uint64_t width = (uint64_t)1 << shift;
-        lo = top - lo >= width ? top - width + 1 : lo;
-        hi = top;
-        __syncthreads();
-      }
-      if (threadIdx.x == 0) sh.n_list = 0;
-      __syncthreads();
-      row.for_each([&](float z, int idx) LP_INLINE {
-        const uint64_t k = token_key(z, idx);
-        if (k >= lo && k <= hi) {
-          const uint32_t s = atomicAdd(&sh.n_list, 1u);
-          if (s < (uint32_t)kList) sh.list[s] = k;
-        }
-      });
-      __syncthreads();
+      const Refined r = refine<D>(row, sh, flo, fhi, count, mode, rank, want);
+      base_cnt = r.cnt;
+      base_mass = r.mass;
     } else {
       gather(row, sh, flo, fhi, INFINITY, INFINITY);
       listed = Listed();
@@ -1274,7 +1273,7 @@ template <class D>
 __device__ __forceinline__ int parts_of_row(const Row<D>& row, float tau, Shared& sh) {
   const float scale2 = scale2_of(tau);
   row.for_chunks(0, row.chunks(), [&](Group<D>(&g)[kGroups], int c) LP_INLINE {
-    const Part p = part_of<D>(g, scale2, [](float, int, int) LP_INLINE {});
+    const Part p = part_of<D>(g, scale2, [](float, int) LP_INLINE {}, [](int) LP_INLINE {});
     if ((threadIdx.x & 63) == 0) sh.parts[c * kWaves + (threadIdx.x >> 6)] = p;
   });
   __syncthreads();
@@ -1367,16 +1366,31 @@ __device__ __forceinline__ void finish_row(const SelectArgs& a, int64_t n, Share
       row.anchor = (double)anchor_of(row, sh.wave_f32);
       const bool ready = a.slices > 1;
       if (ready) {
-        const unsigned long long* mass = a.masses + n * kBuckets;
-        const uint32_t* cnt = a.bucket_counts + n * (kBuckets + 4);
+        const int64_t at = n * a.slices;
+        unsigned long long m[kPerThread];
+        uint32_t c[kPerThread];
+#pragma unroll
+        for (int i = 0; i < kPerThread; ++i) m[i] = c[i] = 0;
+        for (int t = 0; t < a.slices; ++t)
+#pragma unroll
+          for (int i = 0; i < kPerThread; ++i) {
+            const int64_t b = (at + t) * kBuckets + threadIdx.x + i * kThreads;
+            m[i] += read_global(a.masses, b);
+            c[i] += read_global(a.bucket_counts, b);
+          }
 #pragma unroll
         for (int i = 0; i < kPerThread; ++i) {
-          const int b = threadIdx.x + i * kThreads;
-          sh.mass[b] = read_global(mass, b);
-          sh.cnt[b] = read_global(cnt, b);
+          sh.mass[threadIdx.x + i * kThreads] = m[i];
+          sh.cnt[threadIdx.x + i * kThreads] = c[i];
         }
-        if (threadIdx.x == 0)
-          sh.facts = {cnt[kBuckets], cnt[kBuckets + 1], cnt[kBuckets + 2]};
+        if (threadIdx.x == 0) sh.facts = {0u, 0u, 0u, 0u};
+        __syncthreads();
+        if ((int)threadIdx.x < a.slices) {
+          const RowFacts f = a.facts[at + threadIdx.x];
+          atomicMax(&sh.facts.top, f.top);
+          atomicOr(&sh.facts.odd, f.odd);
+          atomicAdd(&sh.facts.masked, f.masked);
+        }
         __syncthreads();
       }
       Totals all;
@@ -1465,13 +1479,6 @@ __global__ __launch_bounds__(kThreads, 4) void overflow_kernel(SelectArgs a) {
 template <class D, bool kTop>
 hipError_t launch(const SelectArgs& a, bool lists, bool buckets, hipStream_t stream) {
   hipError_t e;
-  if (buckets && a.slices > 1) {
-    // Counts, masses and facts of all rows, cleared (they lie side by side).
-    const uint32_t words = (uint32_t)(a.bucket_bytes / sizeof(uint4));
-    clear_kernel<<<dim3((words + 255) / 256), 256, 0, stream>>>(
-        reinterpret_cast<uint4*>(a.masses), words);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
-  }
   if (lists || (buckets && a.slices > 1)) {
     collect_kernel<D, kTop><<<dim3((uint32_t)(a.N * a.slices)), kThreads, 0, stream>>>(a);
     if ((e = hipGetLastError()) != hipSuccess) return e;
@@ -1506,8 +1513,9 @@ SelectWorkspace select_workspace_layout(int64_t N, int64_t V, int32_t dtype) {
   w.off_parts = up(lists * sizeof(uint32_t));
   w.off_keys = w.off_parts + cut * up((size_t)N * chunks * kWaves * sizeof(Part));
   w.off_masses = w.off_keys + cut * up(lists * kListMax * sizeof(uint64_t));
-  w.off_bucket_counts = w.off_masses + cut * (size_t)N * kBuckets * sizeof(unsigned long long);
-  w.total = w.off_bucket_counts + cut * up((size_t)N * (kBuckets + 4) * sizeof(uint32_t));
+  w.off_bucket_counts = w.off_masses + cut * lists * kBuckets * sizeof(unsigned long long);
+  w.off_facts = w.off_bucket_counts + cut * lists * kBuckets * sizeof(uint32_t);
+  w.total = w.off_facts + cut * up(lists * sizeof(RowFacts));
   return w;
 }
 
@@ -1520,7 +1528,7 @@ hipError_t launch_select(SelectArgs a, void* workspace, hipStream_t stream) {
   a.keys = reinterpret_cast<uint64_t*>(base + w.off_keys);
   a.masses = reinterpret_cast<unsigned long long*>(base + w.off_masses);
   a.bucket_counts = reinterpret_cast<uint32_t*>(base + w.off_bucket_counts);
-  a.bucket_bytes = w.total - w.off_masses;
+  a.facts = reinterpret_cast<RowFacts*>(base + w.off_facts);
   const bool top = a.u == nullptr;
   // Which ways the rows can take, as far as the host sees the settings.
   const bool seen = !a.temperatures && !a.top_ks && !a.top_ps && !a.min_ps;
