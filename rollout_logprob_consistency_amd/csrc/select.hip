@@ -35,6 +35,7 @@ constexpr int kThreads = kSelectThreads;
 constexpr int kWaves = kThreads / 64;
 constexpr int kGroups = 4;            // 16-byte groups per thread and chunk
 constexpr int kBuckets = 2048;        // of 1/32 nat; the last one: weight 0
+constexpr int kSlots = kBuckets + 64; // while they are collected
 constexpr double kPerNat = 32.0;
 constexpr double kHead = 768.0;       // the anchor's place: 24 nats from the top
 constexpr int kPerThread = kBuckets / kThreads;
@@ -76,10 +77,10 @@ struct Shared {
   // Buckets: counts and masses while they are collected, then exclusive
   // prefix sums (masses as doubles in units of the anchor's weight).
   union {
-    unsigned long long mass[kBuckets];
+    unsigned long long mass[kSlots];
     double above[kBuckets + 1];
   };
-  uint32_t cnt[kBuckets + 1];
+  uint32_t cnt[kSlots];
   // The listed tokens, or the finer buckets of one that is too full to list.
   union {
     uint64_t list[kList];
@@ -114,6 +115,13 @@ struct Row {
   }
   static __device__ __forceinline__ uint32_t bucket(double x) {
     return min((uint32_t)__double_as_longlong(x + kMagic), (uint32_t)(kBuckets - 1));
+  }
+  // Where a lane counts it. The last bucket weighs nothing and takes whole waves
+  // (masked tokens, places behind the row), whose adds to one word would go one
+  // by one: each lane has a word of its own for it.
+  static __device__ __forceinline__ uint32_t slot(double x) {
+    const uint32_t b = (uint32_t)__double_as_longlong(x + kMagic);
+    return b < (uint32_t)(kBuckets - 1) ? b : kBuckets + (threadIdx.x & 63);
   }
   // exp((b - x) / 32) in units of 2^-43, b = rint(x), by its Taylor series to
   // degree 5 (|b - x| / 32 <= 1/64: truncation 2e-14 relative); the last term
@@ -448,9 +456,10 @@ __device__ __forceinline__ float scale2_of(float tau) {
 }
 
 // Slices of a row: every slice leaves at most k (kTopK) or kListMax tokens,
-// which have to fit one list together.
+// which have to fit one list together; half of it for kTopK, as sorting a
+// whole one costs more (64 rows, k = 400: FIGK) than the slices gain.
 __device__ __forceinline__ int slices_of(const SelectArgs& a, const Settings& s) {
-  const int most = s.kind == kTopK ? kList / (int)s.k : kList / kListMax;
+  const int most = s.kind == kTopK ? kList / 2 / (int)s.k : kList / kListMax;
   return min(a.slices, max(most, 1));
 }
 
@@ -607,8 +616,8 @@ struct CollectShared {
   union {
     uint64_t list[kShort];
     struct {  // a slice's buckets
-      unsigned long long mass[kBuckets];
-      uint32_t cnt[kBuckets];
+      unsigned long long mass[kSlots];
+      uint32_t cnt[kSlots];
     };
   };
   Part parts[kMaxParts];
@@ -640,11 +649,11 @@ __device__ __forceinline__ float anchor_of(const Row<D>& row, float* words) {
 
 // Counts and masses of the chunks [c0, c1) into LDS (cleared here), and their
 // facts. Logits above the first bucket land in the last one: the caller sees
-// by the maximum that there are some. No element is skipped: -inf goes to the
-// last bucket and is counted apart.
+// by the maximum that there are some. -inf goes to the last bucket and is
+// counted apart.
 template <class D, class S>
 __device__ __forceinline__ void collect_buckets(const Row<D>& row, S& sh, int c0, int c1) {
-  for (int i = threadIdx.x; i < kBuckets; i += kThreads) {
+  for (int i = threadIdx.x; i < kSlots; i += kThreads) {
     sh.mass[i] = 0;
     sh.cnt[i] = 0;
   }
@@ -660,7 +669,7 @@ __device__ __forceinline__ void collect_buckets(const Row<D>& row, S& sh, int c0
       for (int i = 0; i < D::kVec; ++i) {
         const float z = g[j].get(i);
         const double x = row.x_of(z);
-        const uint32_t b = Row<D>::bucket(x);
+        const uint32_t b = Row<D>::slot(x);
         atomicAdd(&sh.cnt[b], 1u);
         atomicAdd(&sh.mass[b], Row<D>::mass(x));
         top = fmaxf(top, z);
@@ -675,6 +684,8 @@ __device__ __forceinline__ void collect_buckets(const Row<D>& row, S& sh, int c0
     if (odd) atomicOr(&sh.facts.odd, 1u);
     atomicAdd(&sh.facts.masked, masked);
   }
+  __syncthreads();
+  if (threadIdx.x < 64) atomicAdd(&sh.cnt[kBuckets - 1], sh.cnt[kBuckets + threadIdx.x]);
   __syncthreads();
 }
 
@@ -1280,43 +1291,41 @@ __device__ __forceinline__ int parts_of_row(const Row<D>& row, float tau, Shared
   return row.chunks() * kWaves;
 }
 
-template <class D>
-__device__ __forceinline__ float max_of(const Row<D>& row, Shared& sh) {
-  float m = -INFINITY;
-  row.for_each([&](float z, int) LP_INLINE { m = fmaxf(m, z); });
-  return block_max(m, sh.wave_f32);
-}
-
 // A row of the short lists whose list overflowed: its tokens by selection,
 // then the same ending, so that its results do not depend on how the row was
 // cut. A row where min-p leaves more than kListMax goes by buckets for good.
 template <class D, bool kTop>
 __device__ __noinline__ void list_by_buckets(SelectArgs a, Settings st, int64_t n, Row<D> row,
                                              Shared& sh) {
-  const int parts = parts_of_row(row, st.tau, sh);
-  const Log2Sum log2_all = join_parts(sh.parts, parts, scale2_of(st.tau), sh.wave_f64);
-  if (!isfinite(log2_all.rest)) {
+  row.anchor = (double)anchor_of(row, sh.wave_f32);
+  row.inv = kPerNat / (double)st.tau;
+  Totals all;
+  if (!fill_buckets(row, sh, false, &all)) {
     if constexpr (kTop) write_bad_top(a, n);
     else if (threadIdx.x == 0) write_bad_draw(a, n);
     return;
   }
-  row.inv = kPerNat / (double)st.tau;
-  if (!kTop && st.kind == kMinP) {
-    const float lo = bound(max_of(row, sh) - depth_of(st));
-    const uint32_t m = gather(row, sh, lo, INFINITY, INFINITY, INFINITY);
-    __syncthreads();
-    if (m <= (uint32_t)kListMax) {
-      sort_list(sh.list, m);
-      if constexpr (!kTop) finish_draw(a, st, n, sh.list, m, log2_all, sh);
-      return;
-    }
-  }
-  row.anchor = (double)anchor_of(row, sh.wave_f32);
-  Totals all;
-  if (!fill_buckets(row, sh, false, &all)) return;  // (a bad row has left above)
+  float lo = 0.0f;
   if constexpr (!kTop)
     if (st.kind == kMinP) {
-      draw_from_buckets(a, st, n, row, all, sh);
+      lo = bound(row.zmax - depth_of(st));
+      // Far more than a short list holds, by the buckets above lo's alone, or
+      // by the list itself.
+      bool many = sh.cnt[Row<D>::bucket(row.x_of(lo))] > (uint32_t)kListMax;
+      if (!many) many = gather(row, sh, lo, INFINITY, INFINITY, INFINITY) > (uint32_t)kListMax;
+      if (many) {
+        draw_from_buckets(a, st, n, row, all, sh);
+        return;
+      }
+    }
+  const int parts = parts_of_row(row, st.tau, sh);
+  const Log2Sum log2_all = join_parts(sh.parts, parts, scale2_of(st.tau), sh.wave_f64);
+  if constexpr (!kTop)
+    if (st.kind == kMinP) {
+      const uint32_t m = gather(row, sh, lo, INFINITY, INFINITY, INFINITY);
+      __syncthreads();
+      sort_list(sh.list, m);
+      finish_draw(a, st, n, sh.list, m, log2_all, sh);
       return;
     }
   const uint32_t want = min(st.k, all.finite);
@@ -1324,7 +1333,7 @@ __device__ __noinline__ void list_by_buckets(SelectArgs a, Settings st, int64_t 
   uint32_t m = sh.cnt[b + 1];
   if (m <= (uint32_t)kList) {
     least_logits(row, sh, b, -1, -1, -1);
-    const float lo = sh.least[0];
+    lo = sh.least[0];
     m = gather(row, sh, lo, INFINITY, INFINITY, INFINITY);
   } else {
     // More than the list holds reach that bucket: up to the last token's key.
