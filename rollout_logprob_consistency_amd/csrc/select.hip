@@ -920,11 +920,20 @@ __device__ __forceinline__ void least_logits(const Row<D>& row, Shared& sh, int 
   __syncthreads();
 }
 
+// The largest finite float below hi (below both zeros where hi is one).
+__device__ __forceinline__ float float_before(float hi) {
+  return key_value(key_of(hi) - (hi == 0.0f ? 2u : 1u));
+}
+
 // Tokens with lo0 <= z < hi0 or lo1 <= z < hi1 appended to the list, in any
 // order; returns their number (which may pass the list's size).
 template <class D>
 __device__ __forceinline__ uint32_t gather(const Row<D>& row, Shared& sh, float lo0, float hi0, float lo1,
                            float hi1) {
+  // lo <= z < hi as one comparison: z is its own median with lo and the float
+  // before hi.
+  const float end0 = float_before(hi0), end1 = float_before(hi1);
+  const bool two = lo1 < INFINITY;
   __syncthreads();
   if (threadIdx.x == 0) sh.n_list = 0;
   __syncthreads();
@@ -935,8 +944,14 @@ __device__ __forceinline__ uint32_t gather(const Row<D>& row, Shared& sh, float 
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const float z = g[(k * 8 + e) / D::kVec].get((k * 8 + e) % D::kVec);
-        hits.set(e, (z >= lo0 && z < hi0) || (z >= lo1 && z < hi1));
+        hits.set(e, __builtin_amdgcn_fmed3f(z, lo0, end0) == z);
       }
+      if (two)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float z = g[(k * 8 + e) / D::kVec].get((k * 8 + e) % D::kVec);
+          hits.masks[e] |= __ballot(__builtin_amdgcn_fmed3f(z, lo1, end1) == z);
+        }
       append<D>(g, k, hits, Row<D>::index(c, 0, 0), sh.list, kList, &sh.n_list);
     }
   });

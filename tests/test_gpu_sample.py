@@ -100,6 +100,22 @@ def test_crowded_buckets(dtype, kind):
     check(t, z, u, top_k=4097, min_p=0.99)
 
 
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_borders_at_zero(dtype):
+    """Logits on a grid of 1/32 around zero: every bucket's border is passed,
+    the one between the zeros and the largest negative value among them."""
+    rng = np.random.default_rng(6)
+    n, v = 24, 700
+    z = rng.integers(-3, 2, (n, v)) / 32.0
+    z[rng.random((n, v)) < 0.1] *= -0.0
+    t, z = place(z, dtype)
+    u = ((np.arange(n) + 0.5) / n).astype(np.float32)
+    check(t, z, u)
+    check(t, z, u, top_k=600, top_p=0.8)
+    for top_p in (0.2, 0.45, 0.7, 0.95):
+        check(t, z, u, top_p=top_p)
+
+
 def test_wide_rows():
     """Logits far below the maximum weigh nothing but count as kept; the
     largest finite logits; temperatures that push everything apart or together."""
