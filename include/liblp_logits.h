@@ -67,10 +67,15 @@ extern "C" {
  * logit, no finite logit, a negative or NaN temperature or a NaN u, top_p or
  * min_p gives token -1, NaN scores and kept 0, and is counted in bad_rows.
  *
- * Precision: weights relative to the row's maximum are taken in fp64 (6e-14
- * relative) and summed as 64-bit integers per 1/32 nat of s, so sums do not
- * depend on an order; tokens more than 63.9 nats below the maximum weigh 0
- * (they still count for top_k and kept).
+ * Precision: what is kept and drawn is decided in fp64. Rows with top_k in
+ * [1, 512], greedy ones and rows with min_p alone (at most 1 024 tokens kept)
+ * go by a short list: fp64 weights and sums. The others go by buckets of 1/32
+ * nat: weights in fp64 (8e-14 relative), summed as 64-bit integers per bucket,
+ * so sums do not depend on an order; tokens more than 39.9 nats below the
+ * maximum may weigh 0 there (they still count for top_k and kept). The raw
+ * score's sum over the vocabulary is, for short lists, of fp32 exponentials
+ * joined in fp64 (about 1e-7 in the score; tested to 86 * 2^-24 + 2^-23 |score|),
+ * else the buckets' (1e-12). Scores are rounded to fp32 once.
  *
  * Layout: u [N] fp32; temperatures, top_ps, min_ps [N] fp32 and top_ks [N]
  * int32 give each row's settings, where NULL the scalar beside it holds for
@@ -114,7 +119,8 @@ lp_status lp_sample(const void* logits, int64_t ld, int32_t dtype, int64_t N,
  * The teacher's side of lp_distill_*: out_ids with out_logits (renormalised
  * there) or with out_logprob (taken as they are).
  *
- * Errors as for lp_sample, plus LP_EINVAL for k < 1 or k > V_true and a
+ * Logprobs and lse have the precision of the token draw's raw score by short
+ * lists. Errors as for lp_sample, plus LP_EINVAL for k < 1 or k > V_true and a
  * temperature that is not finite and > 0, LP_EUNSUPPORTED for k above
  * LP_TOP_MAX. Workspace: lp_top_logprobs_workspace_bytes(N, V_true, dtype).
  * ------------------------------------------------------------------------ */
@@ -169,7 +175,7 @@ lp_status lp_top_logprobs(const void* logits, int64_t ld, int32_t dtype,
  * logits' own buffer (same base, ld_grad = ld): every logit is read before
  * its place is written. Any other overlap is not allowed.
  *
- * Precision: the sums over the vocabulary are fp32 per thread (at most 64
+ * Precision: the sums over the vocabulary are fp32 per thread (at most 32
  * terms) and fp64 from there on, in an order fixed by V_true and the dtype;
  * teacher terms and the loss are fp64.
  *

@@ -259,6 +259,8 @@ struct Entries {
           z[j] = D::value(logits[id]);
           q[k] = exp_f64((double)a.teacher[row * a.K + k] * (a.logprobs ? 1.0 : a.inv_tau) - norm);
         }
+      } else if (k < LP_DISTILL_MAX_K) {
+        at[k] = -1;  // read in fours past K
       }
     }
   }
@@ -269,15 +271,25 @@ struct Entries {
     for (int j = 0; j < kMine; ++j) {
       const int k = j * kThreads + (int)threadIdx.x;
       if (k < a.K && at[k] >= 0) {
-        // An id that occurs again adds up; its first entry writes the sum.
+        // An id that occurs again adds up; its first entry writes the sum. Four
+        // entries a read tell whether there is one (step, 2 304 bf16 rows of
+        // 6 000, K = 256: 90 us instead of 141 us).
         const int32_t mine = at[k];
-        double sum = 0.0;
-        bool first = true;
-        for (int i = 0; i < a.K; ++i)
-          if (at[i] == mine) {
-            first &= i >= k;
-            sum += q[i];
-          }
+        double sum = q[k];
+        bool first = true, again = false;
+        for (int i = 0; i < a.K; i += 4) {
+          const int4 v = *reinterpret_cast<const int4*>(at + i);
+          again |= (v.x == mine && i != k) | (v.y == mine && i + 1 != k) |
+                   (v.z == mine && i + 2 != k) | (v.w == mine && i + 3 != k);
+        }
+        if (again) {
+          sum = 0.0;
+          for (int i = 0; i < a.K; ++i)
+            if (at[i] == mine) {
+              first &= i >= k;
+              sum += q[i];
+            }
+        }
         if (first) {
           const double p = exp_f64(((double)z[j] - s.M) * a.inv_tau) / s.S;
           out[mine] = D::round((float)((double)grad * a.inv_tau * (s.Q * p - sum)));
@@ -312,7 +324,7 @@ __global__ __launch_bounds__(kDistillThreads) void distill_backward_kernel(Disti
     return;
   }
   load_slice<D>(g, row, begin, end, tid);
-  __shared__ int32_t sh_at[LP_DISTILL_MAX_K];
+  __shared__ __align__(16) int32_t sh_at[LP_DISTILL_MAX_K];
   __shared__ double sh_q[LP_DISTILL_MAX_K];
   Entries<D, kDistillThreads> entries;
   entries.take(a, at.row, row, begin, end, s.norm, sh_at, sh_q);
@@ -325,6 +337,10 @@ __global__ __launch_bounds__(kDistillThreads) void distill_backward_kernel(Disti
   entries.write(a, s, grad, out + begin, sh_at, sh_q);
 }
 
+// Measured on bf16 rows of 151 936: step over 2 048 rows 305 us (4.1 TB/s of
+// the bytes it cannot do without) against 375 us by the three kernels above,
+// loss of 4 096 rows 212 us (5.9 TB/s) against 254 us.
+//
 // Loss (and gradient) of one row: kRowWaves / kDistillWaves slices at a time,
 // each by as many threads, in the places and the order of the kernels above.
 template <class D, bool kGradient>
@@ -336,7 +352,7 @@ __global__ __launch_bounds__(kRowWaves * 64, 8) void distill_row_kernel(DistillA
   __shared__ float sh_m[kRowMaxSlices];
   __shared__ double sh_s[kRowMaxSlices];
   __shared__ RowState sh_state;
-  __shared__ int32_t sh_at[LP_DISTILL_MAX_K];
+  __shared__ __align__(16) int32_t sh_at[LP_DISTILL_MAX_K];
   __shared__ double sh_q[LP_DISTILL_MAX_K];
   const int64_t r = row0 + blockIdx.x;
   const Raw* row = static_cast<const Raw*>(a.logits) + r * a.ld;
@@ -415,7 +431,7 @@ hipError_t backward_rows(const DistillArgs& a, int64_t row0, int64_t rows, hipSt
 
 template <class D>
 hipError_t run(const DistillArgs& a, bool forward, bool backward, hipStream_t stream) {
-  if (forward && a.T >= kRowMinRows && a.slices.n <= kRowMaxSlices) {
+  if (forward && a.T >= kRowMinRows && a.slices.n >= kRowMinSlices && a.slices.n <= kRowMaxSlices) {
     const int64_t most = rows_per_dispatch(1, kRowWaves * 64);
     for (int64_t r = 0; r < a.T; r += most) {
       const dim3 rows((uint32_t)std::min(most, a.T - r));

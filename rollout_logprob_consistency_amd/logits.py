@@ -11,7 +11,9 @@ and every arithmetic step runs in the library's kernels.
 
 Rows of logits are [N, columns] bfloat16, float16 or float32 with unit column
 stride and any row stride; `v_true` is the true vocabulary (columns behind it
-are padding).
+are padding). Scratch memory is allocated per call unless `workspace` is given
+(a uint8 tensor of the library's *_workspace_bytes, 256-byte aligned); calls that
+may overlap, captured graphs among them, must not share one.
 """
 
 from __future__ import annotations

@@ -4,7 +4,7 @@ Loss: teacher terms are fp64; ln S carries the fp32 exponentials. Their
 argument (z - m) * (log2 e / tau) has three roundings (3 * 2^-24 |x| relative
 to its value x), so a weight is off by ln2 * 3 * 2^-24 |x|; weighted by the
 weights, |x| averages at most the entropy in bits, at most log2 V <= 17.3: 36
-* 2^-24. The exponential adds 2^-23, a thread's sum of 64 terms at most 63 *
+* 2^-24. The exponential adds 2^-23, a thread's sum (of at most 64 terms) at most 63 *
 2^-24. In total 102 * 2^-24 of S, times Q in the loss; the result is rounded
 to fp32 once.
 

@@ -12,6 +12,7 @@ from oracle import logit_rows as ol
 from workloads import synth
 
 from .gpu_helpers import DEV, SCORE_ATOL, dev_bf16
+from .logits_helpers import TYPES
 
 pytestmark = pytest.mark.gpu
 
@@ -78,6 +79,38 @@ def everything(z, u, w, ids, top):
     out += [loss, lp.distill_backward(z, ids, top, state, w)]
     out += list(lp.distill_step(z.bfloat16(), ids, top, w))
     return out
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_results_do_not_depend_on_the_batch(dtype):
+    """520 rows (whole rows a workgroup) against single rows and batches of 40
+    (rows cut into slices), with settings of every kind: short lists, lists
+    that overflow (ties, many tokens above min-p), wide top-k, nuclei."""
+    n, v = 520, 40009
+    g = torch.Generator(device=DEV).manual_seed(4)
+    z = torch.randn(n, v, generator=g, device=DEV) * 2.0
+    z[::7] = (z[::7] * 2).round() / 2               # heavy ties
+    z[::11, ::3] = float("-inf")
+    z[5] = 1.25
+    z[6, 77] = float("nan")
+    z = z.to(TYPES[dtype])
+    u = torch.rand(n, generator=g, device=DEV)
+
+    def pick(options, kind):
+        o = torch.tensor(options, dtype=kind, device=DEV)
+        return o[torch.randint(0, len(options), (n,), generator=g, device=DEV)]
+    how = (pick([0.0, 0.6, 1.0, 1.8], torch.float32), pick([0, 0, 1, 30, 400, 900], torch.int32),
+           pick([1.0, 0.9, 0.5], torch.float32), pick([0.0, 0.0, 0.05, 1e-4], torch.float32))
+    ref = lp.sample(z, u, *how)
+    top = [lp.top_logprobs(z, k) for k in (20, 700)]
+    spans = [slice(i, i + 1) for i in range(0, 40)] + [slice(i, i + 40) for i in range(40, 520, 40)]
+    for s in spans:
+        got = lp.sample(z[s], u[s], *(h[s] for h in how))
+        for a, b in zip(ref, got):
+            assert torch.equal(a[s].nan_to_num(-9), b.nan_to_num(-9)), s
+        for k, t in zip((20, 700), top):
+            for a, b in zip(t, lp.top_logprobs(z[s], k)):
+                assert torch.equal(a[s].nan_to_num(-9), b.nan_to_num(-9)), (s, k)
 
 
 def test_streams_give_the_default_streams_bits(batch):
