@@ -115,6 +115,7 @@ def sample(logits: torch.Tensor, u: torch.Tensor, temperature=1.0, top_k=0, top_
     pk, top_k = _setting("top_k", top_k, n, torch.int32, dev)
     pp, top_p = _setting("top_p", top_p, n, torch.float32, dev)
     pm, min_p = _setting("min_p", min_p, n, torch.float32, dev)
+    top_k = max(-1, min(int(top_k), 2 ** 31 - 1))
     token = torch.empty(n, dtype=torch.int64, device=dev)
     logprob = torch.empty(n, dtype=torch.float32, device=dev)
     processed = torch.empty(n, dtype=torch.float32, device=dev)
@@ -123,7 +124,7 @@ def sample(logits: torch.Tensor, u: torch.Tensor, temperature=1.0, top_k=0, top_
     ws = _workspace(workspace, L.lp_sample_workspace_bytes(n, vt, code), dev)
     bad = _bad_rows(bad_rows, check, dev)
     _call(L.lp_sample, dev,
-          (logits.data_ptr(), ld, code, n, vt, pu, pt, float(temperature), pk, int(top_k), pp,
+          (logits.data_ptr(), ld, code, n, vt, pu, pt, float(temperature), pk, top_k, pp,
            float(top_p), pm, float(min_p), token.data_ptr(), logprob.data_ptr(),
            processed.data_ptr(), kept.data_ptr(), None if bad is None else bad.data_ptr(),
            ws.data_ptr(), ws.numel() * ws.element_size()), "lp_sample")
@@ -181,11 +182,11 @@ def _out_grad(logits, out, dev):
     if out is None:
         out = torch.empty(logits.shape, dtype=logits.dtype, device=dev)
         return out, out.shape[1]
-    if out.requires_grad:
-        raise ValueError("out must not require gradients")
     if not isinstance(out, torch.Tensor) or out.device != dev or out.dtype != logits.dtype or \
             out.shape != logits.shape:
         raise ValueError("out must have the logits' shape, dtype and device")
+    if out.requires_grad:
+        raise ValueError("out must not require gradients")
     _, _, _, ld, _ = _rows("out", out, None)
     if out.data_ptr() == logits.data_ptr():
         if out.shape[0] > 1 and out.stride(0) != logits.stride(0):

@@ -113,6 +113,30 @@ def test_results_do_not_depend_on_the_batch(dtype):
                 assert torch.equal(a[s].nan_to_num(-9), b.nan_to_num(-9)), (s, k)
 
 
+def test_offsets_past_32_bits():
+    """15 000 bf16 rows of 151 936 (2.3e9 logits, 4.6 GB): the last rows as they
+    are alone, the gradient over the logits' own buffer."""
+    n, v = 15000, 151936
+    z = torch.zeros(n, v, dtype=torch.bfloat16, device=DEV)
+    g = torch.Generator(device=DEV).manual_seed(5)
+    last = slice(n - 4, n)
+    z[last] = torch.randn(4, v, generator=g, device=DEV).to(torch.bfloat16) * 3
+    u = torch.rand(n, generator=g, device=DEV)
+    w = torch.rand(n, generator=g, device=DEV)
+    w[: n - 4] = 0
+    alone = z[last].clone()
+    for how in (dict(top_p=0.9), dict(top_k=30)):
+        whole, one = lp.sample(z, u, **how), lp.sample(alone, u[last], **how)
+        assert all(torch.equal(a[last], b) for a, b in zip(whole, one))
+    whole, one = lp.top_logprobs(z, 16), lp.top_logprobs(alone, 16)
+    assert all(torch.equal(a[last], b) for a, b in zip(whole, one))
+    ids, top, _ = whole
+    loss, grad = lp.distill_step(alone, ids[last].contiguous(), top[last].contiguous(), w[last])
+    loss2, grad2 = lp.distill_step(z, ids, top, w, out=z)
+    assert torch.equal(loss2[last], loss) and torch.equal(grad2[last], grad)
+    assert not grad2[: n - 4].any()
+
+
 def test_streams_give_the_default_streams_bits(batch):
     ref = everything(*batch)
     torch.cuda.synchronize()
