@@ -1246,11 +1246,12 @@ __device__ __forceinline__ void draw_from_buckets(const SelectArgs& a, const Set
     if (sh.cnt[b0] < kept) {
       uint32_t c[3] = {0, 0, 0};
       unsigned long long w[3] = {0, 0, 0};
+      least_logits(row, sh, b1, b0 - 1, -1, -1);
+      const float lo = sh.least[0], hi = sh.least[1];
       row.for_each([&](float z, int) LP_INLINE {
-        const double x = row.x_of(z);
-        const int d = (int)Row<D>::bucket(x) - b0;
-        if (z != -INFINITY && d >= 0 && d <= b1 - b0 &&
-            (row.zmax - (double)z) * row.inv <= most) {
+        if (z >= lo && z < hi && (row.zmax - (double)z) * row.inv <= most) {
+          const double x = row.x_of(z);
+          const int d = (int)Row<D>::bucket(x) - b0;
 #pragma unroll
           for (int i = 0; i < 3; ++i)
             if (d == i) {
