@@ -64,8 +64,9 @@ extern "C" {
  * tau == 0 is the greedy draw: token = the lowest index of the largest logit,
  * logprob at temperature 1, processed 0, kept 1. u is clamped to
  * [0, 1 - 2^-24]. top_p <= 0 keeps one token. A row that has a NaN or +inf
- * logit, no finite logit, a negative or NaN temperature or a NaN u, top_p or
- * min_p gives token -1, NaN scores and kept 0, and is counted in bad_rows.
+ * logit, no finite logit, a temperature other than 0 or a positive normal
+ * number (finite, at least 2^-126), or a NaN u, top_p or min_p gives token -1,
+ * NaN scores and kept 0, and is counted in bad_rows.
  *
  * Precision: what is kept and drawn is decided in fp64. Rows with top_k in
  * [1, 512], greedy ones and rows with min_p alone (at most 1 024 tokens kept)
@@ -87,9 +88,9 @@ extern "C" {
  * Errors: LP_EINVAL for N < 0, V_true < 1, ld < V_true, an unknown dtype, a
  * NULL required pointer, logits or another array not aligned to its element
  * type, a workspace that is too small or misaligned, and for a scalar
- * setting that is used: temperature negative, NaN or infinite, top_p or min_p
- * NaN. LP_EUNSUPPORTED for V_true above LP_SELECT_MAX_VOCAB or N above
- * 4 194 303. N == 0 does nothing.
+ * setting that is used: temperature neither 0 nor a positive normal number,
+ * top_p or min_p NaN. LP_EUNSUPPORTED for V_true above LP_SELECT_MAX_VOCAB or
+ * N above 4 194 303. N == 0 does nothing.
  * ------------------------------------------------------------------------ */
 #define LP_SELECT_MAX_VOCAB 1048576
 
@@ -121,7 +122,7 @@ lp_status lp_sample(const void* logits, int64_t ld, int32_t dtype, int64_t N,
  *
  * Logprobs and lse have the precision of the token draw's raw score by short
  * lists. Errors as for lp_sample, plus LP_EINVAL for k < 1 or k > V_true and a
- * temperature that is not finite and > 0, LP_EUNSUPPORTED for k above
+ * temperature that is not a positive normal number, LP_EUNSUPPORTED for k above
  * LP_TOP_MAX. Workspace: lp_top_logprobs_workspace_bytes(N, V_true, dtype).
  * ------------------------------------------------------------------------ */
 #define LP_TOP_MAX 1024
@@ -177,15 +178,16 @@ lp_status lp_top_logprobs(const void* logits, int64_t ld, int32_t dtype,
  *
  * Precision: the sums over the vocabulary are fp32 per thread (at most 32
  * terms) and fp64 from there on, in an order fixed by V_true and the dtype;
- * teacher terms and the loss are fp64.
+ * teacher terms and the loss are fp64. grad_loss[t] / temperature has to be in
+ * fp32's range: a row where it is not has infinities and NaN in its gradient.
  *
  * Layout: teacher_ids [T, K] int64 and teacher [T, K] fp32, contiguous.
  * Workspace: lp_distill_workspace_bytes(T, V_true, dtype) for forward and
  * step, 256-byte aligned.
  *
  * Errors: LP_EINVAL for T < 0, V_true < 1, ld < V_true, V_columns < V_true,
- * ld_grad < V_columns, K < 1, an unknown dtype or flag, a temperature that is not finite and > 0, NULL
- * required or misaligned pointers, a small or misaligned workspace;
+ * ld_grad < V_columns, K < 1, an unknown dtype or flag, a temperature that is
+ * not a positive normal number, NULL required or misaligned pointers, a small or misaligned workspace;
  * LP_EUNSUPPORTED for K above LP_DISTILL_MAX_K, T above 2^31 - 1 or
  * V_columns above 2^31 - 1. T == 0 does nothing.
  * ------------------------------------------------------------------------ */

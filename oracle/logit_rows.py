@@ -26,7 +26,8 @@ def sample_row(z, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0):
     where there is no valid draw. Settings are fp32 values."""
     z = np.asarray(z, np.float64)
     tau, u, top_p, min_p = (float(np.float32(v)) for v in (temperature, u, top_p, min_p))
-    if not _row_ok(z) or not tau >= 0 or np.isnan([u, top_p, min_p]).any():
+    tau_ok = tau == 0 or 2.0 ** -126 <= tau < np.inf
+    if not _row_ok(z) or not tau_ok or np.isnan([u, top_p, min_p]).any():
         return -1, np.nan, np.nan, 0
     greedy = tau == 0
     order = token_order(z)

@@ -19,7 +19,8 @@ bool dtype_ok(int32_t dtype) { return dtype == LP_F32 || dtype == LP_BF16 || dty
 // Element size of a valid dtype.
 uintptr_t size_of(int32_t dtype) { return (uintptr_t)lp::dtype_bytes(dtype); }
 
-bool temperature_ok(float t) { return isfinite(t) && t > 0.0f; }
+// (Below 2^-126 the kernels' fp32 scale log2(e) / t would be infinite.)
+bool temperature_ok(float t) { return isnormal(t) && t > 0.0f; }
 
 // One workgroup of kSelectThreads per row in a dispatch of 2^32 - 1 work-items
 // at most (and fewer than 4 194 304 rows, the limit the interface names).
@@ -49,7 +50,7 @@ lp_status lp_sample(const void* logits, int64_t ld, int32_t dtype, int64_t N, in
                     float* out_processed, int32_t* out_kept, int32_t* bad_rows, void* workspace,
                     size_t workspace_bytes, hipStream_t stream) {
   if (N < 0 || V_true < 1 || ld < V_true || !dtype_ok(dtype)) return LP_EINVAL;
-  if (!temperatures && !(isfinite(temperature) && temperature >= 0.0f)) return LP_EINVAL;
+  if (!temperatures && temperature != 0.0f && !temperature_ok(temperature)) return LP_EINVAL;
   if ((!top_ps && isnan(top_p)) || (!min_ps && isnan(min_p))) return LP_EINVAL;
   if (N == 0) return LP_OK;
   if (!logits || !u || !out_token || !out_logprob || !workspace) return LP_EINVAL;

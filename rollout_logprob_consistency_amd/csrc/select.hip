@@ -3,8 +3,8 @@
 //
 // Two ways through a row, chosen by its settings alone:
 //
-// By a short list (top_k in [1, 1024], the greedy draw, min-p without top-p,
-// and the top logits): collect_kernel reads the row once, keeps the tokens
+// By a short list (top_k in [1, 512], the greedy draw, min-p alone, and the top
+// logits): collect_kernel reads the row once, keeps the tokens
 // that can still be among the first in a list in LDS, and sums exp(z - m) per
 // wave and chunk for the log-sum-exp. The list is sorted; everything else is
 // decided in it, with weights and sums in fp64. Where there are few rows, a
@@ -433,11 +433,11 @@ __device__ __forceinline__ Settings settings_of(const SelectArgs& a, int64_t n) 
   s.top_k = a.top_ks ? read_global(a.top_ks, n) : a.top_k;
   s.u = read_global(a.u, n);
   s.greedy = s.tau == 0.0f;
-  s.bad = !(s.tau >= 0.0f) || isnan(s.u) || isnan(s.top_p) || isnan(s.min_p);
+  s.bad = !(s.greedy || (s.tau > 0.0f && isnormal(s.tau))) || isnan(s.u) || isnan(s.top_p) || isnan(s.min_p);
   if (s.greedy) s.tau = 1.0f;
   s.k = s.greedy ? 1u : (uint32_t)max(s.top_k, 0);
   s.kind = kBuckets_;
-  if (!s.bad && isfinite(s.tau)) {
+  if (!s.bad) {
     if (s.greedy || (s.top_k > 0 && s.top_k <= kShortTop)) s.kind = kTopK;
     else if (s.top_k <= 0 && s.top_p >= 1.0f && s.min_p > 0.0f && s.min_p <= 1.0f) s.kind = kMinP;
   }

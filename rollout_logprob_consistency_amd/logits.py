@@ -106,7 +106,8 @@ def sample(logits: torch.Tensor, u: torch.Tensor, temperature=1.0, top_k=0, top_
     fp32 under the full vocabulary, processed fp32 under the kept tokens,
     kept int32), each [N]. Ties go to the lower index. With check=True the
     call synchronises and raises ValueError if a row has no valid draw (a NaN
-    or +inf logit or setting, or no finite logit); else its token is -1.
+    or +inf logit, no finite one, a NaN setting, or a temperature that is
+    neither 0 nor a positive normal number); else its token is -1.
     """
     n, _, vt, ld, code = _rows("logits", logits, v_true)
     dev = logits.device

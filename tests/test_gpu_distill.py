@@ -105,6 +105,25 @@ def test_a_language_models_vocabulary(dtype):
     assert not grad[1].any()
 
 
+@pytest.mark.parametrize("T", [3, 300])
+def test_the_smallest_temperature(T):
+    """Loss and gradient scaled by it: the gradient stays in fp32's range."""
+    tau = 2.0 ** -126
+    rng = np.random.default_rng(12)
+    z = rng.normal(size=(T, 25001)) * 3 * tau
+    z[2] = rng.normal(size=25001) * 1e20       # the maximum alone is left
+    t, z = place(z, "fp32")
+    ids, x = teacher(1, np.clip(z / tau, -50, 50), 30)
+    x = (x.astype(np.float64) * tau).astype(np.float32)
+    ids[2, 0], ids[2, 1:], x[2, 0] = z[2].argmax(), -1, z[2].max()
+    w = rng.random(T).astype(np.float32)
+    di, dx, dw = dev(ids, torch.int64), dev(x, torch.float32), dev(w, torch.float32)
+    loss, grad = lp.distill_step(t, di, dx, dw, tau)
+    compare(z, ids, x, tau, True, loss, grad, w)
+    assert torch.isfinite(loss).all() and torch.isfinite(grad).all()
+    assert loss[2] == 0 and not grad[2].any()
+
+
 def test_autograd_and_differences():
     t, z = rows(9, 6, 700, "fp32")
     ids, x = teacher(3, z, 20)

@@ -135,6 +135,26 @@ def test_wide_rows():
     check(t, z, u, min_p=7.0)
 
 
+@pytest.mark.parametrize("how", [dict(), dict(top_k=50), dict(top_p=0.8), dict(min_p=0.1)])
+def test_the_smallest_temperature(how):
+    """Logits of its own size, and logits beside which it is as good as zero."""
+    tau = 2.0 ** -126
+    rng = np.random.default_rng(12)
+    z = rng.normal(size=(6, 9001)) * 4 * tau
+    z[4:] = rng.normal(size=(2, 9001)) * 1e20
+    t, z = place(z, "fp32")
+    check(t, z, rng.random(6, np.float32), tau, **how)
+
+
+def test_temperatures_that_are_none():
+    t, z = rows(8, 5, 500)
+    u = np.full(5, 0.5, np.float32)
+    tau = np.float32([1.0, 1e-45, 2.0 ** -127, np.inf, 2.0 ** -126])
+    for how in (dict(), dict(top_k=20), dict(min_p=0.05)):
+        got = check(t, z, u, tau, **how)
+        assert got[0].cpu().numpy()[1:4].tolist() == [-1, -1, -1]
+
+
 def test_rows_without_a_draw():
     z = np.random.default_rng(1).normal(size=(8, 300))
     z[0, 7], z[1, 299], z[2, :], z[3, 0] = np.nan, np.inf, -np.inf, -np.inf

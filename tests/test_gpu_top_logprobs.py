@@ -63,6 +63,13 @@ def test_ties_and_crowded_buckets(dtype, kind):
         check(t, z, k)
 
 
+def test_the_smallest_temperature():
+    tau = 2.0 ** -126
+    z = np.random.default_rng(12).normal(size=(4, 9001)) * 4 * tau
+    t, z = place(z, "fp32")
+    check(t, z, 50, tau)
+
+
 def test_masks_and_rows_without_logits():
     t, z = rows(6, 6, 3000, "fp32", masked=0.9)
     z[0, 20:] = -np.inf        # fewer finite logits than k

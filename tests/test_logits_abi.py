@@ -138,3 +138,9 @@ def test_binding_refuses_what_it_cannot_pass_on():
             call()
     with pytest.raises(ValueError, match="must not require gradients"):
         lp.distill(z, ids, x.clone().requires_grad_(True))
+
+
+@pytest.mark.parametrize("t", [2.0 ** -127, 1e-45, -1e-45])
+def test_subnormal_temperatures_are_refused(L, t):
+    for call in (sample, top, forward, backward, step):
+        assert call(L, t=t) == EINVAL, call
