@@ -19,6 +19,7 @@ may overlap, captured graphs among them, must not share one.
 from __future__ import annotations
 
 import torch
+from torch.autograd import forward_ad
 
 from ._lib import DISTILL_LOGPROBS, DISTILL_MAX_K, LP_OK, TOP_MAX, LpError, lib
 
@@ -295,12 +296,17 @@ def distill(logits: torch.Tensor, ids: torch.Tensor, teacher: torch.Tensor,
             v_true: int | None = None) -> torch.Tensor:
     """Distillation loss [T] fp32 against a teacher's top logits, differentiable
     once in the logits (arguments as for distill_forward; rows without an
-    entry have loss and gradient 0). The teacher gets no gradient. To record
+    entry have loss and gradient 0), in reverse mode: dual tensors of forward
+    mode raise NotImplementedError. The teacher gets no gradient. To record
     a step into a HIP graph, record distill_forward and distill_backward, or
     distill_step: an autograd graph of the same leaves must not be alive
     while a backward pass is being captured."""
     if isinstance(teacher, torch.Tensor) and teacher.requires_grad:
         raise ValueError("teacher must not require gradients")
+    for name, t in (("logits", logits), ("teacher", teacher)):
+        # (A dual tensor need not require gradients, and would lose its tangent.)
+        if isinstance(t, torch.Tensor) and forward_ad.unpack_dual(t).tangent is not None:
+            raise NotImplementedError(f"distill has no forward-mode derivative: {name} has a tangent")
     if logits.requires_grad and torch.is_grad_enabled():
         return _Distill.apply(logits, ids, teacher, temperature, renormalize, v_true)
     return distill_forward(logits, ids, teacher, temperature, renormalize, v_true)[0]
