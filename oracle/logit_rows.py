@@ -76,10 +76,11 @@ def top_logprobs(z, k, temperature=1.0):
         order = token_order(z[i])
         m = min(k, int(np.isfinite(z[i]).sum()))
         s = z[i] / tau
-        lse[i] = s.max() + np.log(np.exp(s - s.max()).sum())
+        log_sum = np.log(np.exp(s - s.max()).sum())
+        lse[i] = s.max() + log_sum
         ids[i, :m] = order[:m]
         val[i, :m] = z[i][order[:m]]
-        lp[i, :m] = s[order[:m]] - lse[i]
+        lp[i, :m] = s[order[:m]] - s.max() - log_sum  # (s - lse loses log_sum where s is large)
     return ids, val, lp, lse
 
 

@@ -59,6 +59,13 @@ def test_top_logprobs_brute_force():
     assert np.isclose(np.exp(lp[0]).sum(), 1.0)
 
 
+def test_top_logprobs_of_large_logits():
+    """ln 3 is not lost beside logits whose fp64 neighbours are 2^-13 apart and more."""
+    for z in (1e12, 2.0 ** 60, -1e15):
+        lp = ol.top_logprobs(np.full((1, 3), z), 2)[2]
+        assert np.all(np.abs(lp + np.log(3)) <= 1e-15), (z, lp)
+
+
 def test_distill_of_a_full_list_is_the_divergence():
     rng = np.random.default_rng(0)
     z, t = rng.normal(size=6), rng.normal(size=6)
