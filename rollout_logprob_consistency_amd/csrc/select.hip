@@ -313,10 +313,12 @@ __device__ __forceinline__ void sort_list(uint64_t* list, uint32_t m) {
 }
 
 // The log2 offset that a part of base m counts from: the integer next to m c
-// where that is small enough to be one, else m c itself. c = log2(e) / tau as
+// where fp32 has one (below 2^22, within 3/4; further out a rounded product is
+// off by up to 2^15, and every exponential 0 or infinite), else m c itself.
+// c = log2(e) / tau as
 // a float; it stands for the temperature wherever parts are used, so that its
 // rounding scales differences of logits and not the logits.
-__device__ __forceinline__ bool near_offset(float m, float c) { return fabsf(m * c) < 0x1p40f; }
+__device__ __forceinline__ bool near_offset(float m, float c) { return fabsf(m * c) < 0x1p22f; }
 __device__ __forceinline__ double offset_of(float m, float c) {
   return near_offset(m, c) ? (double)rintf(m * c) : (double)m * (double)c;
 }
