@@ -74,9 +74,12 @@ extern "C" {
  * nat: weights in fp64 (8e-14 relative), summed as 64-bit integers per bucket,
  * so sums do not depend on an order; tokens more than 39.9 nats below the
  * maximum may weigh 0 there (they still count for top_k and kept). The raw
- * score's sum over the vocabulary is, for short lists, of fp32 exponentials
- * joined in fp64 (about 1e-7 in the score; tested to 86 * 2^-24 + 2^-23 |score|),
- * else the buckets' (1e-12). Scores are rounded to fp32 once.
+ * score's sum over the vocabulary is, for short lists, fp64 for the listed
+ * tokens and the 16-byte groups that they lie in, and of fp32 exponentials
+ * joined in fp64 for the rest: an error of at most 210 * 2^-24, usually 1e-7, of
+ * the probability outside the list, so that the scores of near-certain tokens
+ * keep their digits. Else it is the buckets' (1e-12). Scores are rounded to fp32
+ * once.
  *
  * Layout: u [N] fp32; temperatures, top_ps, min_ps [N] fp32 and top_ks [N]
  * int32 give each row's settings, where NULL the scalar beside it holds for

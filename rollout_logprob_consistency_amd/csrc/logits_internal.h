@@ -219,7 +219,8 @@ struct RowFacts {
 
 // A base m and the sum of 2^(z c - offset(m)) over a wave's part of a chunk.
 struct SelectPart {
-  float m, s;
+  float m;
+  double s;
 };
 
 struct SelectArgs {

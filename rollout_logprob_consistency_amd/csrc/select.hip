@@ -6,9 +6,10 @@
 // By a short list (top_k in [1, 512], the greedy draw, min-p alone, and the top
 // logits): collect_kernel reads the row once, keeps the tokens
 // that can still be among the first in a list in LDS, and sums exp(z - m) per
-// wave and chunk for the log-sum-exp. The list is sorted; everything else is
-// decided in it, with weights and sums in fp64. Where there are few rows, a
-// row is cut into slices, each leaves its list, and row_kernel joins them.
+// wave and chunk for the log-sum-exp, which log_sum corrects by the listed
+// tokens. The list is sorted; everything else is decided in it, with weights
+// and sums in fp64. Where there are few rows, a row is cut into slices, each
+// leaves its list, and row_kernel joins them.
 //
 // By buckets (everything else, and rows whose list overflows): the weights are
 // collected in 2 048 buckets of 1/32 nat, a count and a mass each, placed so
@@ -79,6 +80,7 @@ struct Shared {
   union {
     unsigned long long mass[kSlots];
     double above[kBuckets + 1];
+    Part parts[kMaxParts];  // once a row's list is made
   };
   uint32_t cnt[kSlots];
   // The listed tokens, or the finer buckets of one that is too full to list.
@@ -88,7 +90,6 @@ struct Shared {
       unsigned long long fmass[kBuckets];
       uint32_t fcnt[kBuckets];
     };
-    Part parts[kMaxParts];
   };
   unsigned long long wave_u64[kWaves];
   double wave_f64[kWaves], shared_f64;
@@ -312,15 +313,27 @@ __device__ __forceinline__ void sort_list(uint64_t* list, uint32_t m) {
   }
 }
 
-// The log2 offset that a part of base m counts from: the integer next to m c
-// where fp32 has one (below 2^22, within 3/4; further out a rounded product is
-// off by up to 2^15, and every exponential 0 or infinite), else m c itself.
-// c = log2(e) / tau as
-// a float; it stands for the temperature wherever parts are used, so that its
-// rounding scales differences of logits and not the logits.
+// A part of base m counts its exponents z c from the integer next to m c where
+// fp32 has one (below 2^22, within 3/4; further out a rounded product is off by
+// up to 2^15, and every exponential 0 or infinite), else from m c itself by
+// differences of logits. c = log2(e) / tau as a float.
 __device__ __forceinline__ bool near_offset(float m, float c) { return fabsf(m * c) < 0x1p22f; }
-__device__ __forceinline__ double offset_of(float m, float c) {
-  return near_offset(m, c) ? (double)rintf(m * c) : (double)m * (double)c;
+struct Offset {
+  float base, b;  // exponents are (z - base) c - b
+};
+__device__ __forceinline__ Offset offset_of(float m, float c) {
+  const bool near = near_offset(m, c);
+  return {near || m == -INFINITY ? 0.0f : m, near ? rintf(m * c) : 0.0f};
+}
+
+// The sum of a group's exponentials: fp32, in order.
+template <class D>
+__device__ __forceinline__ float group_sum(const Group<D>& g, float c, Offset o) {
+  float s = __builtin_amdgcn_exp2f(fmaf(g.get(0) - o.base, c, -o.b));
+#pragma unroll
+  for (int i = 1; i < D::kVec; ++i)
+    s += __builtin_amdgcn_exp2f(fmaf(g.get(i) - o.base, c, -o.b));
+  return s;
 }
 
 // A chunk is gone through in blocks of eight places.
@@ -328,18 +341,21 @@ template <class D>
 constexpr int kBlocks = kGroups * D::kVec / 8;
 
 // The part of a wave whose lanes hold these groups: the same terms in the same
-// order wherever it is formed. Its base is the maximum of the first groups
-// alone, which spares most of a pass; where the sum gets out of 2^32, or is
-// none, it is formed again from the maximum of all. logit(z, e) sees the logit
-// of every place e of a block, block(k) the block's end.
+// order wherever it is formed, fp32 inside a group and fp64 from there on, so
+// that join_parts can take a group's sum out again. Its base is the maximum of
+// the first groups alone, which spares most of a pass; where the sum gets out
+// of 2^32, or is none, it is formed again from the maximum of all. logit(z, e)
+// sees the logit of every place e of a block, block(k) the block's end.
 template <class D, class F, class B>
 __device__ __forceinline__ Part part_of(Group<D> (&g)[kGroups], float c, F logit, B block) {
   float m = g[0].get(0);
 #pragma unroll
   for (int i = 1; i < D::kVec; ++i) m = fmaxf(m, g[0].get(i));
   m = wave_max_f32(m);
-  bool near = near_offset(m, c);
-  float b = near ? rintf(m * c) : 0.0f, s = 0.0f;
+  const bool near = near_offset(m, c);
+  const float b = near ? rintf(m * c) : 0.0f;
+  float gs = 0.0f;
+  double s = 0.0;
 #pragma unroll
   for (int k = 0; k < kBlocks<D>; ++k) {
 #pragma unroll
@@ -347,13 +363,15 @@ __device__ __forceinline__ Part part_of(Group<D> (&g)[kGroups], float c, F logit
       const int j = (k * 8 + e) / D::kVec, i = (k * 8 + e) % D::kVec;
       if (i == 0) g[j].fresh();
       const float z = g[j].get(i);
-      s += __builtin_amdgcn_exp2f(fmaf(z, c, -b));
+      const float t = __builtin_amdgcn_exp2f(fmaf(z, c, -b));
+      gs = i == 0 ? t : gs + t;
+      if (i == D::kVec - 1) s += (double)gs;
       logit(z, e);
     }
     block(k);
   }
-  s = wave_sum_f32(s);
-  if (!(s < 0x1p32f) || !near) {
+  s = wave_sum(s);
+  if (!(s < 0x1p32) || !near) {
 #pragma unroll
     for (int j = 0; j < kGroups; ++j) {
       g[j].fresh();
@@ -361,18 +379,14 @@ __device__ __forceinline__ Part part_of(Group<D> (&g)[kGroups], float c, F logit
       for (int i = 0; i < D::kVec; ++i) m = fmaxf(m, g[j].get(i));
     }
     m = wave_max_f32(m);
-    near = near_offset(m, c);
-    b = near ? rintf(m * c) : 0.0f;
-    const float base = near || m == -INFINITY ? 0.0f : m;  // masked tokens sum to 0
-    s = 0.0f;
+    const Offset o = offset_of(m, c);  // (masked tokens sum to 0)
+    s = 0.0;
 #pragma unroll
     for (int j = 0; j < kGroups; ++j) {
       g[j].fresh();
-#pragma unroll
-      for (int i = 0; i < D::kVec; ++i)
-        s += __builtin_amdgcn_exp2f(fmaf(g[j].get(i) - base, c, -b));
+      s += (double)group_sum<D>(g[j], c, o);
     }
-    s = wave_sum_f32(s);
+    s = wave_sum(s);
   }
   return {m, s};
 }
@@ -487,40 +501,56 @@ __device__ __forceinline__ void write_bad_top(const SelectArgs& a, int64_t n) {
   }
 }
 
-// log2 of the sum of all 2^(z c) as top + rest: top alone may be as large as
-// the logits, and the two are subtracted from a logit's z c one after the other.
-// rest is NaN where a NaN or +inf logit is, -inf where all are masked.
-struct Log2Sum {
-  double top, rest;
-};
-
-// The sum from a row's parts: fixed order, each part scaled in fp64.
-template <class P>  // parts in LDS or in global memory
-__device__ __forceinline__ Log2Sum join_parts(P parts, int n, float c, double* words) {
-  double top = -INFINITY;
-  for (int i = threadIdx.x; i < n; i += kThreads) top = fmax(top, offset_of(parts[i].m, c));
-#pragma unroll
-  for (int d = 32; d > 0; d >>= 1) top = fmax(top, __shfl_xor(top, d));
-  if ((threadIdx.x & 63) == 0) words[threadIdx.x >> 6] = top;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kWaves; ++w) top = fmax(top, words[w]);
-  __syncthreads();
+// ln of the sum of all exp((z - top) / tau), top the largest logit. NaN where a
+// NaN or +inf logit is.
+//
+// The parts' fp32 exponentials would leave an error of 1e-7 to 1e-6 of the whole
+// sum, which is all of a confident row's score. So the groups that hold a listed
+// token are taken out of their parts and summed again in fp64 (a group's largest
+// token does that; if any of a group is listed, it is). What is left of the
+// error is relative to the probability outside the listed groups. c's rounding
+// is confined the same way: a part's base goes into the sum with tau itself,
+// and differences inside the part alone with c. (2 304 bf16 rows of 151 936, k =
+// 64: 191 us with fp64 sums of groups and this, 183 us with fp32 sums alone; one
+// fp32 row 0.5 us more.)
+template <class D, class P>  // parts in LDS or in global memory
+__device__ __forceinline__ double log_sum(const Row<D>& row, P parts, const uint64_t* list,
+                                          uint32_t m, float tau, double* words) {
+  const float top = token_logit(list[0]), c = scale2_of(tau);
+  const double inv_tau = 1.0 / (double)tau;
+  // exp of a part's offset against top's.
+  auto scale_of = [&](float base) LP_INLINE {
+    double x = ((double)base - (double)top) * inv_tau;
+    if (near_offset(base, c))
+      x = fma(fma((double)base, -(double)c, (double)rintf(base * c)), 0.69314718055994531, x);
+    return exp_f64(x);
+  };
   double s = 0.0;
+  const int n = row.chunks() * kWaves;
   for (int i = threadIdx.x; i < n; i += kThreads) {
-    const float m = parts[i].m, t = parts[i].s;
-    s += m == -INFINITY ? (double)t
-                        : (double)t * exp_f64((offset_of(m, c) - top) * 0.69314718055994531);
+    const float base = parts[i].m;
+    const double t = parts[i].s;
+    s += base == -INFINITY ? t : t * scale_of(base);
+  }
+  for (uint32_t i = threadIdx.x; i < m; i += kThreads) {
+    const int idx = token_index(list[i]), first = idx - idx % D::kVec;
+    const Group<D> g = load_group<D>(row.p, first, row.V);
+    bool largest = true;
+#pragma unroll
+    for (int e = 0; e < D::kVec; ++e)
+      if (first + e != idx) largest &= token_key(g.get(e), first + e) < list[i];
+    if (!largest) continue;
+    const int at = idx % chunk_of<D>() / D::kVec % kThreads / 64;
+    const float base = parts[idx / chunk_of<D>() * kWaves + at].m;
+    double t = 0.0;
+#pragma unroll
+    for (int e = 0; e < D::kVec; ++e)
+      t += exp_f64(((double)g.get(e) - (double)top) * inv_tau);
+    s += t - (double)group_sum<D>(g, c, offset_of(base, c)) * scale_of(base);
   }
   double all;
   block_scan(s, words, &all);
-  if (top == -INFINITY) return {0.0, all == 0.0 ? -INFINITY : NAN};
-  return {top, log2(all)};
-}
-
-// The score of a logit under the whole vocabulary, from the sum's log2.
-__device__ __forceinline__ float score_of(float z, float c, const Log2Sum& all) {
-  return (float)(((double)z * (double)c - all.top - all.rest) * 0.69314718055994531);
+  return log(all < 1.0 ? 1.0 : all);  // top's own term is 1, the rest rounds; a NaN stays
 }
 
 // First index (of each thread's, then of all) with hit; n where there is none.
@@ -544,7 +574,7 @@ __device__ __forceinline__ uint32_t first_index(uint32_t* word, uint32_t n, uint
 // The draw from a sorted list that holds every token that can be kept.
 template <class Words>
 __device__ __forceinline__ void finish_draw(const SelectArgs& a, const Settings& st, int64_t n, const uint64_t* list,
-                            uint32_t m, const Log2Sum& all, Words& w) {
+                            uint32_t m, double ln_all, Words& w) {
   // Lists are no longer than kListMax here.
   constexpr int kEach = kListMax / kThreads;
   const double tau = (double)st.tau, top = (double)token_logit(list[0]);
@@ -593,7 +623,7 @@ __device__ __forceinline__ void finish_draw(const SelectArgs& a, const Settings&
     const uint64_t t = list[rank];
     const double s = ((double)token_logit(t) - top) / tau;
     a.out_token[n] = token_index(t);
-    a.out_logprob[n] = score_of(token_logit(t), scale2_of(st.tau), all);
+    a.out_logprob[n] = (float)(s - ln_all);
     if (a.out_processed) a.out_processed[n] = st.greedy ? 0.0f : (float)(s - log(mass));
     if (a.out_kept) a.out_kept[n] = (int32_t)kept;
   }
@@ -601,8 +631,8 @@ __device__ __forceinline__ void finish_draw(const SelectArgs& a, const Settings&
 
 // The first k tokens from a sorted list of m.
 __device__ __forceinline__ void finish_top(const SelectArgs& a, int64_t n, const uint64_t* list, uint32_t m,
-                           const Log2Sum& all) {
-  const float c = scale2_of(a.temperature);
+                           double ln_all) {
+  const double top = (double)token_logit(list[0]), tau = (double)a.temperature;
   for (uint32_t i = threadIdx.x; i < (uint32_t)a.top_k; i += kThreads) {
     const bool there = i < m;
     const uint64_t t = there ? list[i] : 0;
@@ -610,9 +640,9 @@ __device__ __forceinline__ void finish_top(const SelectArgs& a, int64_t n, const
     const int64_t o = n * a.top_k + i;
     a.out_ids[o] = there ? token_index(t) : -1;
     a.out_logits[o] = z;
-    a.out_logprob[o] = score_of(z, c, all);
+    a.out_logprob[o] = (float)(((double)z - top) / tau - ln_all);
   }
-  if (threadIdx.x == 0 && a.out_lse) a.out_lse[n] = -score_of(0.0f, c, all);
+  if (threadIdx.x == 0 && a.out_lse) a.out_lse[n] = (float)(top / tau + ln_all);
 }
 
 struct CollectShared {
@@ -826,15 +856,15 @@ __global__ __launch_bounds__(kThreads, 6) void collect_kernel(SelectArgs a) {
     if (tid == 0) count[slice] = m;
     return;
   }
-  const Log2Sum log2_all = join_parts(sh.parts, chunks * kWaves, scale2, sh.wave_f64);
   if (tid == 0) count[0] = 0;
-  if (m == 0 || isnan(log2_all.rest)) {
+  const double ln_all = m == 0 ? NAN : log_sum(row, sh.parts, sh.list, m, st.tau, sh.wave_f64);
+  if (isnan(ln_all)) {
     if (kTop) write_bad_top(a, n);
     else if (tid == 0) write_bad_draw(a, n);
   } else if (kTop) {
-    finish_top(a, n, sh.list, m, log2_all);
+    finish_top(a, n, sh.list, m, ln_all);
   } else {
-    finish_draw(a, st, n, sh.list, m, log2_all, sh);
+    finish_draw(a, st, n, sh.list, m, ln_all, sh);
   }
 }
 
@@ -1295,17 +1325,18 @@ __device__ __forceinline__ void draw_from_buckets(const SelectArgs& a, const Set
   }
 }
 
-// The parts of a row as collect_kernel forms them, into sh.parts; returns
-// their number.
+// The log-sum of a row with its list, its parts formed (over the buckets' masses)
+// as collect_kernel does.
 template <class D>
-__device__ __forceinline__ int parts_of_row(const Row<D>& row, float tau, Shared& sh) {
+__device__ __forceinline__ double log_sum_of_row(const Row<D>& row, float tau, Shared& sh, uint32_t m) {
   const float scale2 = scale2_of(tau);
+  __syncthreads();
   row.for_chunks(0, row.chunks(), [&](Group<D>(&g)[kGroups], int c) LP_INLINE {
     const Part p = part_of<D>(g, scale2, [](float, int) LP_INLINE {}, [](int) LP_INLINE {});
     if ((threadIdx.x & 63) == 0) sh.parts[c * kWaves + (threadIdx.x >> 6)] = p;
   });
   __syncthreads();
-  return row.chunks() * kWaves;
+  return log_sum(row, (const Part*)sh.parts, sh.list, m, tau, sh.wave_f64);
 }
 
 // A row of the short lists whose list overflowed: its tokens by selection,
@@ -1335,14 +1366,12 @@ __device__ __noinline__ void list_by_buckets(SelectArgs a, Settings st, int64_t 
         return;
       }
     }
-  const int parts = parts_of_row(row, st.tau, sh);
-  const Log2Sum log2_all = join_parts(sh.parts, parts, scale2_of(st.tau), sh.wave_f64);
   if constexpr (!kTop)
     if (st.kind == kMinP) {
-      const uint32_t m = gather(row, sh, lo, INFINITY, INFINITY, INFINITY);
+      const uint32_t m = sh.n_list;
       __syncthreads();
       sort_list(sh.list, m);
-      finish_draw(a, st, n, sh.list, m, log2_all, sh);
+      finish_draw(a, st, n, sh.list, m, log_sum_of_row(row, st.tau, sh, m), sh);
       return;
     }
   const uint32_t want = min(st.k, all.finite);
@@ -1371,8 +1400,9 @@ __device__ __noinline__ void list_by_buckets(SelectArgs a, Settings st, int64_t 
   }
   __syncthreads();
   sort_list(sh.list, m);
-  if constexpr (kTop) finish_top(a, n, sh.list, want, log2_all);
-  else finish_draw(a, st, n, sh.list, want, log2_all, sh);
+  const double ln_all = log_sum_of_row(row, st.tau, sh, want);
+  if constexpr (kTop) finish_top(a, n, sh.list, want, ln_all);
+  else finish_draw(a, st, n, sh.list, want, ln_all, sh);
 }
 
 // One row: its slices' lists or buckets joined, or the whole of it.
@@ -1463,16 +1493,15 @@ __device__ __forceinline__ void finish_row(const SelectArgs& a, int64_t n, Share
       return;
     }
   }
-  const int parts = row.chunks() * kWaves;
-  const Log2Sum log2_all = join_parts((Global<const Part>)(a.parts + n * parts), parts,
-                                     scale2_of(st.tau), sh.wave_f64);
-  if (m == 0 || isnan(log2_all.rest)) {
+  const Global<const Part> parts = (Global<const Part>)(a.parts + n * row.chunks() * kWaves);
+  const double ln_all = m == 0 ? NAN : log_sum(row, parts, sh.list, m, st.tau, sh.wave_f64);
+  if (isnan(ln_all)) {
     if constexpr (kTop) write_bad_top(a, n);
     else if (threadIdx.x == 0) write_bad_draw(a, n);
     return;
   }
-  if constexpr (kTop) finish_top(a, n, sh.list, m, log2_all);
-  else finish_draw(a, st, n, sh.list, m, log2_all, sh);
+  if constexpr (kTop) finish_top(a, n, sh.list, m, ln_all);
+  else finish_draw(a, st, n, sh.list, m, ln_all, sh);
 }
 
 template <class D, bool kTop>

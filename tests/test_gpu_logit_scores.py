@@ -52,3 +52,85 @@ def test_large_quotients(n, scale, tau):
     assert np.array_equal(ids.cpu().numpy(), r_ids)
     near(logp, r_lp, 2.0 ** -23 * np.abs(r_lp) + 86 * 2.0 ** -24)
     near(lse, r_lse, 2.0 ** -23 * np.abs(r_lse) + 86 * 2.0 ** -24)
+
+
+def scores(z, tau, listed):
+    """Per row: ln p of every token, the log-sum-exp, and the probability
+    outside the `listed` first tokens of the order; each sum from its smallest
+    term on, so that a confident row's small rest is not lost."""
+    logp, lse, rest = np.empty(z.shape), np.empty(len(z)), np.empty(len(z))
+    for i, row in enumerate(z):
+        s = (row - row.max()) / tau
+        w = np.sort(np.exp(s))
+        below = w[:w.size - listed[i]].sum()
+        others = w[:-1].sum()
+        logp[i] = s - np.log1p(others)
+        lse[i] = row.max() / tau + np.log1p(others)
+        rest[i] = below / (1 + others)
+    return logp, lse, rest
+
+
+def tolerance(ref, rest):
+    """The groups of the listed tokens are summed in fp64 (1e-13 and less in the
+    sum). What is outside them has fp32 exponentials 2^(z c - b): one rounding
+    of the exponent x, at most ln2 * 2^-24 |x| of a weight; c = log2 e / tau
+    rounded, ln2 * 2^-24 |x| too; 2^-23 for the exponential, at most 7 additions
+    of 2^-24. b is the integer next to the exponent of the largest logit among a
+    wave's first groups: |x| of the largest weight outside is at most 126 (smaller ones
+    weigh nothing), and weighted by the weights the others lie at most log2 V <=
+    17.3 below it. (2 ln2 (126 + 17.3) + 9) * 2^-24 <= 210 * 2^-24 of `rest`.
+    One rounding of the score to fp32."""
+    return 2.0 ** -24 * np.abs(ref) + 210 * 2.0 ** -24 * rest + 1e-13
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16", "fp16"])
+@pytest.mark.parametrize("n,v", [(1, 151936), (8, 30011), (300, 9001), (40, 257)])
+@pytest.mark.parametrize("gap", [0.0, 5.0, 12.0, 25.0])
+def test_confident_rows(dtype, n, v, gap):
+    """One token `gap` above the others: the score of a token that has nearly
+    all of the probability is the little that the others have."""
+    rng = np.random.default_rng(int(v + gap))
+    z = rng.normal(size=(n, v)) * 2.2
+    z[np.arange(n), rng.integers(0, v, n)] = z.max(1) + gap
+    t, z = place(z, dtype)
+    u = dev(rng.random(n, np.float32), F32)
+    for tau in (1.0, 0.7, 1.3):
+        tau = float(np.float32(tau))
+        rows = np.arange(n)
+        for how in (dict(top_k=20, top_p=0.95), dict(min_p=0.05), dict(greedy=True)):
+            if "greedy" in how:
+                token, raw, _, kept = lp.sample(t, u, 0.0)
+                listed, at = np.full(n, 1), 1.0
+            else:
+                token, raw, _, kept = lp.sample(t, u, tau, **how)
+                listed, at = np.full(n, 20) if "top_k" in how else kept.cpu().numpy(), tau
+            logp, _, rest = scores(z, at, listed)
+            ref = logp[rows, token.cpu().numpy()]
+            near(raw, ref, tolerance(ref, rest))
+            assert (raw <= 0).all()
+        for k in (1, 20, min(v, 700)):
+            lse = torch.empty(n, device=DEV)
+            ids, _, got = lp.top_logprobs(t, k, tau, lse=lse)
+            logp, r_lse, rest = scores(z, tau, np.full(n, k))
+            ref = np.take_along_axis(logp, ids.cpu().numpy(), 1)
+            near(got, ref, tolerance(ref, rest[:, None]))
+            near(lse, r_lse, tolerance(r_lse, rest))
+
+
+@pytest.mark.parametrize("n", [4, 300])
+def test_confident_rows_whose_list_overflows(n):
+    """More ties than a list holds, under tokens that have the probability."""
+    v = 20011
+    z = np.full((n, v), -30.0)
+    rng = np.random.default_rng(1)
+    for i in range(n):
+        z[i, rng.integers(0, v, 3)] = [1.0, 0.5, -14.0]
+    t, z = place(z)
+    u = dev(rng.random(n, np.float32), F32)
+    token, raw, _, _ = lp.sample(t, u, top_k=30)
+    logp, _, rest = scores(z, 1.0, np.full(n, 30))
+    ref = logp[np.arange(n), token.cpu().numpy()]
+    near(raw, ref, tolerance(ref, rest))
+    ids, _, got = lp.top_logprobs(t, 30)
+    ref = np.take_along_axis(logp, ids.cpu().numpy(), 1)
+    near(got, ref, tolerance(ref, rest[:, None]))
