@@ -13,7 +13,9 @@ Rows of logits are [N, columns] bfloat16, float16 or float32 with unit column
 stride and any row stride; `v_true` is the true vocabulary (columns behind it
 are padding). Scratch memory is allocated per call unless `workspace` is given
 (a uint8 tensor of the library's *_workspace_bytes, 256-byte aligned); calls that
-may overlap, captured graphs among them, must not share one.
+may overlap, captured graphs among them, must not share one. `bad_rows` (int32
+[1]) is a counter that a call adds its bad rows to; with check=True a call
+raises for its own rows only.
 """
 
 from __future__ import annotations
@@ -84,14 +86,18 @@ def _workspace(ws: torch.Tensor | None, need: int, device: torch.device) -> torc
 
 
 def _bad_rows(bad: torch.Tensor | None, check: bool, device: torch.device):
+    """What a call counts its bad rows in: with `check` a counter of its own,
+    as the caller's may hold the rows of earlier calls."""
     if bad is not None:
         _like("bad_rows", bad, (1,), torch.int32, device)
-        return bad
-    return torch.zeros(1, dtype=torch.int32, device=device) if check else None
+    return torch.zeros(1, dtype=torch.int32, device=device) if check else bad
 
 
-def _raise_bad(bad: torch.Tensor, what: str) -> None:
-    n = int(bad.item())
+def _raise_bad(count: torch.Tensor, bad: torch.Tensor | None, what: str) -> None:
+    """After a checked call: its count goes to the caller's counter, and raises."""
+    if bad is not None:
+        bad.add_(count)
+    n = int(count.item())
     if n:
         raise ValueError(f"{n} row(s) {what}")
 
@@ -124,14 +130,14 @@ def sample(logits: torch.Tensor, u: torch.Tensor, temperature=1.0, top_k=0, top_
     kept = torch.empty(n, dtype=torch.int32, device=dev)
     L = lib()
     ws = _workspace(workspace, L.lp_sample_workspace_bytes(n, vt, code), dev)
-    bad = _bad_rows(bad_rows, check, dev)
+    count = _bad_rows(bad_rows, check, dev)
     _call(L.lp_sample, dev,
           (logits.data_ptr(), ld, code, n, vt, pu, pt, float(temperature), pk, top_k, pp,
            float(top_p), pm, float(min_p), token.data_ptr(), logprob.data_ptr(),
-           processed.data_ptr(), kept.data_ptr(), None if bad is None else bad.data_ptr(),
+           processed.data_ptr(), kept.data_ptr(), None if count is None else count.data_ptr(),
            ws.data_ptr(), ws.numel() * ws.element_size()), "lp_sample")
     if check:
-        _raise_bad(bad, "have no valid draw")
+        _raise_bad(count, bad_rows, "have no valid draw")
     return token, logprob, processed, kept
 
 
@@ -156,13 +162,13 @@ def top_logprobs(logits: torch.Tensor, k: int, temperature: float = 1.0,
     logprobs = torch.empty((n, k), dtype=torch.float32, device=dev)
     L = lib()
     ws = _workspace(workspace, L.lp_top_logprobs_workspace_bytes(n, vt, code), dev)
-    bad = _bad_rows(bad_rows, check, dev)
+    count = _bad_rows(bad_rows, check, dev)
     _call(L.lp_top_logprobs, dev,
           (logits.data_ptr(), ld, code, n, vt, k, float(temperature), ids.data_ptr(),
-           values.data_ptr(), logprobs.data_ptr(), plse, None if bad is None else bad.data_ptr(),
+           values.data_ptr(), logprobs.data_ptr(), plse, None if count is None else count.data_ptr(),
            ws.data_ptr(), ws.numel() * ws.element_size()), "lp_top_logprobs")
     if check:
-        _raise_bad(bad, "have a NaN or infinite logit, or no finite one")
+        _raise_bad(count, bad_rows, "have a NaN or infinite logit, or no finite one")
     return ids, values, logprobs
 
 
@@ -220,14 +226,14 @@ def distill_forward(logits: torch.Tensor, ids: torch.Tensor, teacher: torch.Tens
     state = torch.empty((n, 4), dtype=torch.float64, device=dev)
     L = lib()
     ws = _workspace(workspace, L.lp_distill_workspace_bytes(n, vt, code), dev)
-    bad = _bad_rows(bad_rows, check, dev)
+    count = _bad_rows(bad_rows, check, dev)
     _call(L.lp_distill_forward, dev,
           (logits.data_ptr(), ld, code, n, vt, pi, pt, K, float(temperature),
            0 if renormalize else DISTILL_LOGPROBS, loss.data_ptr(), state.data_ptr(),
-           None if bad is None else bad.data_ptr(), ws.data_ptr(),
+           None if count is None else count.data_ptr(), ws.data_ptr(),
            ws.numel() * ws.element_size()), "lp_distill_forward")
     if check:
-        _raise_bad(bad, f"have a teacher id outside [0, {vt})")
+        _raise_bad(count, bad_rows, f"have a teacher id outside [0, {vt})")
     return loss, state
 
 
@@ -264,14 +270,14 @@ def distill_step(logits: torch.Tensor, ids: torch.Tensor, teacher: torch.Tensor,
     loss = torch.empty(n, dtype=torch.float32, device=dev)
     L = lib()
     ws = _workspace(workspace, L.lp_distill_workspace_bytes(n, vt, code), dev)
-    bad = _bad_rows(bad_rows, check, dev)
+    count = _bad_rows(bad_rows, check, dev)
     _call(L.lp_distill_step, dev,
           (logits.data_ptr(), ld, code, n, vt, columns, pi, pt, K, float(temperature),
            0 if renormalize else DISTILL_LOGPROBS, pw, loss.data_ptr(), out.data_ptr(), ldg,
-           None if bad is None else bad.data_ptr(), ws.data_ptr(),
+           None if count is None else count.data_ptr(), ws.data_ptr(),
            ws.numel() * ws.element_size()), "lp_distill_step")
     if check:
-        _raise_bad(bad, f"have a teacher id outside [0, {vt})")
+        _raise_bad(count, bad_rows, f"have a teacher id outside [0, {vt})")
     return loss, out
 
 

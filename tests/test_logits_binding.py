@@ -52,3 +52,22 @@ def test_tensors_without_a_tangent_pass(no_launch):
         forward_ad.make_dual(torch.ones(2), torch.ones(2))
         assert lp.distill(z, ids, x).shape == (3,)
         assert lp.distill(z.clone().requires_grad_(), ids, x).requires_grad
+
+
+@pytest.mark.parametrize("earlier", [0, 5])
+def test_a_checked_call_counts_apart_from_the_callers_counter(earlier):
+    """A counter that holds earlier calls' rows neither raises for them nor
+    loses a checked call's."""
+    cpu = torch.device("cpu")
+    bad = torch.full((1,), earlier, dtype=torch.int32)
+    count = binding._bad_rows(bad, True, cpu)
+    assert count is not bad and count.item() == 0
+    binding._raise_bad(count, bad, "are bad")             # a clean call
+    assert bad.item() == earlier
+    count = binding._bad_rows(bad, True, cpu)
+    count += 2                                            # a call with two
+    with pytest.raises(ValueError, match="^2 row"):
+        binding._raise_bad(count, bad, "are bad")
+    assert bad.item() == earlier + 2
+    assert binding._bad_rows(bad, False, cpu) is bad      # unchecked: counted there
+    assert binding._bad_rows(None, False, cpu) is None
