@@ -20,7 +20,8 @@
  *
  * Scratch memory: where a call takes a workspace, its contents on entry are
  * ignored, and calls that may overlap need one each (two captured graphs that
- * replay side by side too).
+ * replay side by side too). The *_workspace_bytes of a number of rows and a V_true
+ * serve every call of the same dtype with fewer of either, too.
  */
 #ifndef LIBLP_LOGITS_H
 #define LIBLP_LOGITS_H

@@ -31,8 +31,13 @@ size_t select_workspace_bytes(int64_t N, int64_t V_true, int32_t dtype) {
   if (N < 0 || N > kSelectMaxRows || V_true < 1 || V_true > LP_SELECT_MAX_VOCAB ||
       !dtype_ok(dtype))
     return 0;
-  const size_t total = lp::select_workspace_layout(N, V_true, dtype).total;
-  return total < 256 ? 256 : (total + 255) / 256 * 256;
+  const size_t most = lp::select_workspace_most(N, V_true, dtype);
+  return most < 256 ? 256 : most;
+}
+
+bool select_workspace_ok(const void* workspace, size_t bytes, int64_t N, int64_t V_true,
+                         int32_t dtype) {
+  return aligned(workspace, 256) && bytes >= lp::select_workspace_layout(N, V_true, dtype).total;
 }
 
 }  // namespace
@@ -60,8 +65,7 @@ lp_status lp_sample(const void* logits, int64_t ld, int32_t dtype, int64_t N, in
       !aligned(out_kept, 4) || !aligned(bad_rows, 4))
     return LP_EINVAL;
   if (V_true > LP_SELECT_MAX_VOCAB || N > kSelectMaxRows) return LP_EUNSUPPORTED;
-  if (!aligned(workspace, 256) || workspace_bytes < select_workspace_bytes(N, V_true, dtype))
-    return LP_EINVAL;
+  if (!select_workspace_ok(workspace, workspace_bytes, N, V_true, dtype)) return LP_EINVAL;
   lp::SelectArgs a = {};
   a.logits = logits;
   a.ld = ld;
@@ -101,8 +105,7 @@ lp_status lp_top_logprobs(const void* logits, int64_t ld, int32_t dtype, int64_t
       !aligned(out_logprob, 4) || !aligned(out_lse, 4) || !aligned(bad_rows, 4))
     return LP_EINVAL;
   if (k > LP_TOP_MAX || V_true > LP_SELECT_MAX_VOCAB || N > kSelectMaxRows) return LP_EUNSUPPORTED;
-  if (!aligned(workspace, 256) || workspace_bytes < select_workspace_bytes(N, V_true, dtype))
-    return LP_EINVAL;
+  if (!select_workspace_ok(workspace, workspace_bytes, N, V_true, dtype)) return LP_EINVAL;
   lp::SelectArgs a = {};
   a.logits = logits;
   a.ld = ld;

@@ -261,6 +261,9 @@ struct SelectWorkspace {
   size_t off_counts, off_parts, off_keys, off_masses, off_bucket_counts, off_facts, total;
 };
 SelectWorkspace select_workspace_layout(int64_t N, int64_t V, int32_t dtype);
+// Bytes that serve every number of rows up to N (fewer rows are cut into more
+// slices, so one layout may be larger than that of more rows).
+size_t select_workspace_most(int64_t N, int64_t V, int32_t dtype);
 
 // The token draw, or the top logits where u is null.
 hipError_t launch_select(SelectArgs a, void* workspace, hipStream_t stream);

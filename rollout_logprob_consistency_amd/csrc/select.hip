@@ -1549,35 +1549,52 @@ hipError_t launch(const SelectArgs& a, bool lists, bool buckets, hipStream_t str
 }  // namespace
 
 // Slices of a row. Rows that fill the card by themselves are not cut.
-static int select_slices(int64_t N, int64_t V, int32_t dtype) {
+constexpr int64_t kSelectPlaces = 512;
+static_assert(kSelectPlaces <= kMaxSlices, "slices of one row");
+static int64_t select_chunks(int64_t V, int32_t dtype) {
   const int64_t chunk = (int64_t)kThreads * kGroups * (16 / dtype_bytes(dtype));
-  const int64_t chunks = (V + chunk - 1) / chunk;
-  const int64_t most = std::min<int64_t>(chunks, kMaxSlices);
-  return (int)std::max<int64_t>(1, std::min<int64_t>(most, 512 / std::max<int64_t>(N, 1)));
+  return (V + chunk - 1) / chunk;
+}
+static int64_t select_slices(int64_t N, int64_t V, int32_t dtype) {
+  return std::max<int64_t>(
+      1, std::min(select_chunks(V, dtype), kSelectPlaces / std::max<int64_t>(N, 1)));
+}
+
+// A count per row or slice; parts of `cut_rows` rows and the rest of `cut_slices`
+// slices, which only cut rows need.
+static SelectWorkspace layout_of(size_t counts, size_t cut_rows, size_t cut_slices, size_t chunks) {
+  auto up = [](size_t b) { return (b + 255) / 256 * 256; };
+  SelectWorkspace w;
+  w.off_counts = 0;
+  w.off_parts = up(counts * sizeof(uint32_t));
+  w.off_keys = w.off_parts + up(cut_rows * chunks * kWaves * sizeof(Part));
+  w.off_masses = w.off_keys + up(cut_slices * kListMax * sizeof(uint64_t));
+  w.off_bucket_counts = w.off_masses + cut_slices * kBuckets * sizeof(unsigned long long);
+  w.off_facts = w.off_bucket_counts + cut_slices * kBuckets * sizeof(uint32_t);
+  w.total = up(w.off_facts + cut_slices * sizeof(RowFacts));
+  return w;
 }
 
 SelectWorkspace select_workspace_layout(int64_t N, int64_t V, int32_t dtype) {
-  const int64_t chunk = (int64_t)kThreads * kGroups * (16 / dtype_bytes(dtype));
-  const size_t chunks = (size_t)((V + chunk - 1) / chunk);
-  const int slices = select_slices(N, V, dtype);
-  const size_t lists = (size_t)N * (size_t)slices;
-  const size_t cut = slices > 1 ? 1 : 0;  // what only cut rows need
-  auto up = [](size_t b) LP_INLINE { return (b + 255) / 256 * 256; };
-  SelectWorkspace w;
-  w.off_counts = 0;
-  w.off_parts = up(lists * sizeof(uint32_t));
-  w.off_keys = w.off_parts + cut * up((size_t)N * chunks * kWaves * sizeof(Part));
-  w.off_masses = w.off_keys + cut * up(lists * kListMax * sizeof(uint64_t));
-  w.off_bucket_counts = w.off_masses + cut * lists * kBuckets * sizeof(unsigned long long);
-  w.off_facts = w.off_bucket_counts + cut * lists * kBuckets * sizeof(uint32_t);
-  w.total = w.off_facts + cut * up(lists * sizeof(RowFacts));
-  return w;
+  const int64_t slices = select_slices(N, V, dtype);
+  const size_t all = (size_t)(N * slices);
+  return layout_of(all, slices > 1 ? (size_t)N : 0, slices > 1 ? all : 0, select_chunks(V, dtype));
+}
+
+size_t select_workspace_most(int64_t N, int64_t V, int32_t dtype) {
+  // Every term of layout_of at its largest over 1 .. N rows.
+  const int64_t chunks = select_chunks(V, dtype);
+  const int64_t cut_rows = chunks > 1 ? std::min(N, kSelectPlaces / 2) : 0;
+  const int64_t cut_slices = std::min(kSelectPlaces, cut_rows * chunks);
+  return layout_of((size_t)std::max(N, cut_slices), (size_t)cut_rows, (size_t)cut_slices,
+                   (size_t)chunks)
+      .total;
 }
 
 hipError_t launch_select(SelectArgs a, void* workspace, hipStream_t stream) {
   const SelectWorkspace w = select_workspace_layout(a.N, a.V, a.dtype);
   char* base = static_cast<char*>(workspace);
-  a.slices = select_slices(a.N, a.V, a.dtype);
+  a.slices = (int32_t)select_slices(a.N, a.V, a.dtype);
   a.counts = reinterpret_cast<uint32_t*>(base + w.off_counts);
   a.parts = reinterpret_cast<SelectPart*>(base + w.off_parts);
   a.keys = reinterpret_cast<uint64_t*>(base + w.off_keys);

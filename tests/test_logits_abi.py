@@ -144,3 +144,20 @@ def test_binding_refuses_what_it_cannot_pass_on():
 def test_subnormal_temperatures_are_refused(L, t):
     for call in (sample, top, forward, backward, step):
         assert call(L, t=t) == EINVAL, call
+
+
+@pytest.mark.parametrize("dtype", [0, 1, 2])
+@pytest.mark.parametrize("V", [1, 1025, 9001, 151936, _lib.SELECT_MAX_VOCAB])
+def test_a_workspace_serves_fewer_rows_and_smaller_vocabularies(L, dtype, V):
+    """Sizes ascend with the rows and with the vocabulary: a caller's buffer for
+    its largest batch is not refused for a smaller one."""
+    rows = list(range(0, 700)) + [1000, 4096, 100000, 4194303]
+    for f in (L.lp_sample_workspace_bytes, L.lp_top_logprobs_workspace_bytes,
+              L.lp_distill_workspace_bytes):
+        sizes = [f(n, V, dtype) for n in rows]
+        assert sizes == sorted(sizes) and all(s % 256 == 0 for s in sizes)
+        for n in (1, 5, 39, 256, 257, 512, 513, 4096):
+            by_v = [f(n, v, dtype) for v in (1, 300, 4096, 4097, 8193, 30000, 151936, 1048576)]
+            assert by_v == sorted(by_v)
+    # Scratch memory stays within tens of megabytes, but for a row's counter.
+    assert L.lp_sample_workspace_bytes(4096, V, dtype) < 40 << 20
