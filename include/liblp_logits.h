@@ -79,8 +79,9 @@ extern "C" {
  * tokens and the 16-byte groups that they lie in, and of fp32 exponentials
  * joined in fp64 for the rest: an error of at most 210 * 2^-24, usually 1e-7, of
  * the probability outside the list, so that the scores of near-certain tokens
- * keep their digits. Else it is the buckets' (1e-12). Scores are rounded to fp32
- * once.
+ * keep their digits. Else it is the buckets': 1e-12, and the probability of the
+ * tokens more than 39.9 nats below the maximum (at most V_true e^-39.9, 5e-12).
+ * Scores are rounded to fp32 once.
  *
  * Layout: u [N] fp32; temperatures, top_ps, min_ps [N] fp32 and top_ks [N]
  * int32 give each row's settings, where NULL the scalar beside it holds for
