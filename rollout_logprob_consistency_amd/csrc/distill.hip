@@ -273,7 +273,7 @@ struct Entries {
       if (k < a.K && at[k] >= 0) {
         // An id that occurs again adds up; its first entry writes the sum. Four
         // entries a read tell whether there is one (step, 2 304 bf16 rows of
-        // 6 000, K = 256: 90 us instead of 141 us).
+        // 6 000, K = 256: 55 us, by single entries 57 us).
         const int32_t mine = at[k];
         double sum = q[k];
         bool first = true, again = false;
@@ -337,9 +337,9 @@ __global__ __launch_bounds__(kDistillThreads) void distill_backward_kernel(Disti
   entries.write(a, s, grad, out + begin, sh_at, sh_q);
 }
 
-// Measured on bf16 rows of 151 936: step over 2 048 rows 305 us (4.1 TB/s of
-// the bytes it cannot do without) against 375 us by the three kernels above,
-// loss of 4 096 rows 212 us (5.9 TB/s) against 254 us.
+// Measured on bf16 rows of 151 936: step over 2 048 rows 316 us (3.9 TB/s of
+// the bytes it cannot do without) against 361 us by the three kernels above,
+// loss of 4 096 rows 211 us (5.9 TB/s) against 267 us.
 //
 // Loss (and gradient) of one row: kRowWaves / kDistillWaves slices at a time,
 // each by as many threads, in the places and the order of the kernels above.

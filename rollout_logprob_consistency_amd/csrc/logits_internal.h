@@ -106,8 +106,9 @@ __device__ __forceinline__ Group<D> load_group(const typename D::Raw* p, int64_t
 
 template <class D>
 __device__ __forceinline__ void store_whole(typename D::Raw* p, const Group<D>& g) {
-  // Streamed past the caches: gradients are not read again soon (backward of
-  // 1 100 bf16 rows of 151 936 with its forward: 208 us instead of 219 us).
+  // Streamed past the caches: gradients are not read again soon (bf16 rows of
+  // 151 936, backward of 1 100 115 us and step over 2 048 319 us, with plain stores
+  // 127 us and 359 us).
   __builtin_nontemporal_store((Words{g.w[0], g.w[1], g.w[2], g.w[3]}), (Global<Words>)(Words*)p);
 }
 
@@ -157,10 +158,13 @@ constexpr int kDistillWaves = kDistillThreads / 64;
 constexpr int kDistillGroups = 4;  // 16-byte groups per thread and slice, at most
 // Forward and step take one workgroup per row from this many rows on, where the
 // row has at least three slices (with fewer, most of its 16 waves would idle:
-// step over 2 304 bf16 rows of 1 500, 47 us against 26 us by slices; of 12 000,
-// 59 us and 50 us; 1 000 rows of 20 000, three slices, 34 us against 36 us) and
-// at most kRowMaxSlices. With fewer rows, cutting them fills the card (500 fp32
-// rows of 50 021: 55 us by rows, 62 us by slices).
+// step over 2 304 bf16 rows of 1 500, 47 us against 27 us by slices; of 12 000,
+// 59 us and 49 us; 1 000 rows of 20 000, three slices, 34 us against 37 us) and
+// at most kRowMaxSlices. With few rows, cutting them fills the card. Step by rows
+// and by slices, bf16 rows of 151 936: 64 rows 32 us and 21 us, 128 33 and 33, 200
+// 40 and 45, 256 45 and 53, 300 62 and 59, 400 65 and 74, 2 048 316 and 360; fp32
+// rows of 50 021: 64 20 and 21, 255 34 and 41, 500 55 and 64. (Both fill the card
+// from 256 rows on; between 128 and 255 whole rows would gain up to a sixth.)
 constexpr int kRowWaves = 16;
 constexpr int64_t kRowMinRows = 256;
 constexpr int kRowMinSlices = 3;

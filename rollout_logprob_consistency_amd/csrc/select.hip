@@ -482,8 +482,9 @@ __device__ __forceinline__ float scale2_of(float tau) {
 
 // Slices of a row: every slice leaves at most k (kTopK) or kListMax tokens,
 // which have to fit one list together; half of it for kTopK, as sorting a
-// whole one costs more than the slices gain (64 bf16 rows of 151 936, k = 400:
-// 83 us with whole lists, 74 us with half).
+// whole one costs more than the slices gain (draws with top-k 400 over bf16 rows
+// of 151 936: 64 rows 83 us with whole lists and 71 us with half, 8 rows 109 us
+// and 59 us).
 __device__ __forceinline__ int slices_of(const SelectArgs& a, const Settings& s) {
   const int most = s.kind == kTopK ? kList / 2 / (int)s.k : kList / kListMax;
   return min(a.slices, max(most, 1));
@@ -784,7 +785,8 @@ __global__ __launch_bounds__(kThreads, 6) void collect_kernel(SelectArgs a) {
 
   // Loads are not taken ahead: with 80 registers three workgroups share a CU,
   // and their loads overlap each other's arithmetic (top 64 of 2 304 bf16 rows
-  // of 151 936: 224 us; with the next chunk in registers, 264 us).
+  // of 151 936: 194 us; with the next chunk in registers 206 us, or 223 us with
+  // the registers of two workgroups a CU).
   bool fits = !kTop || st.k <= (uint32_t)kShortTop;
   for (int c = c0; c < c1 && fits; ++c) {
     Group<D> g[kGroups];
@@ -1557,7 +1559,12 @@ hipError_t launch(const SelectArgs& a, bool lists, bool buckets, hipStream_t str
 
 }  // namespace
 
-// Slices of a row. Rows that fill the card by themselves are not cut.
+// Slices of a row: whole chunks, in all at most two workgroups for each of the
+// card's 256 CUs. Times with 256, 512, 768 and 1 024 workgroups at most: top 100 of
+// fp16 rows of 50 021, 100 rows 29, 30, 30 and 30 us, 200 rows 33, 34, 34 and 41, 300
+// rows 40, 40, 42 and 44, 400 rows 42, 41, 42 and 51; draws over rows of 151 936, 64
+// bf16 rows by top-k 20 30, 30, 27 and 27, 300 rows 55, 55, 52 and 53, 512 rows 61, 61,
+// 61 and 73; 64 fp32 rows by nucleus 93, 96, 97 and 103.
 constexpr int64_t kSelectPlaces = 512;
 static_assert(kSelectPlaces <= kMaxSlices, "slices of one row");
 static int64_t select_chunks(int64_t V, int32_t dtype) {

@@ -11,11 +11,12 @@ and every arithmetic step runs in the library's kernels.
 
 Rows of logits are [N, columns] bfloat16, float16 or float32 with unit column
 stride and any row stride; `v_true` is the true vocabulary (columns behind it
-are padding). Scratch memory is allocated per call unless `workspace` is given
-(a uint8 tensor of the library's *_workspace_bytes, 256-byte aligned); calls that
-may overlap, captured graphs among them, must not share one. `bad_rows` (int32
-[1]) is a counter that a call adds its bad rows to; with check=True a call
-raises for its own rows only.
+are padding). distill() alone is differentiable: the other calls' results carry
+no derivative, also where the logits require gradients. Scratch memory is
+allocated per call unless `workspace` is given (a uint8 tensor of the library's
+*_workspace_bytes, 256-byte aligned); calls that may overlap, captured graphs
+among them, must not share one. `bad_rows` (int32 [1]) is a counter that a call
+adds its bad rows to; with check=True a call raises for its own rows only.
 """
 
 from __future__ import annotations
@@ -114,7 +115,8 @@ def sample(logits: torch.Tensor, u: torch.Tensor, temperature=1.0, top_k=0, top_
     kept int32), each [N]. Ties go to the lower index. With check=True the
     call synchronises and raises ValueError if a row has no valid draw (a NaN
     or +inf logit, no finite one, a NaN setting, or a temperature that is
-    neither 0 nor a positive normal number); else its token is -1.
+    neither 0 nor a positive normal number); else its token is -1. The scores
+    are detached from the logits.
     """
     n, _, vt, ld, code = _rows("logits", logits, v_true)
     dev = logits.device
@@ -150,7 +152,8 @@ def top_logprobs(logits: torch.Tensor, k: int, temperature: float = 1.0,
     `temperature`), each [N, k]. A row with fewer finite logits ends in id -1
     and -inf. lse [N] fp32 receives the row's log-sum-exp. With check=True the
     call synchronises and raises ValueError if a row has a NaN or +inf logit
-    or no finite one; else its ids are -1 and its values NaN."""
+    or no finite one; else its ids are -1 and its values NaN. The results are
+    detached from the logits."""
     n, _, vt, ld, code = _rows("logits", logits, v_true)
     k = int(k)
     if not 1 <= k <= min(vt, TOP_MAX):
