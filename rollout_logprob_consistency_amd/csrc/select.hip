@@ -803,16 +803,23 @@ __global__ __launch_bounds__(kThreads, 6) void collect_kernel(SelectArgs a) {
       if (st.kind == kTopK) {
         // A first theta: with r = ceil(k / 8), the least of the eight waves'
         // r-th largest thread maximum is reached by k tokens of this chunk
-        // (with more than 256 wanted, of the four groups' maxima apart).
-        if (st.k > 256) {
-          const uint32_t r = (st.k + 4 * kWaves - 1) / (4 * kWaves);
-          tm = rth_largest(gm[0], r);
+        // (with more than 256 wanted, of the four groups' maxima apart: 32 sets
+        // of 64). In a chunk that the row ends in, of the sets that have a
+        // token in every lane.
+        const int groups = (min(row.V - c * chunk_of<D>(), chunk_of<D>())) / D::kVec;
+        const int sets = min(groups / 64, st.k > 256 ? kGroups * kWaves : kWaves);
+        const uint32_t r = (st.k + max(sets, 1) - 1) / max(sets, 1);
+        float least = INFINITY;
+        if (sets == 0 || r > 64) {
+          least = -INFINITY;  // too few tokens for a bound
+        } else if (st.k > 256) {
 #pragma unroll
-          for (int j = 1; j < kGroups; ++j) tm = fminf(tm, rth_largest(gm[j], r));
-        } else {
-          tm = rth_largest(tm, (st.k + kWaves - 1) / kWaves);
+          for (int j = 0; j < kGroups; ++j)
+            if (j * kWaves + wave < sets) least = fminf(least, rth_largest(gm[j], r));
+        } else if (wave < sets) {
+          least = rth_largest(tm, r);
         }
-        theta = bound(-block_max(-tm, sh.wave_f32));
+        theta = bound(-block_max(-least, sh.wave_f32));
       } else {
         theta = bound(block_max(tm, sh.wave_f32) - depth);
       }
