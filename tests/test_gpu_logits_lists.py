@@ -59,3 +59,15 @@ def test_many_wanted_of_a_chunk_that_the_row_ends_in(dtype, n, v):
     for k in (257, 300, 400):
         assert count(t, n, v, dtype, k, True) == 0, k
         assert count(t, n, v, dtype, k, False) == 0, k
+
+
+@pytest.mark.parametrize("n", [2, 300])
+def test_more_top_logits_than_a_list_are_not_collected(n):
+    """Longer lists than collect_kernel makes go by buckets at once: no slice is
+    collected and given up."""
+    t, _ = rows(n, n, 20011, "bf16")
+    for k in (513, 1024):
+        assert count(t, n, 20011, "bf16", k, False) == 0, k
+    for k in (511, 512):
+        ids = lp.top_logprobs(t, k)[0]
+        assert torch.equal(ids, lp.top_logprobs(t, 513)[0][:, :k])
