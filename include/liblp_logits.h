@@ -70,7 +70,7 @@ extern "C" {
  * NaN scores and kept 0, and is counted in bad_rows.
  *
  * Precision: what is kept and drawn is decided in fp64. Rows with top_k in
- * [1, 400], greedy ones and rows with min_p alone (at most 1 024 tokens kept)
+ * [1, 420], greedy ones and rows with min_p alone (at most 1 024 tokens kept)
  * go by a short list: fp64 weights and sums. The others go by buckets of 1/32
  * nat: weights in fp64 (8e-14 relative), summed as 64-bit integers per bucket,
  * so sums do not depend on an order; tokens more than 39.9 nats below the

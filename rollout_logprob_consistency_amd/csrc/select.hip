@@ -3,7 +3,7 @@
 //
 // Two ways through a row, chosen by its settings alone:
 //
-// By a short list (top_k in [1, 400], the greedy draw, min-p alone, and the top
+// By a short list (top_k in [1, 420], the greedy draw, min-p alone, and the top
 // logits): collect_kernel reads the row once, keeps the tokens
 // that can still be among the first in a list in LDS, and sums exp(z - m) per
 // wave and chunk for the log-sum-exp, which log_sum corrects by the listed
@@ -42,16 +42,14 @@ constexpr double kHead = 768.0;       // the anchor's place: 24 nats from the to
 constexpr int kPerThread = kBuckets / kThreads;
 constexpr int kList = 4096;           // tokens listed at once
 constexpr int kShort = 2048;          // ... by a workgroup of collect_kernel
-// Largest top_k of a draw that goes by short lists. From about 440 on, ordinary
-// rows list more than kShort before the first sort, and go twice. Lists against
-// buckets, 512 bf16 rows of 151 936: k = 300 108 us and 116 us, 400 116 and 117, 460
-// 211 and 119, 512 262 and 117; 512 rows of 262 144, k = 400 141 and 172; 64 rows of
-// 151 936, k = 300 65 and 60, 400 71 and 61, 512 154 and 61.
-constexpr int kShortDraw = 400;
-// The same of the top logits, whose lists are all that is asked for (512 bf16
-// rows: k = 400 113 us and 665 us, 480 401 and 673, 512 782 and 686; 64 rows: k =
-// 400 66 and 86, 512 148 and 89).
-constexpr int kShortTop = 512;
+// Largest top_k that goes by short lists. From about 440 on, ordinary rows list
+// more than kShort before the first sort, and are gone through twice. Lists
+// against buckets, bf16 rows of 151 936. Draws, 512 rows: k = 300 108 us and 116 us,
+// 420 119 and 117, 460 211 and 119, 512 262 and 117; 64 rows: 300 65 and 60, 420 84
+// and 61, 512 154 and 61 (512 rows of 262 144: 420 146 and 172). Top logits, 512
+// rows: 300 101 and 137, 420 112 and 140, 460 282 and 145, 512 778 and 150; 64 rows:
+// 420 79 and 81, 460 144 and 82; one row: 420 60 and 77, 512 62 and 80.
+constexpr int kShortTop = 420;
 constexpr int kListMax = LP_TOP_MAX;  // tokens that a slice leaves
 constexpr int kMaxSlices = 512;       // of a row
 constexpr uint32_t kOverflow = 0xFFFFFFFFu;    // a slice's count: take the buckets
@@ -463,7 +461,7 @@ __device__ __forceinline__ Settings settings_of(const SelectArgs& a, int64_t n) 
   s.k = s.greedy ? 1u : (uint32_t)max(s.top_k, 0);
   s.kind = kBuckets_;
   if (!s.bad) {
-    if (s.greedy || (s.top_k > 0 && s.top_k <= kShortDraw)) s.kind = kTopK;
+    if (s.greedy || (s.top_k > 0 && s.top_k <= kShortTop)) s.kind = kTopK;
     else if (s.top_k <= 0 && s.top_p >= 1.0f && s.min_p > 0.0f && s.min_p <= 1.0f) s.kind = kMinP;
   }
   return s;
@@ -1634,7 +1632,7 @@ hipError_t launch_select(SelectArgs a, void* workspace, hipStream_t stream) {
   const bool top = a.u == nullptr;
   // Which ways the rows can take, as far as the host sees the settings.
   const bool seen = !a.temperatures && !a.top_ks && !a.top_ps && !a.min_ps;
-  const bool short_list = a.temperature == 0.0f || (a.top_k > 0 && a.top_k <= kShortDraw) ||
+  const bool short_list = a.temperature == 0.0f || (a.top_k > 0 && a.top_k <= kShortTop) ||
                           (a.top_k <= 0 && a.top_p >= 1.0f && a.min_p > 0.0f && a.min_p <= 1.0f);
   const bool lists = top ? a.top_k <= kShortTop : !seen || short_list;
   const bool buckets = !top && (!seen || !short_list);
