@@ -3,13 +3,13 @@
 //
 // Two ways through a row, chosen by its settings alone:
 //
-// By a short list (top_k in [1, 420], the greedy draw, min-p alone, and the top
-// logits): collect_kernel reads the row once, keeps the tokens
-// that can still be among the first in a list in LDS, and sums exp(z - m) per
-// wave and chunk for the log-sum-exp, which log_sum corrects by the listed
-// tokens. The list is sorted; everything else is decided in it, with weights
-// and sums in fp64. Where there are few rows, a row is cut into slices, each
-// leaves its list, and row_kernel joins them.
+// By a short list (top_k in [1, 420], the greedy draw, min-p alone, and up to 420
+// top logits): collect_kernel reads the row once, keeps the tokens that can still
+// be among the first in a list in LDS, and sums exp(z - m) per wave and chunk for
+// the log-sum-exp, which log_sum corrects by the listed tokens. The list is
+// sorted; everything else is decided in it, with weights and sums in fp64. Where
+// there are few rows, a row is cut into slices, each leaves its list, and
+// row_kernel joins them.
 //
 // By buckets (everything else, and rows whose list overflows): the weights are
 // collected in 2 048 buckets of 1/32 nat, a count and a mass each, placed so
@@ -518,7 +518,9 @@ __device__ __forceinline__ void write_bad_top(const SelectArgs& a, int64_t n) {
 // token does that; if any of a group is listed, it is). What is left of the
 // error is relative to the probability outside the listed groups. c's rounding
 // is confined the same way: a part's base goes into the sum with tau itself,
-// and differences inside the part alone with c. (2 304 bf16 rows of 151 936, k =
+// and differences inside the part alone with c. Products that a sum follows are
+// fused here by name, as the same bits are due in every kernel that this is part
+// of. (2 304 bf16 rows of 151 936, k =
 // 64: 191 us with fp64 sums of groups and this, 183 us with fp32 sums alone; one
 // fp32 row 0.5 us more.)
 template <class D, class P>  // parts in LDS or in global memory
@@ -538,7 +540,7 @@ __device__ __forceinline__ double log_sum(const Row<D>& row, P parts, const uint
   for (int i = threadIdx.x; i < n; i += kThreads) {
     const float base = parts[i].m;
     const double t = parts[i].s;
-    s += base == -INFINITY ? t : t * scale_of(base);
+    s = base == -INFINITY ? s + t : fma(t, scale_of(base), s);
   }
   for (uint32_t i = threadIdx.x; i < m; i += kThreads) {
     const int idx = token_index(list[i]), first = idx - idx % D::kVec;
@@ -554,7 +556,7 @@ __device__ __forceinline__ double log_sum(const Row<D>& row, P parts, const uint
 #pragma unroll
     for (int e = 0; e < D::kVec; ++e)
       t += exp_f64(((double)g.get(e) - (double)top) * inv_tau);
-    s += t - (double)group_sum<D>(g, c, offset_of(base, c)) * scale_of(base);
+    s += fma(-(double)group_sum<D>(g, c, offset_of(base, c)), scale_of(base), t);
   }
   double all;
   block_scan(s, words, &all);
@@ -1369,10 +1371,9 @@ __device__ __noinline__ void list_by_buckets(SelectArgs a, Settings st, int64_t 
     else if (threadIdx.x == 0) write_bad_draw(a, n);
     return;
   }
-  float lo = 0.0f;
   if constexpr (!kTop)
     if (st.kind == kMinP) {
-      lo = bound(row.zmax - depth_of(st));
+      const float lo = bound(row.zmax - depth_of(st));
       // Far more than a short list holds, by the buckets above lo's alone, or
       // by the list itself.
       bool many = sh.cnt[Row<D>::bucket(row.x_of(lo))] > (uint32_t)kListMax;
@@ -1381,9 +1382,6 @@ __device__ __noinline__ void list_by_buckets(SelectArgs a, Settings st, int64_t 
         draw_from_buckets(a, st, n, row, all, sh);
         return;
       }
-    }
-  if constexpr (!kTop)
-    if (st.kind == kMinP) {
       const uint32_t m = sh.n_list;
       __syncthreads();
       sort_list(sh.list, m);
@@ -1395,7 +1393,7 @@ __device__ __noinline__ void list_by_buckets(SelectArgs a, Settings st, int64_t 
   uint32_t m = sh.cnt[b + 1];
   if (m <= (uint32_t)kList) {
     least_logits(row, sh, b, -1, -1, -1);
-    lo = sh.least[0];
+    const float lo = sh.least[0];
     m = gather(row, sh, lo, INFINITY, INFINITY, INFINITY);
   } else {
     // More than the list holds reach that bucket: up to the last token's key.
