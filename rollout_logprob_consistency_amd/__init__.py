@@ -23,6 +23,12 @@ On rows of logits (logits.py, include/liblp_logits.h):
     top_logprobs(logits, k, temperature)                  -> ids, logits, logprobs
     distill(logits, ids, teacher, ...)                    -> loss, differentiable
     distill_forward / distill_backward / distill_step     -> its directions by hand
+
+The LM head in 8-bit integers (int8.py, include/liblp_int8.h):
+
+    quantize_int8(x)                                      -> codes, scale
+    logits_int8(x, x_scale, w, w_scale, dtype)            -> rows of logits
+    score_int8(x, x_scale, w, w_scale, ids, ...)          -> logprob
 """
 
 from __future__ import annotations
@@ -36,6 +42,7 @@ import torch
 from ._lib import (CORR_SEQ_DTYPE, EXPORTS, LP_OK, REJECT_K1, REJECT_K3,  # noqa: F401
                    REJECT_NONE, SEQ_STATS_DTYPE, TAIL_STATS_DTYPE, WORST_DTYPE, WORST_MAX, LpError,
                    lib, status_string)
+from .int8 import logits_int8, quantize_int8, score_int8  # noqa: F401
 from .logits import (distill, distill_backward, distill_forward, distill_step, sample,  # noqa: F401
                      top_logprobs)
 

@@ -1,4 +1,5 @@
-"""ctypes declarations of the liblp C ABI (include/liblp.h, include/liblp_logits.h).
+"""ctypes declarations of the liblp C ABI (include/liblp.h, include/liblp_logits.h,
+include/liblp_int8.h).
 
 The shared library must have been built in-tree (build.py); importing the
 package without it raises, there is no fallback path.
@@ -29,6 +30,10 @@ EXPORTS = ("lp_status_string", "lp_score_workspace_bytes", "lp_score",
 LOGITS_EXPORTS = ("lp_sample_workspace_bytes", "lp_sample", "lp_top_logprobs_workspace_bytes",
                   "lp_top_logprobs", "lp_distill_workspace_bytes", "lp_distill_forward",
                   "lp_distill_backward", "lp_distill_step")
+
+# Names of every function include/liblp_int8.h declares.
+INT8_EXPORTS = ("lp_quantize_int8", "lp_logits_int8_workspace_bytes", "lp_logits_int8",
+                "lp_score_int8_workspace_bytes", "lp_score_int8")
 
 REJECT_NONE, REJECT_K1, REJECT_K3 = 0, 1, 3  # LP_REJECT_*
 
@@ -73,6 +78,7 @@ SELECT_MAX_VOCAB = 1048576  # LP_SELECT_MAX_VOCAB
 TOP_MAX = 1024  # LP_TOP_MAX
 DISTILL_MAX_K = 1024  # LP_DISTILL_MAX_K
 DISTILL_LOGPROBS = 1  # LP_DISTILL_LOGPROBS
+INT8_MAX_HIDDEN = 131071  # LP_INT8_MAX_HIDDEN
 NOALLOC_SCRATCH_BYTES = 32 << 20  # LP_NOALLOC_SCRATCH_BYTES
 
 
@@ -162,6 +168,16 @@ def lib() -> ctypes.CDLL:
     L.lp_distill_backward.argtypes = rows + [i64, vp, vp, i64, f32, u32, vp, vp, vp, i64, vp]
     L.lp_distill_step.argtypes = rows + [i64, vp, vp, i64, f32, u32, vp, vp, vp, i64, vp, vp, sz,
                                          vp]
+    L.lp_logits_int8_workspace_bytes.restype = sz
+    L.lp_logits_int8_workspace_bytes.argtypes = [i64, i64]
+    L.lp_score_int8_workspace_bytes.restype = sz
+    L.lp_score_int8_workspace_bytes.argtypes = [i64, i64, i64]
+    for name in ("lp_quantize_int8", "lp_logits_int8", "lp_score_int8"):
+        getattr(L, name).restype = ctypes.c_int
+    L.lp_quantize_int8.argtypes = [vp, i64, i32, i64, i64, vp, i64, vp, vp, vp]
+    operands = [vp, i64, vp, vp, i64, vp]  # x, ldx, x_scale, w, ldw, w_scale
+    L.lp_logits_int8.argtypes = operands + [i64, i64, i64, vp, i64, i32, vp, sz, vp]
+    L.lp_score_int8.argtypes = operands + [vp, i64, i64, i64, f32, u32, vp, vp, vp, vp, sz, vp]
     _lib = L
     return L
 
