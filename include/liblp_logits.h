@@ -1,6 +1,6 @@
 /*
- * liblp, operators on rows of logits: the token draw of a rollout, the top
- * logits of a scored position, and the distillation loss against a teacher's
+ * liblp, operators on rows of logits: the token draw of a rollout, the
+ * verification of drafted tokens, the top logits of a scored position, and the distillation loss against a teacher's
  * top logits with its gradient, for AMD Instinct MI355X (gfx950).
  *
  * The conventions are liblp.h's: C ABI, every pointer argument device memory
@@ -108,6 +108,73 @@ lp_status lp_sample(const void* logits, int64_t ld, int32_t dtype, int64_t N,
                     float min_p, int64_t* out_token, float* out_logprob,
                     float* out_processed, int32_t* out_kept, int32_t* bad_rows,
                     void* workspace, size_t workspace_bytes,
+                    hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Verification of drafted tokens
+ *
+ * Speculative decoding: a draft (a smaller model, or text copied from the
+ * prompt) proposes D tokens at most for each of B sequences, the target model
+ * scores all of them at once, and from given random numbers a prefix of them is
+ * accepted and one token more is drawn, so that every token that comes out is
+ * distributed as lp_sample's would be.
+ *
+ * Sequence b has n = counts[b] drafted tokens x_0 .. x_{n-1} (D where counts is
+ * NULL), the target's rows b (D + 1) + j, j <= n, and the draft model's rows
+ * b D + j, j < n, under one setting of temperature, top_k, top_p and min_p.
+ *
+ *   p_j(v)   the probability with which lp_sample draws v from the target's row
+ *            j: w_v / C(kept) for the kept tokens, 0 for the others
+ *   q_j(v)   the same of the draft's row j; without draft logits (NULL) 1 for
+ *            v = x_j: the draft proposes that token alone
+ *   x_j is accepted if all before it are and u[b, j] q_j(x_j) < p_j(x_j)
+ *   a        the number of accepted tokens
+ *   token a  the least v with  sum_{i <= v} r_i > u[b, D] sum_i r_i,  where
+ *            r_v = max(p_a(v) - q_a(v), 0) if a < n (p_a(v) where no r is
+ *            positive), and r_v = p_n(v) if a = n
+ *
+ * out_tokens [B, D + 1]: x_0 .. x_{a-1}, token a, then -1. out_accepted [B]: a.
+ * out_logprob, out_processed [B, D + 1]: ln of the token's probability under the
+ * target's full vocabulary at the temperature (as lp_sample's logprob,
+ * comparable with lp_score) and under p_j (as its processed score); 0 behind
+ * token a. Temperature 0 (greedy) has p and q concentrated on the lowest index
+ * of the largest logit, logprob at temperature 1 and processed 0. The random
+ * numbers are clamped to [0, 1 - 2^-24].
+ *
+ * A sequence whose count lies outside [0, D], whose drafted tokens (j < n) lie
+ * outside [0, V_true), whose rows (target j <= n, draft j < n) or settings have
+ * no valid draw (see lp_sample), or whose random numbers (j < n, and D) are NaN
+ * gives tokens -1, NaN scores and accepted -1, and is counted in bad_rows.
+ * Rows, ids and random numbers behind a sequence's drafts are not read.
+ *
+ * Precision: p and q in fp64, with C and the borders as lp_sample has them;
+ * acceptances, the sums over r and the last token are decided in fp64, sums in
+ * an order fixed by V_true and the dtype. Scores are rounded to fp32 once.
+ *
+ * Layout: draft_logits has the logits' dtype, row stride ld_draft; draft_ids
+ * [B, D] int64; u [B, D + 1] fp32; counts [B] int32 or NULL; settings as for
+ * lp_sample, arrays [B]; out_processed may be NULL. D may be 0 (draft_ids NULL).
+ * Workspace: at least lp_verify_workspace_bytes(B, D, V_true, dtype) bytes,
+ * 256-byte aligned.
+ *
+ * Errors: as for lp_sample, with D < 0 and ld_draft < V_true; LP_EUNSUPPORTED
+ * for D above LP_VERIFY_MAX_DRAFTS or B (2 D + 1) above 4 194 303. B == 0 does
+ * nothing.
+ * ------------------------------------------------------------------------ */
+#define LP_VERIFY_MAX_DRAFTS 63
+
+size_t lp_verify_workspace_bytes(int64_t B, int64_t D, int64_t V_true, int32_t dtype);
+
+lp_status lp_verify(const void* logits, int64_t ld, int32_t dtype, int64_t B,
+                    int64_t D, int64_t V_true, const void* draft_logits,
+                    int64_t ld_draft, const int64_t* draft_ids,
+                    const int32_t* counts, const float* u,
+                    const float* temperatures, float temperature,
+                    const int32_t* top_ks, int32_t top_k, const float* top_ps,
+                    float top_p, const float* min_ps, float min_p,
+                    int64_t* out_tokens, int32_t* out_accepted,
+                    float* out_logprob, float* out_processed,
+                    int32_t* bad_rows, void* workspace, size_t workspace_bytes,
                     hipStream_t stream);
 
 /* ------------------------------------------------------------------------

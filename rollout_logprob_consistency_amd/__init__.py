@@ -20,6 +20,7 @@ streams.
 On rows of logits (logits.py, include/liblp_logits.h):
 
     sample(logits, u, temperature, top_k, top_p, min_p)   -> token, logprob, processed, kept
+    verify(logits, draft_ids, u, draft_logits, ...)       -> tokens, accepted, logprob, processed
     top_logprobs(logits, k, temperature)                  -> ids, logits, logprobs
     distill(logits, ids, teacher, ...)                    -> loss, differentiable
     distill_forward / distill_backward / distill_step     -> its directions by hand
@@ -44,7 +45,7 @@ from ._lib import (CORR_SEQ_DTYPE, EXPORTS, LP_OK, REJECT_K1, REJECT_K3,  # noqa
                    lib, status_string)
 from .int8 import logits_int8, quantize_int8, score_int8  # noqa: F401
 from .logits import (distill, distill_backward, distill_forward, distill_step, sample,  # noqa: F401
-                     top_logprobs)
+                     top_logprobs, verify)
 
 PAIRS = ("AB", "BC", "AC")
 

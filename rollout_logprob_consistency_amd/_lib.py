@@ -27,9 +27,10 @@ EXPORTS = ("lp_status_string", "lp_score_workspace_bytes", "lp_score",
            "lp_compare_quantiles", "lp_score_noalloc")
 
 # Names of every function include/liblp_logits.h declares.
-LOGITS_EXPORTS = ("lp_sample_workspace_bytes", "lp_sample", "lp_top_logprobs_workspace_bytes",
-                  "lp_top_logprobs", "lp_distill_workspace_bytes", "lp_distill_forward",
-                  "lp_distill_backward", "lp_distill_step")
+LOGITS_EXPORTS = ("lp_sample_workspace_bytes", "lp_sample", "lp_verify_workspace_bytes",
+                  "lp_verify", "lp_top_logprobs_workspace_bytes", "lp_top_logprobs",
+                  "lp_distill_workspace_bytes", "lp_distill_forward", "lp_distill_backward",
+                  "lp_distill_step")
 
 # Names of every function include/liblp_int8.h declares.
 INT8_EXPORTS = ("lp_quantize_int8", "lp_logits_int8_workspace_bytes", "lp_logits_int8",
@@ -76,6 +77,7 @@ assert WORST_DTYPE.itemsize == 16
 WORST_MAX = 4096  # LP_WORST_MAX
 SELECT_MAX_VOCAB = 1048576  # LP_SELECT_MAX_VOCAB
 TOP_MAX = 1024  # LP_TOP_MAX
+VERIFY_MAX_DRAFTS = 63  # LP_VERIFY_MAX_DRAFTS
 DISTILL_MAX_K = 1024  # LP_DISTILL_MAX_K
 DISTILL_LOGPROBS = 1  # LP_DISTILL_LOGPROBS
 INT8_MAX_HIDDEN = 131071  # LP_INT8_MAX_HIDDEN
@@ -157,12 +159,16 @@ def lib() -> ctypes.CDLL:
                  "lp_distill_workspace_bytes"):
         getattr(L, name).restype = sz
         getattr(L, name).argtypes = [i64, i64, i32]
-    for name in ("lp_sample", "lp_top_logprobs", "lp_distill_forward", "lp_distill_backward",
-                 "lp_distill_step"):
+    L.lp_verify_workspace_bytes.restype = sz
+    L.lp_verify_workspace_bytes.argtypes = [i64, i64, i64, i32]
+    for name in ("lp_sample", "lp_verify", "lp_top_logprobs", "lp_distill_forward",
+                 "lp_distill_backward", "lp_distill_step"):
         getattr(L, name).restype = ctypes.c_int
     rows = [vp, i64, i32, i64, i64]  # logits, ld, dtype, rows, V_true
     L.lp_sample.argtypes = rows + [vp, vp, f32, vp, i32, vp, f32, vp, f32, vp, vp, vp, vp, vp,
                                    vp, sz, vp]
+    L.lp_verify.argtypes = [vp, i64, i32, i64, i64, i64, vp, i64, vp, vp, vp, vp, f32, vp, i32, vp,
+                            f32, vp, f32, vp, vp, vp, vp, vp, vp, sz, vp]
     L.lp_top_logprobs.argtypes = rows + [i32, f32, vp, vp, vp, vp, vp, vp, sz, vp]
     L.lp_distill_forward.argtypes = rows + [vp, vp, i64, f32, u32, vp, vp, vp, vp, sz, vp]
     L.lp_distill_backward.argtypes = rows + [i64, vp, vp, i64, f32, u32, vp, vp, vp, i64, vp]

@@ -89,6 +89,71 @@ lp_status lp_sample(const void* logits, int64_t ld, int32_t dtype, int64_t N, in
   return lp::launch_select(a, workspace, stream) == hipSuccess ? LP_OK : LP_EHIP;
 }
 
+size_t lp_verify_workspace_bytes(int64_t B, int64_t D, int64_t V_true, int32_t dtype) {
+  if (B < 0 || D < 0 || D > LP_VERIFY_MAX_DRAFTS || B > kSelectMaxRows / (2 * D + 1) ||
+      V_true < 1 || V_true > LP_SELECT_MAX_VOCAB || !dtype_ok(dtype))
+    return 0;
+  const size_t total = lp::verify_workspace_layout(B, D, V_true, dtype).total;
+  return total < 256 ? 256 : total;
+}
+
+lp_status lp_verify(const void* logits, int64_t ld, int32_t dtype, int64_t B, int64_t D,
+                    int64_t V_true, const void* draft_logits, int64_t ld_draft,
+                    const int64_t* draft_ids, const int32_t* counts, const float* u,
+                    const float* temperatures, float temperature, const int32_t* top_ks,
+                    int32_t top_k, const float* top_ps, float top_p, const float* min_ps,
+                    float min_p, int64_t* out_tokens, int32_t* out_accepted, float* out_logprob,
+                    float* out_processed, int32_t* bad_rows, void* workspace,
+                    size_t workspace_bytes, hipStream_t stream) {
+  if (B < 0 || D < 0 || V_true < 1 || ld < V_true || (draft_logits && ld_draft < V_true) ||
+      !dtype_ok(dtype))
+    return LP_EINVAL;
+  if (!temperatures && temperature != 0.0f && !temperature_ok(temperature)) return LP_EINVAL;
+  if ((!top_ps && isnan(top_p)) || (!min_ps && isnan(min_p))) return LP_EINVAL;
+  if (B == 0) return LP_OK;
+  if (!logits || (D > 0 && !draft_ids) || !u || !out_tokens || !out_accepted || !out_logprob ||
+      !workspace)
+    return LP_EINVAL;
+  if (!aligned(logits, size_of(dtype)) || !aligned(draft_logits, size_of(dtype)) ||
+      !aligned(draft_ids, 8) || !aligned(counts, 4) || !aligned(u, 4) ||
+      !aligned(temperatures, 4) || !aligned(top_ks, 4) || !aligned(top_ps, 4) ||
+      !aligned(min_ps, 4) || !aligned(out_tokens, 8) || !aligned(out_accepted, 4) ||
+      !aligned(out_logprob, 4) || !aligned(out_processed, 4) || !aligned(bad_rows, 4) ||
+      !aligned(workspace, 256))
+    return LP_EINVAL;
+  if (D > LP_VERIFY_MAX_DRAFTS || V_true > LP_SELECT_MAX_VOCAB ||
+      B > kSelectMaxRows / (2 * D + 1))
+    return LP_EUNSUPPORTED;
+  if (workspace_bytes < lp::verify_workspace_layout(B, D, V_true, dtype).total) return LP_EINVAL;
+  lp::VerifyArgs a = {};
+  lp::SelectArgs& r = a.rows;
+  r.logits = logits;
+  r.ld = ld;
+  r.dtype = dtype;
+  r.V = (int32_t)V_true;
+  r.temperatures = temperatures;
+  r.top_ks = top_ks;
+  r.top_ps = top_ps;
+  r.min_ps = min_ps;
+  r.temperature = temperature;
+  r.top_p = top_p;
+  r.min_p = min_p;
+  r.top_k = top_k;
+  r.draft_logits = D > 0 ? draft_logits : nullptr;
+  r.ld_draft = ld_draft;
+  r.seqs = B;
+  r.drafts = (int32_t)D;
+  r.draft_counts = counts;
+  a.draft_ids = draft_ids;
+  a.u = u;
+  a.out_tokens = out_tokens;
+  a.out_accepted = out_accepted;
+  a.out_logprob = out_logprob;
+  a.out_processed = out_processed;
+  a.bad_rows = bad_rows;
+  return lp::launch_verify(a, workspace, stream) == hipSuccess ? LP_OK : LP_EHIP;
+}
+
 size_t lp_top_logprobs_workspace_bytes(int64_t N, int64_t V_true, int32_t dtype) {
   return select_workspace_bytes(N, V_true, dtype);
 }

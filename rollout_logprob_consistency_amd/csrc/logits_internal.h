@@ -227,6 +227,16 @@ struct SelectPart {
   double s;
 };
 
+// Where the tokens that a draw from a row keeps end, and what they weigh: token v
+// has the probability exp((z_v - base) / tau - ln_kept) where its key (the order
+// of the selection) is at least `last`, else 0; its raw score is
+// (z_v - base) / tau - ln_all.
+struct SelectLimit {
+  uint64_t last;
+  double base, ln_kept, ln_all;
+};
+constexpr uint64_t kNoLimit = ~0ull;  // `last` of a row without a valid draw
+
 struct SelectArgs {
   const void* logits;
   int64_t ld;
@@ -259,6 +269,13 @@ struct SelectArgs {
   unsigned long long* masses;  // [N][slices][buckets]
   uint32_t* bucket_counts;     // [N][slices][buckets]
   RowFacts* facts;             // [N][slices]
+  // Limits of drafted sequences' rows, settings per sequence: `logits` are the
+  // targets' (drafts + 1 rows a sequence), N counts both kinds.
+  const void* draft_logits;
+  int64_t ld_draft, seqs;
+  int32_t drafts;
+  const int32_t* draft_counts;  // [seqs] or null: all of them
+  SelectLimit* limits;          // [N]
 };
 
 struct SelectWorkspace {
@@ -269,7 +286,38 @@ SelectWorkspace select_workspace_layout(int64_t N, int64_t V, int32_t dtype);
 // slices, so one layout may be larger than that of more rows).
 size_t select_workspace_most(int64_t N, int64_t V, int32_t dtype);
 
+// Sets the slices and the workspace's parts.
+void place_select(SelectArgs& a, void* workspace);
+// Which ways the draw's rows can take, as far as the host sees the settings.
+struct SelectWays {
+  bool lists, buckets;
+};
+SelectWays select_ways(const SelectArgs& a);
+
 // The token draw, or the top logits where u is null.
 hipError_t launch_select(SelectArgs a, void* workspace, hipStream_t stream);
+
+// ---- Verification of drafted tokens -----------------------------------------
+
+struct VerifyArgs {
+  SelectArgs rows;          // both models' rows and the settings
+  const int64_t* draft_ids; // [seqs, drafts]
+  const float* u;           // [seqs, drafts + 1]
+  int64_t* out_tokens;      // [seqs, drafts + 1]
+  int32_t* out_accepted;    // [seqs]
+  float* out_logprob;       // [seqs, drafts + 1]
+  float* out_processed;     // [seqs, drafts + 1] or null
+  int32_t* bad_rows;        // or null
+  // Set by launch_verify.
+  double* chunk_sums;       // [seqs][chunks]
+};
+
+struct VerifyWorkspace {
+  size_t off_select, off_limits, off_sums, total;
+};
+// Where a call's parts lie; `total` serves smaller calls too.
+VerifyWorkspace verify_workspace_layout(int64_t seqs, int64_t drafts, int64_t V, int32_t dtype);
+
+hipError_t launch_verify(VerifyArgs a, void* workspace, hipStream_t stream);
 
 }  // namespace lp

@@ -1,0 +1,383 @@
+// Verification of drafted tokens (lp_verify).
+//
+// With p_j what the target's row j would be drawn from and q_j the draft's, the
+// drafted token x_j is accepted where u_j q_j(x_j) < p_j(x_j); the first one that
+// is not is replaced by a draw from max(p - q, 0), and behind the last accepted
+// one a token is drawn from p. Either is found in index order: the least token
+// through which the weights pass u times their sum.
+//
+// The rows' limits (where the kept tokens end, and what they weigh) come from
+// the draw's own kernels. Two more launches end the call: residual_kernel sums
+// the weights of the one row (or two) that a sequence's last token is drawn from
+// by chunks, final_kernel finds the chunk and the token in it. Both look at the
+// drafts again: a few loads, against a launch that would only store the verdict.
+#include <algorithm>
+
+#include "select_row.h"
+
+namespace lp {
+namespace {
+
+constexpr int kVerifyThreads = 256;
+constexpr int kVerifyWaves = kVerifyThreads / 64;
+constexpr int kVerifyChunk = 4096;  // tokens summed at once
+constexpr int kEach = kVerifyChunk / kVerifyThreads;
+constexpr int64_t kVerifyPlaces = 16384;  // workgroups, at most, that sum chunks
+static_assert(LP_VERIFY_MAX_DRAFTS < 64, "a wave holds a sequence's positions");
+
+// The distribution that a row would be drawn from.
+struct Dist {
+  double base, inv_tau, ln_kept;
+  uint64_t last;
+
+  __device__ __forceinline__ double gap(float z) const { return ((double)z - base) * inv_tau; }
+  __device__ __forceinline__ bool keeps(float z, int v) const { return token_key(z, v) >= last; }
+  // Of a token that it keeps.
+  __device__ __forceinline__ double prob(float z) const { return exp_f64(gap(z) - ln_kept); }
+};
+
+struct Sequence {
+  int64_t b;
+  int count;     // drafts
+  int accepted;  // of them; -1: a sequence that has no verdict
+  bool greedy;
+  double inv_tau;
+};
+
+// The target's (at <= count) or the draft's (at < count) row of a sequence.
+__device__ __forceinline__ int64_t target_row(const VerifyArgs& a, int64_t b, int at) {
+  return b * (a.rows.drafts + 1) + at;
+}
+__device__ __forceinline__ int64_t draft_limit(const VerifyArgs& a, int64_t b, int at) {
+  return a.rows.seqs * (a.rows.drafts + 1) + b * a.rows.drafts + at;
+}
+__device__ __forceinline__ Dist dist_of(const VerifyArgs& a, const Sequence& s, int64_t limit) {
+  const SelectLimit l = a.rows.limits[limit];
+  return {l.base, s.inv_tau, l.ln_kept, l.last};
+}
+
+template <class D>
+__device__ __forceinline__ float logit_at(const void* logits, int64_t ld, int64_t row, int64_t v) {
+  return D::value(read_global(static_cast<const typename D::Raw*>(logits), row * ld + v));
+}
+
+// How far a sequence's drafts are accepted: lane j looks at position j. Every
+// wave of a workgroup finds the same.
+template <class D>
+__device__ __forceinline__ Sequence judge(const VerifyArgs& a, int64_t b) {
+  const SelectArgs& r = a.rows;
+  const int lane = threadIdx.x & 63;
+  Sequence s;
+  s.b = b;
+  s.count = r.draft_counts ? read_global(r.draft_counts, b) : r.drafts;
+  const float tau = r.temperatures ? read_global(r.temperatures, b) : r.temperature;
+  s.greedy = tau == 0.0f;
+  s.inv_tau = s.greedy ? 1.0 : 1.0 / (double)tau;
+  s.accepted = -1;
+  if (s.count < 0 || s.count > r.drafts) return s;
+  const int width = r.drafts + 1;
+  bool bad = lane == 63 && isnan(read_global(a.u, b * width + r.drafts)), passed = false;
+  if (lane <= s.count) {
+    bad |= r.limits[target_row(a, b, lane)].last == kNoLimit;
+    if (lane < s.count) {
+      const int64_t id = read_global(a.draft_ids, b * r.drafts + lane);
+      const float u = read_global(a.u, b * width + lane);
+      bad |= isnan(u) || id < 0 || id >= r.V;
+      if (r.draft_logits) bad |= r.limits[draft_limit(a, b, lane)].last == kNoLimit;
+      if (!bad) {
+        const float z = logit_at<D>(r.logits, r.ld, target_row(a, b, lane), id);
+        const Dist p = dist_of(a, s, target_row(a, b, lane));
+        const double px = p.keeps(z, (int)id) ? p.prob(z) : 0.0;
+        double qx = 1.0;
+        if (r.draft_logits) {
+          const float y = logit_at<D>(r.draft_logits, r.ld_draft, b * r.drafts + lane, id);
+          const Dist q = dist_of(a, s, draft_limit(a, b, lane));
+          qx = q.keeps(y, (int)id) ? q.prob(y) : 0.0;
+        }
+        passed = fmin(fmax((double)u, 0.0), 1.0 - 0x1p-24) * qx < px;
+      }
+    }
+  }
+  if (__ballot(bad)) return s;
+  const uint64_t rejected = ~__ballot(passed);  // (position `count` is one)
+  s.accepted = __ffsll((long long)rejected) - 1;
+  return s;
+}
+
+// The weights that a sequence's last token is drawn from, in its row.
+template <class D>
+struct Weights {
+  Dist p, q;
+  const typename D::Raw* target;
+  const typename D::Raw* draft;  // null: there is none
+  int64_t gone;                  // the token that weighs nothing, -1: none
+  int V;
+
+  // With `whole`, p itself.
+  __device__ __forceinline__ Weights(const VerifyArgs& a, const Sequence& s, bool whole) {
+    const SelectArgs& r = a.rows;
+    const int64_t t = target_row(a, s.b, s.accepted);
+    p = dist_of(a, s, t);
+    target = static_cast<const typename D::Raw*>(r.logits) + t * r.ld;
+    draft = nullptr;
+    gone = -1;
+    V = r.V;
+    if (whole || s.accepted == s.count) return;
+    const int64_t d = s.b * r.drafts + s.accepted;
+    if (r.draft_logits) {
+      draft = static_cast<const typename D::Raw*>(r.draft_logits) + d * r.ld_draft;
+      q = dist_of(a, s, draft_limit(a, s.b, s.accepted));
+    } else {
+      gone = read_global(a.draft_ids, d);  // the draft's whole probability
+    }
+  }
+  __device__ __forceinline__ double of(float z, float y, int v) const {
+    if (!p.keeps(z, v) || v == gone) return 0.0;
+    const double w = p.prob(z);
+    return draft && q.keeps(y, v) ? fmax(w - q.prob(y), 0.0) : w;
+  }
+  // The weights of the tokens from v on, kVec of them; 0 behind the row.
+  __device__ __forceinline__ void group(int v, double (&w)[D::kVec]) const {
+    const Group<D> z = load_group<D>(target, v, V);
+    Group<D> y = z;
+    if (draft) y = load_group<D>(draft, v, V);
+#pragma unroll
+    for (int i = 0; i < D::kVec; ++i) w[i] = v + i < V ? of(z.get(i), y.get(i), v + i) : 0.0;
+  }
+};
+
+// The sum of a chunk's weights, every thread's groups in order, then the threads.
+template <class D>
+__device__ __forceinline__ double chunk_sum(const Weights<D>& w, int chunk, double* words) {
+  double s = 0.0;
+#pragma unroll
+  for (int j = 0; j < kEach / D::kVec; ++j) {
+    const int v = chunk * kVerifyChunk + (j * kVerifyThreads + (int)threadIdx.x) * D::kVec;
+    double x[D::kVec];
+    w.group(v, x);
+#pragma unroll
+    for (int i = 0; i < D::kVec; ++i) s += x[i];
+  }
+  s = wave_sum(s);
+  if ((threadIdx.x & 63) == 0) words[threadIdx.x >> 6] = s;
+  __syncthreads();
+  s = words[0];
+#pragma unroll
+  for (int i = 1; i < kVerifyWaves; ++i) s += words[i];
+  __syncthreads();
+  return s;
+}
+
+template <class D>
+__global__ __launch_bounds__(kVerifyThreads) void residual_kernel(VerifyArgs a, int parts) {
+  __shared__ double words[kVerifyWaves];
+  const int64_t b = blockIdx.x / (uint32_t)parts;
+  const Sequence s = judge<D>(a, b);
+  if (s.accepted < 0) return;
+  const Weights<D> w(a, s, false);
+  const int chunks = (a.rows.V + kVerifyChunk - 1) / kVerifyChunk;
+  for (int c = (int)(blockIdx.x % (uint32_t)parts); c < chunks; c += parts) {
+    const double sum = chunk_sum(w, c, words);
+    if (threadIdx.x == 0) a.chunk_sums[b * chunks + c] = sum;
+  }
+}
+
+// Exclusive prefix sum over the workgroup.
+__device__ __forceinline__ double scan(double v, double* words, double* total) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  double s = v;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const double o = __shfl_up(s, d);
+    if (lane >= d) s += o;
+  }
+  double before = __shfl_up(s, 1);
+  if (lane == 0) before = 0.0;
+  if (lane == 63) words[wave] = s;
+  __syncthreads();
+  double base = 0.0, sum = 0.0;
+#pragma unroll
+  for (int w = 0; w < kVerifyWaves; ++w) {
+    if (w == wave) base = sum;
+    sum += words[w];
+  }
+  __syncthreads();
+  *total = sum;
+  return base + before;
+}
+
+struct FinalShared {
+  double words[kVerifyWaves], sums[LP_SELECT_MAX_VOCAB / kVerifyChunk];
+  double before;
+  int chunk, token, last;
+};
+
+// The least token through which the chunks' weights pass u times their sum; -1
+// where all weigh nothing. Where rounding leaves none, the last that weighs.
+template <class D>
+__device__ __forceinline__ int draw(const Weights<D>& w, double u, int chunks, FinalShared& sh) {
+  constexpr int kMost = LP_SELECT_MAX_VOCAB / kVerifyChunk;
+  static_assert(kMost <= kVerifyThreads, "a chunk for each thread");
+  const int tid = threadIdx.x;
+  const double mine = tid < chunks ? sh.sums[tid] : 0.0;
+  double total;
+  const double before = scan(mine, sh.words, &total);
+  if (!(total > 0.0)) return -1;
+  const double want = u * total;
+  if (tid == 0) {
+    sh.chunk = kMost;
+    sh.last = -1;
+    sh.token = INT32_MAX;
+  }
+  __syncthreads();
+  if (mine > 0.0) {
+    atomicMax(&sh.last, tid);
+    if (before + mine > want) atomicMin(&sh.chunk, tid);
+  }
+  __syncthreads();
+  const int chunk = sh.chunk < kMost ? sh.chunk : sh.last;
+  if (tid == chunk) sh.before = before;
+  __syncthreads();
+  if (tid == 0) sh.last = -1;
+  __syncthreads();
+  double base = sh.before;
+#pragma unroll
+  for (int j = 0; j < kEach / D::kVec; ++j) {
+    const int v = chunk * kVerifyChunk + (j * kVerifyThreads + tid) * D::kVec;
+    double x[D::kVec], sum = 0.0;
+    w.group(v, x);
+#pragma unroll
+    for (int i = 0; i < D::kVec; ++i) sum += x[i];
+    double all;
+    double c = base + scan(sum, sh.words, &all);
+    base += all;
+#pragma unroll
+    for (int i = D::kVec - 1; i >= 0; --i)
+      if (x[i] > 0.0) {
+        atomicMax(&sh.last, v + i);
+        break;
+      }
+#pragma unroll
+    for (int i = 0; i < D::kVec; ++i) {
+      c += x[i];
+      if (x[i] > 0.0 && c > want) {
+        atomicMin(&sh.token, v + i);
+        break;
+      }
+    }
+  }
+  __syncthreads();
+  return sh.token != INT32_MAX ? sh.token : sh.last;
+}
+
+template <class D>
+__global__ __launch_bounds__(kVerifyThreads) void final_kernel(VerifyArgs a) {
+  __shared__ FinalShared sh;
+  const SelectArgs& r = a.rows;
+  const int64_t b = blockIdx.x;
+  const int tid = threadIdx.x, width = r.drafts + 1;
+  const Sequence s = judge<D>(a, b);
+  const int64_t out = b * width + tid;
+  if (s.accepted < 0) {
+    if (tid < width) {
+      a.out_tokens[out] = -1;
+      a.out_logprob[out] = NAN;
+      if (a.out_processed) a.out_processed[out] = NAN;
+    }
+    if (tid == 0) {
+      a.out_accepted[b] = -1;
+      if (a.bad_rows) atomicAdd(a.bad_rows, 1);
+    }
+    return;
+  }
+  const int chunks = (r.V + kVerifyChunk - 1) / kVerifyChunk;
+  const double u =
+      fmin(fmax((double)read_global(a.u, b * width + r.drafts), 0.0), 1.0 - 0x1p-24);
+  if (tid < chunks) sh.sums[tid] = a.chunk_sums[b * chunks + tid];
+  __syncthreads();
+  int token = draw(Weights<D>(a, s, false), u, chunks, sh);
+  if (token < 0) {
+    // The target has nothing beyond the draft: a token of the target's own.
+    const Weights<D> w(a, s, true);
+    for (int c = 0; c < chunks; ++c) {
+      const double sum = chunk_sum(w, c, sh.words);
+      if (tid == 0) sh.sums[c] = sum;
+    }
+    __syncthreads();
+    token = draw(w, u, chunks, sh);
+  }
+  if (tid < width) {
+    float logprob = 0.0f, processed = 0.0f;
+    int64_t t = -1;
+    if (tid <= s.accepted) {
+      t = tid < s.accepted ? read_global(a.draft_ids, b * r.drafts + tid) : token;
+      const int64_t row = target_row(a, b, tid);
+      const SelectLimit l = r.limits[row];
+      const Dist p = {l.base, s.inv_tau, l.ln_kept, l.last};
+      const double gap = p.gap(logit_at<D>(r.logits, r.ld, row, t));
+      logprob = (float)(gap - l.ln_all);
+      processed = (float)(gap - l.ln_kept);
+    }
+    a.out_tokens[out] = t;
+    a.out_logprob[out] = logprob;
+    if (a.out_processed) a.out_processed[out] = processed;
+  }
+  if (tid == 0) a.out_accepted[b] = s.accepted;
+}
+
+template <class D>
+hipError_t launch(const VerifyArgs& a, hipStream_t stream) {
+  const SelectArgs& r = a.rows;
+  const SelectWays ways = select_ways(r);
+  hipError_t e;
+  if (ways.lists || r.slices > 1) {
+    collect_kernel<D, kLimit><<<dim3((uint32_t)(r.N * r.slices)), kThreads, 0, stream>>>(r);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+  }
+  row_kernel<D, kLimit><<<dim3((uint32_t)r.N), kThreads, 0, stream>>>(r);
+  if ((e = hipGetLastError()) != hipSuccess) return e;
+  const int64_t chunks = (r.V + kVerifyChunk - 1) / kVerifyChunk;
+  const int64_t parts = std::max<int64_t>(1, std::min(chunks, kVerifyPlaces / r.seqs));
+  residual_kernel<D><<<dim3((uint32_t)(r.seqs * parts)), kVerifyThreads, 0, stream>>>(a,
+                                                                                    (int)parts);
+  if ((e = hipGetLastError()) != hipSuccess) return e;
+  final_kernel<D><<<dim3((uint32_t)r.seqs), kVerifyThreads, 0, stream>>>(a);
+  return hipGetLastError();
+}
+
+size_t up(size_t b) { return (b + 255) / 256 * 256; }
+
+VerifyWorkspace layout_of(size_t select, int64_t rows, int64_t seqs, int64_t V) {
+  VerifyWorkspace w;
+  w.off_select = 0;
+  w.off_limits = up(select);
+  w.off_sums = w.off_limits + up((size_t)rows * sizeof(SelectLimit));
+  w.total = w.off_sums +
+            up((size_t)seqs * (size_t)((V + kVerifyChunk - 1) / kVerifyChunk) * sizeof(double));
+  return w;
+}
+
+}  // namespace
+
+VerifyWorkspace verify_workspace_layout(int64_t seqs, int64_t drafts, int64_t V, int32_t dtype) {
+  // (Without a draft model fewer rows have limits; the layout is the same.)
+  const int64_t rows = seqs * (2 * drafts + 1);
+  return layout_of(select_workspace_most(rows, V, dtype), rows, seqs, V);
+}
+
+hipError_t launch_verify(VerifyArgs a, void* workspace, hipStream_t stream) {
+  SelectArgs& r = a.rows;
+  const VerifyWorkspace w = verify_workspace_layout(r.seqs, r.drafts, r.V, r.dtype);
+  char* base = static_cast<char*>(workspace);
+  r.N = r.seqs * (r.drafts + 1) + (r.draft_logits ? r.seqs * r.drafts : 0);
+  r.limits = reinterpret_cast<SelectLimit*>(base + w.off_limits);
+  a.chunk_sums = reinterpret_cast<double*>(base + w.off_sums);
+  place_select(r, base + w.off_select);
+  switch (r.dtype) {
+    case LP_F32: return launch<F32>(a, stream);
+    case LP_BF16: return launch<BF16>(a, stream);
+    default: return launch<F16>(a, stream);
+  }
+}
+
+}  // namespace lp

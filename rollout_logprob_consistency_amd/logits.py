@@ -4,6 +4,8 @@ A thin binding like the rest of the package: it checks and marshals arguments,
 and every arithmetic step runs in the library's kernels.
 
     sample(logits, u, temperature, top_k, top_p, min_p)  -> token, logprob, processed, kept
+    verify(logits, draft_ids, u, draft_logits, counts, ...)
+                                                         -> tokens, accepted, logprob, processed
     top_logprobs(logits, k, temperature)                 -> ids, logits, logprobs [N, k]
     distill(logits, ids, teacher, ...)                   -> loss [T], differentiable
     distill_forward / distill_backward                   -> the two directions by hand
@@ -24,7 +26,8 @@ from __future__ import annotations
 import torch
 from torch.autograd import forward_ad
 
-from ._lib import DISTILL_LOGPROBS, DISTILL_MAX_K, LP_OK, TOP_MAX, LpError, lib
+from ._lib import (DISTILL_LOGPROBS, DISTILL_MAX_K, LP_OK, TOP_MAX, VERIFY_MAX_DRAFTS, LpError,
+                   lib)
 
 _DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}  # LP_F32, LP_BF16, LP_F16
 
@@ -141,6 +144,71 @@ def sample(logits: torch.Tensor, u: torch.Tensor, temperature=1.0, top_k=0, top_
     if check:
         _raise_bad(count, bad_rows, "have no valid draw")
     return token, logprob, processed, kept
+
+
+def verify(logits: torch.Tensor, draft_ids: torch.Tensor, u: torch.Tensor,
+           draft_logits: torch.Tensor | None = None, counts: torch.Tensor | None = None,
+           temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, v_true: int | None = None, *,
+           workspace: torch.Tensor | None = None, bad_rows: torch.Tensor | None = None,
+           check: bool = False):
+    """Drafted tokens verified against the target's rows (lp_verify): of the
+    draft_ids [B, D] int64 a prefix is accepted and one token more is drawn, so
+    that every token is distributed as sample()'s would be.
+
+    logits [B * (D + 1), columns] are the target's, D + 1 rows a sequence;
+    draft_logits [B * D, columns] the draft model's in the same dtype, or None
+    for tokens that were copied, not drawn. u [B, D + 1] fp32: one uniform random
+    number per drafted token, and the last column for the token that is drawn.
+    counts [B] int32: a sequence's drafted tokens, where they are fewer than D.
+    temperature, top_p, min_p (fp32) and top_k (int32) are numbers or tensors
+    [B], as sample() takes them, for both models' rows.
+
+    Returns (tokens int64 [B, D + 1]: the accepted ones, the drawn one, then -1;
+    accepted int32 [B]; logprob fp32 [B, D + 1] under the full vocabulary;
+    processed fp32 [B, D + 1] under the kept tokens; scores are 0 behind the
+    drawn token). With check=True the call synchronises and raises ValueError if
+    a sequence has no verdict (see lp_verify); else its tokens and accepted are
+    -1. The scores are detached from the logits.
+    """
+    n, _, vt, ld, code = _rows("logits", logits, v_true)
+    dev = logits.device
+    if not isinstance(draft_ids, torch.Tensor) or draft_ids.dim() != 2:
+        raise ValueError("expected draft_ids [B, D]")
+    b, d = draft_ids.shape
+    if d > VERIFY_MAX_DRAFTS:
+        raise ValueError(f"D must be at most {VERIFY_MAX_DRAFTS}")
+    if n != b * (d + 1):
+        raise ValueError(f"logits must have B * (D + 1) = {b * (d + 1)} rows, got {n}")
+    pi = _like("draft_ids", draft_ids, (b, d), torch.int64, dev)
+    pu = _like("u", u, (b, d + 1), torch.float32, dev)
+    pc = None if counts is None else _like("counts", counts, (b,), torch.int32, dev)
+    pq, ldq = None, 0
+    if draft_logits is not None and b * d > 0:
+        m, columns, _, ldq, draft_code = _rows("draft_logits", draft_logits, None)
+        if m != b * d or columns < vt or draft_code != code or draft_logits.device != dev:
+            raise ValueError(f"draft_logits must be [{b * d}, at least {vt}] in the logits' dtype "
+                             "and on their device")
+        pq = draft_logits.data_ptr()
+    pt, temperature = _setting("temperature", temperature, b, torch.float32, dev)
+    pk, top_k = _setting("top_k", top_k, b, torch.int32, dev)
+    pp, top_p = _setting("top_p", top_p, b, torch.float32, dev)
+    pm, min_p = _setting("min_p", min_p, b, torch.float32, dev)
+    top_k = max(-1, min(int(top_k), 2 ** 31 - 1))
+    tokens = torch.empty((b, d + 1), dtype=torch.int64, device=dev)
+    accepted = torch.empty(b, dtype=torch.int32, device=dev)
+    logprob = torch.empty((b, d + 1), dtype=torch.float32, device=dev)
+    processed = torch.empty((b, d + 1), dtype=torch.float32, device=dev)
+    L = lib()
+    ws = _workspace(workspace, L.lp_verify_workspace_bytes(b, d, vt, code), dev)
+    count = _bad_rows(bad_rows, check, dev)
+    _call(L.lp_verify, dev,
+          (logits.data_ptr(), ld, code, b, d, vt, pq, ldq, pi, pc, pu, pt, float(temperature), pk,
+           top_k, pp, float(top_p), pm, float(min_p), tokens.data_ptr(), accepted.data_ptr(),
+           logprob.data_ptr(), processed.data_ptr(), None if count is None else count.data_ptr(),
+           ws.data_ptr(), ws.numel() * ws.element_size()), "lp_verify")
+    if check:
+        _raise_bad(count, bad_rows, "have no verdict")
+    return tokens, accepted, logprob, processed
 
 
 def top_logprobs(logits: torch.Tensor, k: int, temperature: float = 1.0,
