@@ -39,7 +39,8 @@ extern "C" {
  * For every row r of x (LP_F32, LP_BF16 or LP_F16, row stride ldx, any
  * alignment of the element type):
  *
- *   scale[r] = max_k |x[r, k]| / 127, rounded to fp32
+ *   scale[r] = max_k |x[r, k]| times the fp32 number nearest to 1/127, rounded
+ *              to fp32
  *   q[r, k]  = the integer nearest to x[r, k] / scale[r] (the quotient of the
  *              real numbers, ties to even), within [-127, 127]
  *

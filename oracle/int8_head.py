@@ -20,7 +20,7 @@ def quantize(x):
     for r, row in enumerate(x):
         if not np.isfinite(row).all():
             continue
-        scale[r] = np.abs(row).max() / np.float32(127)
+        scale[r] = np.abs(row).max() * (np.float32(1) / np.float32(127))
         if scale[r] > 0:
             ratio = row.astype(np.float64) / np.float64(scale[r])
             codes[r] = np.clip(np.rint(ratio), -127, 127).astype(np.int8)

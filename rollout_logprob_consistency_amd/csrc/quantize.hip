@@ -1,6 +1,6 @@
 // Rows in 8-bit integers with a scale each (lp_quantize_int8).
 //
-//   scale = max |x| / 127,   q = the integer nearest to x / scale
+//   scale = max |x| (1 / 127),   q = the integer nearest to x / scale
 //
 // One pass: a wave holds its row in registers between the maximum and the
 // codes, so the row is read once (longer rows are read again, from L2).
@@ -75,7 +75,7 @@ __global__ __launch_bounds__(kThreads) void quantize_kernel(QuantizeArgs a) {
   }
   m = wave_max_f32(m);
   const bool bad = __ballot(odd) != 0;
-  float s = bad ? 0.0f : m / 127.0f;
+  float s = bad ? 0.0f : m * (1.0f / 127.0f);
   if (lane == 0) {
     a.scale[row] = bad ? NAN : s;
     if (bad && a.bad_rows) atomicAdd(a.bad_rows, 1);

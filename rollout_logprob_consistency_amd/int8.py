@@ -54,8 +54,8 @@ def quantize_int8(x: torch.Tensor, *, out: torch.Tensor | None = None,
                   scale: torch.Tensor | None = None, bad_rows: torch.Tensor | None = None,
                   check: bool = False):
     """Rows in 8 bits (lp_quantize_int8): (codes int8 [R, H], scale fp32 [R]),
-    scale = max |x| / 127 of the row and codes the integers nearest to
-    x / scale, ties to even.
+    scale = max |x| / 127 of the row (by fp32's reciprocal of 127) and codes the
+    integers nearest to x / scale, ties to even.
 
     x [R, H] bf16, fp16 or fp32 with unit column stride and any row stride. The
     codes' rows start at multiples of 16 bytes; `out` (and `scale`) may be given

@@ -63,7 +63,7 @@ def test_borders_under_awkward_scales():
     rows = []
     for _ in range(64):
         top = np.float32(rng.uniform(1, 2) * 2.0 ** rng.integers(-100, 100))
-        s = np.float64(top / np.float32(127))
+        s = np.float64(top * (np.float32(1) / np.float32(127)))
         near = ((rng.integers(-126, 126, 255) + 0.5) * s).astype(np.float32)
         near = np.where(rng.random(255) < 0.5, near, np.nextafter(near, np.float32(0)))
         rows.append(np.concatenate([[top], near]))
