@@ -7,9 +7,9 @@ file, with hipcc for gfx950. Packed-fp32 instructions are disabled for all
 device code. The device assembly of score.hip is then checked for wait-state
 hazards around its inline-assembly MFMAs (isa_check.py); a violation fails
 the build. The comparison kernel's assembly is checked for ds_bpermute (its
-reductions use DPP, ds_swizzle and readlane). Both files' buffer -> LDS copies
-(inline assembly) are checked for VALU writes of their SGPR operands fewer than
-5 wait states before them.
+reductions use DPP, ds_swizzle and readlane). These files' and int8.hip's buffer
+-> LDS copies (inline assembly) are checked for VALU writes of their SGPR
+operands fewer than 5 wait states before them.
 """
 
 from __future__ import annotations
@@ -73,6 +73,7 @@ def build(verbose: bool = False, extra: list[str] | None = None) -> str:
         futs = [ex.submit(compile_one, so) for so in zip(srcs, objs)]
         futs.append(ex.submit(check_score_isa, objdir, extra, verbose))
         futs.append(ex.submit(check_compare_isa, objdir, extra, verbose))
+        futs.append(ex.submit(check_int8_isa, objdir, extra, verbose))
         for f in futs:
             f.result()
     tmp = LIB + ".tmp"
@@ -124,6 +125,22 @@ def check_compare_isa(objdir: str, extra: list[str] | None = None, verbose: bool
     if problems:
         raise RuntimeError("compare_kernel cross-lane check failed:\n" + "\n".join(problems))
     problems = isa_check.check_lds_dma_sgpr(text, "compare_kernel")
+    if problems:
+        raise RuntimeError("buffer -> LDS copy SGPR hazard check failed:\n" + "\n".join(problems[:20]))
+
+
+def check_int8_isa(objdir: str, extra: list[str] | None = None, verbose: bool = False) -> None:
+    """Compile int8.hip to device assembly and check its buffer -> LDS copies."""
+    from rollout_logprob_consistency_amd import isa_check
+    src = os.path.join(CSRC, "int8.hip")
+    out = os.path.join(objdir, "int8.device.s")
+    cmd = [hipcc(), *compile_flags(), *(extra or []), "--cuda-device-only", "-S", src, "-o", out]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"hipcc -S failed for {src}:\n{r.stdout}\n{r.stderr}")
+    problems = isa_check.check_lds_dma_sgpr(open(out).read(), "tile_kernel")
     if problems:
         raise RuntimeError("buffer -> LDS copy SGPR hazard check failed:\n" + "\n".join(problems[:20]))
 

@@ -21,6 +21,7 @@
 #include <type_traits>
 
 #include "int8_internal.h"
+#include "tile_common.h"
 
 namespace lp {
 namespace {
@@ -52,18 +53,6 @@ __device__ __forceinline__ int fragment_row(int lane, int i) {
 }
 
 // ---- Scores -----------------------------------------------------------------
-
-template <int kOff>
-__device__ __forceinline__ float xor_lane(float v) {
-  const int x = __float_as_int(v), lane = (int)__lane_id();
-  if constexpr (kOff == 16) {
-    const auto r = __builtin_amdgcn_permlane16_swap(x, x, false, false);
-    return __int_as_float((lane & 16) ? (int)r[0] : (int)r[1]);
-  } else {
-    const auto r = __builtin_amdgcn_permlane32_swap(x, x, false, false);
-    return __int_as_float((lane & 32) ? (int)r[0] : (int)r[1]);
-  }
-}
 
 // A logit from its sum, each step rounded to fp32. The empty statement hides the
 // product from what follows: the compiler would fuse it with the rounding to
@@ -228,6 +217,149 @@ __global__ __launch_bounds__(64 * kStreamWaves) void stream_kernel(Int8Args a) {
   }
 }
 
+// ---- Tile kernel --------------------------------------------------------------
+// Four waves compute 256 vocabulary rows x 256 tokens, 128 x 128 each: 256
+// accumulators in the AGPRs. K stages of 128 bytes go from memory straight into
+// two alternating LDS buffers of 64 KiB; the 16-byte chunks of a row are
+// permuted (swz_w, swz_x) so that the fragment reads meet no bank conflicts. One
+// barrier a stage: the MFMAs of a stage's second half are carried across it, and
+// the next stage's copies are spread over the whole stage.
+constexpr int kTileRows = 256;                  // of W, and tokens
+constexpr int kTileThreads = 256;
+constexpr int kUnitB = kTileRows * kInt8StageK; // 32 KiB of either operand
+constexpr int kBufferB = 2 * kUnitB;
+constexpr int kUnitCopies = kUnitB / 1024 / 4;  // 1-KiB copies per wave (8)
+constexpr int kGroupV = 4;                      // vocabulary tiles per scheduling group
+constexpr int kSlotsPerCopy = 6;                // MFMAs from one copy to the next
+static_assert(kSlotsPerCopy * 2 * kUnitCopies < 2 * kTiles * kTiles, "copies fit in a stage");
+
+// Physical chunk of logical chunk c in LDS row `row`; its own inverse. A wave's
+// read takes the chunks 4 h + (l >> 4) of sixteen rows: of X consecutive ones, of
+// W those of fragment_row, 32 a + 4 i + b with a, b < 4.
+__device__ __forceinline__ int swz_x(int row, int c) { return c ^ (row & 7); }
+__device__ __forceinline__ int swz_w(int row, int c) {
+  return c ^ ((row & 3) | ((row >> 3) & 4));
+}
+
+template <class D>  // the logits' type, or void for scores
+__global__ __launch_bounds__(kTileThreads, 1) void tile_kernel(Int8Args a, int n_vt, int n_tt) {
+  __shared__ __attribute__((aligned(1024))) char ring[2 * kBufferB];
+  int vt, tt;
+  tile_of(blockIdx.x, n_vt, n_tt, kGroupV, vt, tt);
+  vt = __builtin_amdgcn_readfirstlane(vt);
+  tt = __builtin_amdgcn_readfirstlane(tt);
+  const int v0 = vt * kTileRows, t0 = tt * kTileRows;
+  const int lane = threadIdx.x & 63, lcol = lane & 15, lg = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave & 1, wn = wave >> 1;
+
+  // Copy j of a unit: wave w fills rows 8 (4 j + w) .. + 7, lane l the physical
+  // chunk l & 7 of row l >> 3 of them. Bit 5 of a row is j's lowest bit, so odd
+  // copies of W take the other half of a row. Rows behind the matrices read as
+  // zeros (the resources end there) and their results are not stored.
+  const int nk = (a.H + kInt8StageK - 1) / kInt8StageK;
+  const int64_t w_bytes = (int64_t)(a.V - v0 - 1) * a.ldw + (a.H + 15) / 16 * 16;
+  const int64_t x_bytes = (int64_t)(a.T - t0 - 1) * a.ldx + (int64_t)nk * kInt8StageK;
+  const __amdgpu_buffer_rsrc_t wres = rsrc_of(a.w + (int64_t)v0 * a.ldw, w_bytes);
+  const __amdgpu_buffer_rsrc_t xres = rsrc_of(a.x + (int64_t)t0 * a.ldx, x_bytes);
+  const uint32_t ldw = (uint32_t)a.ldw, ldx = (uint32_t)a.ldx;
+  const uint32_t row = (uint32_t)(8 * wave + (lane >> 3));
+  const uint32_t offW0 = row * ldw + 16 * swz_w(lane >> 3, lane & 7);
+  const uint32_t offW1 = row * ldw + 16 * (swz_w(lane >> 3, lane & 7) ^ 4);
+  const uint32_t offX = row * ldx + 16 * swz_x(lane >> 3, lane & 7);
+  const uint32_t lds0 =
+      __builtin_amdgcn_readfirstlane((uint32_t)reinterpret_cast<uintptr_t>((lds_char*)ring));
+// Copy c (0 .. 15, W's first) of stage k into buffer b. A stage behind the last
+// one copies that again, into the buffer that nothing reads any more.
+#define COPY(c_, k_, b_)                                                                      \
+  do {                                                                                        \
+    const bool w_ = (c_) < kUnitCopies;                                                       \
+    const uint32_t j_ = (uint32_t)((c_) & (kUnitCopies - 1));                                 \
+    uint32_t voff_;                                                                           \
+    asm volatile("v_add_u32 %0, %1, %2"                                                       \
+                 : "=v"(voff_)                                                                \
+                 : "s"(j_ * 32 * (w_ ? ldw : ldx)), "v"(w_ ? ((j_ & 1) ? offW1 : offW0) : offX)); \
+    copy_lds(w_ ? wres : xres,                                                                \
+             lds0 + (uint32_t)(b_) * kBufferB + (w_ ? 0u : (uint32_t)kUnitB) + (4 * j_ + wave) * 1024, \
+             voff_, (uint32_t)min((k_), nk - 1) * kInt8StageK);                                \
+  } while (0)
+
+  // Fragment reads of half h (64 codes) of a stage.
+  uint32_t rdW[2], rdX[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int wr = wm * kInt8BlockV + fragment_row(lane, 0), xr = wn * 128 + lcol;
+    // Tile i adds 4 i rows, which swz_w sees in none of its bits.
+    rdW[h] = (uint32_t)(wr * kInt8StageK + 16 * swz_w(wr, 4 * h + lg));
+    rdX[h] = (uint32_t)(kUnitB + xr * kInt8StageK + 16 * swz_x(xr, 4 * h + lg));
+  }
+#define RD_W(i_, h_, b_) \
+  *reinterpret_cast<const i32x4*>(ring + (rdW[(h_)] + (uint32_t)(b_) * kBufferB) + (i_) * 4 * kInt8StageK)
+#define RD_X(j_, h_, b_) \
+  *reinterpret_cast<const i32x4*>(ring + (rdX[(h_)] + (uint32_t)(b_) * kBufferB) + (j_) * 16 * kInt8StageK)
+#define FENCE() __builtin_amdgcn_sched_barrier(0)
+
+  // One step: eight groups (W tile g with X tiles 0 .. 7) on fw and mx_, 64 codes
+  // (z_: from zero sums), while the next step's fragments are read from half rh_
+  // of buffer rb_: X tiles 2 g and 2 g + 1 into nx_ during group g < 4, W tile g
+  // into fw[g] behind group g, its last use. A stage (two steps, slots from p0_
+  // on) issues its copies of stage ck_ into buffer cb_. The order is fixed.
+  i32x4 acc[kTiles][kTiles];  // [W tile][X tile]
+  i32x4 fw[kTiles], fx0[kTiles], fx1[kTiles];
+#define STEP(do_mma_, z_, do_rd_, mx_, nx_, rh_, rb_, p0_, ck_, cb_)                          \
+  do {                                                                                        \
+    _Pragma("unroll") for (int u = 0; u < kTiles * kTiles; ++u) {                             \
+      const int g_ = u >> 3, j_ = u & 7;                                                      \
+      if (do_mma_)                                                                            \
+        acc[g_][j_] = mma(fw[g_], mx_[j_], (z_) ? i32x4{0, 0, 0, 0} : acc[g_][j_]);           \
+      if ((do_rd_) && g_ < 4 && j_ == 2) nx_[2 * (g_ & 3)] = RD_X(2 * (g_ & 3), (rh_), (rb_)); \
+      if ((do_rd_) && g_ < 4 && j_ == 5)                                                      \
+        nx_[2 * (g_ & 3) + 1] = RD_X(2 * (g_ & 3) + 1, (rh_), (rb_));                         \
+      if ((do_rd_) && j_ == 7) fw[g_] = RD_W(g_, (rh_), (rb_));                               \
+      const int pu_ = (p0_) + u;                                                              \
+      if (pu_ % kSlotsPerCopy == 1 && pu_ / kSlotsPerCopy < 2 * kUnitCopies)                  \
+        COPY(pu_ / kSlotsPerCopy, (ck_), (cb_));                                              \
+      FENCE();                                                                                \
+    }                                                                                         \
+  } while (0)
+
+#pragma unroll
+  for (int c = 0; c < 2 * kUnitCopies; ++c) COPY(c, 0, 0);
+  __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0) lgkmcnt(0)
+  __syncthreads();
+  FENCE();
+  constexpr int kHalf = kTiles * kTiles;
+  STEP(false, false, true, fx1, fx0, 0, 0, 0, 1, 1);
+  STEP(true, true, true, fx0, fx1, 1, 0, kHalf, 1, 1);
+  for (int k = 1; k < nk; ++k) {
+    const int b = k & 1;
+    __builtin_amdgcn_s_waitcnt(0x0070);
+    __syncthreads();
+    FENCE();
+    STEP(true, false, true, fx1, fx0, 0, b, 0, k + 1, b ^ 1);
+    STEP(true, false, true, fx0, fx1, 1, b, kHalf, k + 1, b ^ 1);
+  }
+  STEP(true, false, false, fx1, fx0, 0, 0, 4 * kHalf, 0, 0);
+  __builtin_amdgcn_s_waitcnt(0x0070);  // the last copies land before the LDS is given back
+#undef STEP
+#undef COPY
+#undef RD_W
+#undef RD_X
+#undef FENCE
+
+  const int vb = v0 + wm * kInt8BlockV;
+  if (vb >= a.V) return;
+#pragma unroll
+  for (int j = 0; j < kTiles; ++j) {
+    const int t = t0 + wn * 128 + 16 * j + lcol;
+    i32x4 sum[kTiles];
+#pragma unroll
+    for (int i = 0; i < kTiles; ++i) sum[i] = acc[i][j];
+    if constexpr (std::is_void_v<D>) store_partial(a, sum, vb, t, lg);
+    else store_logits<D>(a, sum, vb, t, lg);
+  }
+}
+
 // ---- Merge ------------------------------------------------------------------
 // A workgroup joins 64 tokens' partials: wave w folds the blocks of segment w
 // in ascending order, then the segments are folded in order. The bounds depend
@@ -285,6 +417,15 @@ void stream(const Int8Args& a, hipStream_t s) {
   else stream_kernel<kNT, F16><<<grid, threads, 0, s>>>(a);
 }
 
+void tiles(const Int8Args& a, hipStream_t s) {
+  const int n_vt = (a.V + kTileRows - 1) / kTileRows, n_tt = (a.T + kTileRows - 1) / kTileRows;
+  const dim3 grid((uint32_t)n_vt * (uint32_t)n_tt);
+  if (!a.out) tile_kernel<void><<<grid, kTileThreads, 0, s>>>(a, n_vt, n_tt);
+  else if (a.dtype == LP_F32) tile_kernel<F32><<<grid, kTileThreads, 0, s>>>(a, n_vt, n_tt);
+  else if (a.dtype == LP_BF16) tile_kernel<BF16><<<grid, kTileThreads, 0, s>>>(a, n_vt, n_tt);
+  else tile_kernel<F16><<<grid, kTileThreads, 0, s>>>(a, n_vt, n_tt);
+}
+
 }  // namespace
 
 Int8Workspace int8_workspace_layout(int64_t T, int64_t H, int64_t V) {
@@ -317,7 +458,8 @@ hipError_t launch_int8(Int8Args a, hipStream_t stream_) {
   }
   if (a.T <= 16) stream<1>(a, stream_);
   else if (a.T <= 32) stream<2>(a, stream_);
-  else stream<4>(a, stream_);
+  else if (a.T <= 64) stream<4>(a, stream_);
+  else tiles(a, stream_);
   if ((e = hipGetLastError()) != hipSuccess || a.out) return e;
   merge_kernel<<<dim3((uint32_t)((a.T + 63) / 64)), 64 * kSegs, 0, stream_>>>(a);
   return hipGetLastError();
