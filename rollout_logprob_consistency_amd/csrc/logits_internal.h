@@ -128,6 +128,25 @@ __device__ __forceinline__ void store_group(typename D::Raw* p, int64_t i, int64
     }
 }
 
+// 2^t in fp64: 2^r for |r| <= 1/2 by the polynomial of degree 8 that meets it at
+// the Chebyshev nodes (1.1e-12 relative at most, of either sign), then the exact
+// scaling, to 0 or infinity far out. An infinite t gives NaN.
+__device__ __forceinline__ double exp2_f64(double t) {
+  const double n = rint(t), r = t - n;
+  double p = 0x1.63d13639e5a95p-20;
+  p = fma(p, r, 0x1.00dc4a53498e8p-16);
+  p = fma(p, r, 0x1.4308ac85a7188p-13);
+  p = fma(p, r, 0x1.5d8745a728180p-10);
+  p = fma(p, r, 0x1.3b2ab7181b779p-7);
+  p = fma(p, r, 0x1.c6b08dd6fd237p-5);
+  p = fma(p, r, 0x1.ebfbdff823cedp-3);
+  p = fma(p, r, 0x1.62e42fef84cf0p-1);
+  p = fma(p, r, 1.0);
+  int k;  // (the instruction saturates, which a conversion in C need not)
+  asm("v_cvt_i32_f64 %0, %1" : "=v"(k) : "v"(n));
+  return ldexp(p, k);
+}
+
 // Maximum and sum over a wave by the fixed XOR butterfly.
 __device__ __forceinline__ float wave_max_f32(float m) {
   m = fmaxf(m, __int_as_float(xlane<1>(__float_as_int(m))));
@@ -276,6 +295,8 @@ struct SelectArgs {
   int32_t drafts;
   const int32_t* draft_counts;  // [seqs] or null: all of them
   SelectLimit* limits;          // [N]
+  SelectPart* whole;            // [N][chunks][waves], of rows that are summed whole
+  int32_t whole_blocks;         // workgroups that do so
 };
 
 struct SelectWorkspace {
@@ -310,10 +331,11 @@ struct VerifyArgs {
   int32_t* bad_rows;        // or null
   // Set by launch_verify.
   double* chunk_sums;       // [seqs][chunks]
+  int32_t* verdicts;        // [seqs] what out_accepted gets
 };
 
 struct VerifyWorkspace {
-  size_t off_select, off_limits, off_sums, total;
+  size_t off_select, off_limits, off_whole, off_sums, off_verdicts, total;
 };
 // Where a call's parts lie; `total` serves smaller calls too.
 VerifyWorkspace verify_workspace_layout(int64_t seqs, int64_t drafts, int64_t V, int32_t dtype);

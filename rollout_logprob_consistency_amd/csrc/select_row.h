@@ -444,7 +444,7 @@ __device__ __forceinline__ void append(const Group<D> (&g)[kGroups], int k, cons
   }
 }
 
-enum Kind { kBuckets_, kTopK, kMinP };
+enum Kind { kBuckets_, kTopK, kMinP, kWhole, kWholeMinP };  // the last two: kLimit
 
 struct Settings {
   float tau, top_p, min_p, u;
@@ -515,6 +515,10 @@ __device__ __forceinline__ Settings settings_of(const SelectArgs& a, int64_t n) 
   if (!s.bad) {
     if (s.greedy || (s.top_k > 0 && s.top_k <= kShortTop)) s.kind = kTopK;
     else if (s.top_k <= 0 && s.top_p >= 1.0f && s.min_p > 0.0f && s.min_p <= 1.0f) s.kind = kMinP;
+    if (kJob == kLimit && s.kind == kMinP) s.kind = kWholeMinP;
+    if (kJob == kLimit && s.kind == kBuckets_ && s.top_k <= 0 && s.top_p >= 1.0f &&
+        !(s.min_p > 0.0f))
+      s.kind = kWhole;
   }
   return s;
 }
@@ -793,15 +797,132 @@ __device__ __forceinline__ void collect_buckets(const Row<D>& row, S& sh, int c0
   __syncthreads();
 }
 
+// ---- Rows that are summed whole (kLimit) ----------------------------------------
+// Where every token is kept, or those that min-p leaves, nothing has to be ordered:
+// a row's weights are summed, in fp64, as what is drawn between two distributions
+// needs digits that fp32's exponentials lose. An element takes 17 instructions,
+// which bounds it: rows of 151 936 bf16 logits, 1 920 of them, at XX us.
+
+constexpr double kLog2E = 1.4426950408889634;
+
+// The sum of 2^((z - m) c) over a wave's part of a chunk, and m: the part's
+// maximum, or without `top` that of its first groups, which spares an instruction
+// an element, and fp64 has room for 700 nats more. Formed again where it does not
+// suffice or a logit is not finite. The wave's groups from `groups` on lie behind
+// the row.
+template <class D>
+__device__ __forceinline__ Part whole_part(Group<D> (&g)[kGroups], int groups, double c, bool top) {
+  float m = g[0].get(0);
+#pragma unroll
+  for (int i = 1; i < D::kVec; ++i) m = fmaxf(m, g[0].get(i));
+  auto maximum = [&] LP_INLINE {
+    bool odd = false;
+#pragma unroll
+    for (int j = 0; j < kGroups; ++j) {
+      g[j].fresh();
+#pragma unroll
+      for (int i = 0; i < D::kVec; ++i) {
+        m = fmaxf(m, g[j].get(i));
+        odd |= !(g[j].get(i) < INFINITY);
+      }
+    }
+    return odd;
+  };
+  if (top) maximum();
+  m = wave_max_f32(m);
+  double b = (double)m * c, s = 0.0;
+#pragma unroll
+  for (int j = 0; j < kGroups; ++j) {
+    if (j >= groups) break;
+    g[j].fresh();
+#pragma unroll
+    for (int i = 0; i < D::kVec; ++i) {
+      s += exp2_f64(fma((double)g[j].get(i), c, -b));
+      if (i % 4 == 3) __builtin_amdgcn_sched_barrier(0);  // bounds the registers in use
+    }
+  }
+  s = wave_sum(s);
+  if (!(s < 0x1p1000)) {
+    const bool odd = __ballot(maximum()) != 0;
+    m = wave_max_f32(m);
+    b = m == -INFINITY ? 0.0 : (double)m * c;
+    s = 0.0;
+#pragma unroll
+    for (int j = 0; j < kGroups; ++j) {
+      g[j].fresh();
+#pragma unroll
+      for (int i = 0; i < D::kVec; ++i) {
+        const float z = g[j].get(i);
+        s += z == -INFINITY ? 0.0 : exp2_f64(fma((double)z, c, -b));
+        if (i % 4 == 3) __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+    s = odd ? (double)NAN : wave_sum(s);
+  }
+  return {m, s};
+}
+
+__device__ __forceinline__ bool is_whole(const Settings& s) {
+  return s.kind == kWhole || s.kind == kWholeMinP;
+}
+
+// Workgroup `block` of whole_blocks: an equal share of all rows' chunks, whatever
+// rows they belong to, the next one's loads in flight. Lane i looks up the
+// settings of the share's i-th row.
+template <class D>
+__device__ __forceinline__ void whole_rows(const SelectArgs& a, int block) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int chunks = (a.V + chunk_of<D>() - 1) / chunk_of<D>();
+  const int64_t items = a.N * chunks;
+  const int64_t lo = items * block / a.whole_blocks, hi = items * (block + 1) / a.whole_blocks;
+  for (int64_t r0 = lo / chunks; r0 * chunks < hi; r0 += 64) {
+    bool mine = (r0 + lane) * chunks < hi && !skipped<kLimit>(a, r0 + lane);
+    double scale = 0.0;
+    bool min_p = false;
+    if (mine) {
+      const Settings st = settings_of<kLimit>(a, r0 + lane);
+      mine = is_whole(st);
+      min_p = st.kind == kWholeMinP;
+      scale = kLog2E / (double)st.tau;
+    }
+    const uint64_t min_ps = __ballot(min_p);
+    for (uint64_t rows = __ballot(mine); rows; rows &= rows - 1) {
+      const int i = __ffsll((long long)rows) - 1;
+      const int64_t n = r0 + i;
+      const double c = lane_value(scale, i);
+      const Row<D> row = row_at<D, kLimit>(a, n);
+      const int c0 = (int)max(lo - n * chunks, (int64_t)0);
+      const int c1 = (int)min(hi - n * chunks, (int64_t)chunks);
+      SelectPart* parts = a.whole + n * chunks * kWaves + wave;
+      row.for_chunks(c0, c1, [&](Group<D>(&g)[kGroups], int k) LP_INLINE {
+        const int left = row.V - k * chunk_of<D>() - wave * 64 * D::kVec;
+        Part p = {-INFINITY, 0.0};
+        if (left > 0)
+          p = whole_part<D>(g, (left - 1) / (kThreads * D::kVec) + 1, c, min_ps >> i & 1);
+        if (lane == 0) parts[k * kWaves] = p;
+      });
+    }
+  }
+}
+
 // One slice of a row (the whole row where a.slices is 1).
 template <class D, Job kJob>
 __global__ __launch_bounds__(kThreads, 6) void collect_kernel(SelectArgs a) {
   constexpr bool kTop = kJob == kTopLogits;
   __shared__ CollectShared sh;
-  const int64_t n = blockIdx.x / (uint32_t)a.slices;
-  const int slice = (int)(blockIdx.x - (uint32_t)n * (uint32_t)a.slices);
+  uint32_t block = blockIdx.x;
+  if constexpr (kJob == kLimit) {
+    if (block < (uint32_t)a.whole_blocks) {
+      whole_rows<D>(a, (int)block);
+      return;
+    }
+    block -= (uint32_t)a.whole_blocks;
+  }
+  const int64_t n = block / (uint32_t)a.slices;
+  const int slice = (int)(block - (uint32_t)n * (uint32_t)a.slices);
   if (skipped<kJob>(a, n)) return;
   const Settings st = settings_of<kJob>(a, n);
+  if (kJob == kLimit && is_whole(st)) return;
   uint32_t* count = a.counts + n * a.slices;
   Row<D> row = row_at<D, kJob>(a, n);
   const int chunks = row.chunks(), tid = threadIdx.x, wave = tid >> 6;
@@ -1290,6 +1411,21 @@ __device__ __forceinline__ int bucket_of_mass(Shared& sh, double want, bool over
   return b < kBuckets ? b : e;
 }
 
+// How many tokens of bucket b have a logit of at least `least`, which lies in it.
+// The bucket's tokens are listed by then (no more than a list holds).
+template <class D>
+__device__ __forceinline__ uint32_t rank_of_value(const Row<D>& row, Shared& sh, Listed& listed,
+                                                  int b, float least) {
+  select_in_bucket(row, sh, listed, b, kByRank, 1, 0.0);
+  const uint32_t at = b == listed.lo0 ? 0u : sh.cnt[b] - sh.cnt[listed.lo0];
+  const uint32_t m = sh.cnt[b + 1] - sh.cnt[b];
+  constexpr int kEach = kList / kThreads;
+  const uint32_t base = threadIdx.x * kEach;
+  return first_index(&sh.found, m, base, kEach, [&](int i) LP_INLINE {
+    return token_logit(sh.list[at + base + i]) < least;
+  });
+}
+
 // Least finite logit that min-p keeps (least where (zmax - z) / tau reaches
 // `most`, 1/32 nat): a search over the finite keys, 64 at a time, by every wave
 // alike. The differences ascend as the keys descend, in fp64 too.
@@ -1334,10 +1470,25 @@ __device__ __forceinline__ void draw_from_buckets(const SelectArgs& a, const Set
       last = f.key;
     }
   }
+  // kLimit: where min-p ends what is kept, and whether in a bucket before the
+  // nucleus' (which then needs no selection) or behind it.
+  float least = -INFINITY;
+  int least_bucket = kBuckets;
+  const bool min_p = st.min_p > 0.0f && st.min_p <= 1.0f;
+  if constexpr (kJob == kLimit)
+    if (min_p) {
+      least = least_kept(row, fmax(0.0, -log((double)st.min_p) * kPerNat));
+      least_bucket = (int)Row<D>::bucket(row.x_of(least));
+    }
+  bool inside = true;  // min-p may still end it
   if (st.top_p < 1.0f) {
     const double want = (double)st.top_p * mass;
-    if (want > 0.0) {
-      const int b = bucket_of_mass(sh, want, false);
+    int b = 0;
+    if (want > 0.0) b = bucket_of_mass(sh, want, false);
+    if (kJob == kLimit && want > 0.0 && least_bucket < b) {
+      // min-p ends it before.
+    } else if (want > 0.0) {
+      inside = kJob != kLimit || least_bucket == b;
       if (kJob == kDraw && !(st.min_p > 0.0f)) {
         // The kept mass lies between the bucket's ends, so the drawn token's
         // bucket is known to one or a few: list both in one pass.
@@ -1376,7 +1527,23 @@ __device__ __forceinline__ void draw_from_buckets(const SelectArgs& a, const Set
     kept = 1;
     mass = row.max_weight();
     if constexpr (kJob == kLimit) last = first_token();
-  } else if (st.min_p > 0.0f) {
+  } else if (kJob == kLimit && min_p && inside && sh.cnt[least_bucket] < kept &&
+             least_bucket < kBuckets - 1 &&
+             sh.cnt[least_bucket + 1] - sh.cnt[least_bucket] <= (uint32_t)kList) {
+    // The tokens of that bucket that reach it (there may be none), from the list
+    // that the nucleus may have left.
+    const uint32_t before = sh.cnt[least_bucket];
+    const uint32_t r =
+        sh.cnt[least_bucket + 1] != before ? rank_of_value(row, sh, listed, least_bucket, least) : 0u;
+    if (before + r < kept) {
+      kept = before + r;
+      mass = sh.above[least_bucket];
+      if (r > 0)
+        mass += (double)select_in_bucket(row, sh, listed, least_bucket, kByRank, r, 0.0).mass *
+                Row<D>::unit(least_bucket);
+      last = (uint64_t)key_of(least) << 32;
+    }
+  } else if (st.min_p > 0.0f && inside) {
     // w >= min_p where 32 (max - z) / tau <= -32 ln min_p. The bucket that
     // this falls in is certain to one, so three are looked through.
     const double most = fmax(0.0, -log((double)st.min_p) * kPerNat);
@@ -1515,13 +1682,82 @@ __device__ __noinline__ void list_by_buckets(SelectArgs a, Settings st, int64_t 
   else finish_draw<kJob>(a, st, n, sh.list, want, ln_all, sh);
 }
 
+// A row's parts joined by a wave: its maximum (of a kWhole row, one that suffices
+// as a base), and the sum of all weights from there. NaN: there is none.
+struct Whole {
+  float top;
+  double sum;
+};
+__device__ __forceinline__ Whole join_whole(const SelectArgs& a, int64_t n, float tau, int parts) {
+  const int lane = threadIdx.x & 63;
+  const Global<const Part> p = (Global<const Part>)(a.whole + n * parts);
+  float top = -INFINITY;
+  for (int i = lane; i < parts; i += 64) top = fmaxf(top, p[i].m);
+  top = wave_max_f32(top);
+  const double c = kLog2E / (double)tau;
+  double sum = 0.0;
+  for (int i = lane; i < parts; i += 64) {
+    const double s = p[i].s;
+    sum += p[i].m == -INFINITY ? s : s * exp2_f64((double)p[i].m * c - (double)top * c);
+  }
+  sum = wave_sum(sum);
+  return {top, top == -INFINITY ? (double)NAN : sum};
+}
+
+// The limit of row n, if it keeps every token.
+__device__ __forceinline__ void join_row(const SelectArgs& a, int64_t n, int parts) {
+  if (skipped<kLimit>(a, n)) return;
+  const Settings st = settings_of<kLimit>(a, n);
+  if (st.kind != kWhole) return;
+  const Whole w = join_whole(a, n, st.tau, parts);
+  if ((threadIdx.x & 63) != 0) return;
+  const double ln = log(w.sum);
+  if (isnan(w.sum)) write_bad_draw<kLimit>(a, n);
+  else a.limits[n] = {0ull, (double)w.top, ln, ln};
+}
+
+// The limit of a row by min-p alone, whose parts are there: what is kept, least_kept
+// says by the maximum, and its weights are summed in a second pass, in which few
+// waves have exponentials to form.
+template <class D>
+__device__ __forceinline__ void limit_min_p(const SelectArgs& a, const Settings& st, int64_t n,
+                                            Row<D>& row, Shared& sh) {
+  const Whole w = join_whole(a, n, st.tau, row.chunks() * kWaves);
+  if (isnan(w.sum)) {
+    if (threadIdx.x == 0) write_bad_draw<kLimit>(a, n);
+    return;
+  }
+  row.zmax = w.top;
+  row.inv = kPerNat / (double)st.tau;
+  const float least = least_kept(row, fmax(0.0, -log((double)st.min_p) * kPerNat));
+  const double c = kLog2E / (double)st.tau, b = (double)w.top * c;
+  double s = 0.0, all;
+  row.for_chunks(0, row.chunks(), [&](Group<D>(&g)[kGroups], int) LP_INLINE {
+#pragma unroll
+    for (int j = 0; j < kGroups; ++j)
+#pragma unroll
+      for (int i = 0; i < D::kVec; ++i) {
+        const float z = g[j].get(i);
+        if (__ballot(z >= least) == 0) continue;
+        s += z >= least ? exp2_f64(fma((double)z, c, -b)) : 0.0;
+      }
+  });
+  block_scan(s, sh.wave_f64, &all);
+  if (threadIdx.x == 0)
+    a.limits[n] = {(uint64_t)key_of(least) << 32, (double)w.top, log(all), log(w.sum)};
+}
+
 // One row: its slices' lists or buckets joined, or the whole of it.
 template <class D, Job kJob>
 __device__ __forceinline__ void finish_row(const SelectArgs& a, int64_t n, Shared& sh) {
   constexpr bool kTop = kJob == kTopLogits;
-  if (skipped<kJob>(a, n)) return;
   const Settings st = settings_of<kJob>(a, n);
   Row<D> row = row_at<D, kJob>(a, n);
+  if constexpr (kJob == kLimit)
+    if (st.kind == kWholeMinP) {
+      limit_min_p(a, st, n, row, sh);
+      return;
+    }
   if constexpr (!kTop)
     if (st.kind == kBuckets_) {
       if (st.bad) {
@@ -1622,6 +1858,13 @@ __device__ __forceinline__ void finish_row(const SelectArgs& a, int64_t n, Share
 template <class D, Job kJob>
 __global__ __launch_bounds__(kThreads, 4) void row_kernel(SelectArgs a) {
   __shared__ Shared sh;
+  if constexpr (kJob == kLimit) {
+    // Rows that keep every token are joined by a wave each, eight by a workgroup,
+    // and end there.
+    const int64_t n = (int64_t)blockIdx.x * kWaves + (threadIdx.x >> 6);
+    if (n < a.N) join_row(a, n, (a.V + chunk_of<D>() - 1) / chunk_of<D>() * kWaves);
+    if (skipped<kLimit>(a, blockIdx.x) || settings_of<kLimit>(a, blockIdx.x).kind == kWhole) return;
+  }
   finish_row<D, kJob>(a, blockIdx.x, sh);
 }
 

@@ -7,10 +7,12 @@
 // through which the weights pass u times their sum.
 //
 // The rows' limits (where the kept tokens end, and what they weigh) come from
-// the draw's own kernels. Two more launches end the call: residual_kernel sums
-// the weights of the one row (or two) that a sequence's last token is drawn from
-// by chunks, final_kernel finds the chunk and the token in it. Both look at the
-// drafts again: a few loads, against a launch that would only store the verdict.
+// the draw's own kernels. Two more launches end the call: residual_kernel judges
+// the drafts (each workgroup for itself: a few loads, against a launch more) and
+// sums the weights of the one row, or two, that a sequence's last token is drawn
+// from by chunks; final_kernel finds the chunk and the token in it. (One launch
+// whose last workgroup of a sequence ends it took longer: 147 us against 91 us for
+// 128 sequences of 151 936, as the fences that it needs empty the L2 caches.)
 #include <algorithm>
 
 #include "select_row.h"
@@ -22,26 +24,34 @@ constexpr int kVerifyThreads = 256;
 constexpr int kVerifyWaves = kVerifyThreads / 64;
 constexpr int kVerifyChunk = 4096;  // tokens summed at once
 constexpr int kEach = kVerifyChunk / kVerifyThreads;
-constexpr int64_t kVerifyPlaces = 16384;  // workgroups, at most, that sum chunks
+// Workgroups that run at once: of residual_kernel six on each of 256 CUs, of
+// collect_kernel three.
+constexpr int64_t kVerifyPlaces = 1536;
+constexpr int64_t kWholePlaces = 768;
 static_assert(LP_VERIFY_MAX_DRAFTS < 64, "a wave holds a sequence's positions");
 
-// The distribution that a row would be drawn from.
+// The distribution that a row would be drawn from: token v is kept where (z,
+// lower index) is no less than the last kept token's.
 struct Dist {
-  double base, inv_tau, ln_kept;
-  uint64_t last;
+  double base, c, log2_kept;  // c = log2(e) / tau
+  float z_last;
+  int v_last;
 
-  __device__ __forceinline__ double gap(float z) const { return ((double)z - base) * inv_tau; }
-  __device__ __forceinline__ bool keeps(float z, int v) const { return token_key(z, v) >= last; }
-  // Of a token that it keeps.
-  __device__ __forceinline__ double prob(float z) const { return exp_f64(gap(z) - ln_kept); }
+  __device__ __forceinline__ bool near(float z) const { return z >= z_last; }
+  __device__ __forceinline__ bool keeps(float z, int v) const {
+    return z > z_last || (z == z_last && v <= v_last);
+  }
+  // Of a finite token that it keeps.
+  __device__ __forceinline__ double prob(float z) const {
+    return exp2_f64(fma((double)z - base, c, -log2_kept));
+  }
 };
 
 struct Sequence {
   int64_t b;
   int count;     // drafts
   int accepted;  // of them; -1: a sequence that has no verdict
-  bool greedy;
-  double inv_tau;
+  double inv_tau;  // 1 where it is greedy
 };
 
 // The target's (at <= count) or the draft's (at < count) row of a sequence.
@@ -53,12 +63,23 @@ __device__ __forceinline__ int64_t draft_limit(const VerifyArgs& a, int64_t b, i
 }
 __device__ __forceinline__ Dist dist_of(const VerifyArgs& a, const Sequence& s, int64_t limit) {
   const SelectLimit l = a.rows.limits[limit];
-  return {l.base, s.inv_tau, l.ln_kept, l.last};
+  // (No limit, and one that is a value alone, hold the lowest place of an index.)
+  const bool all = l.last == 0;
+  return {l.base, kLog2E * s.inv_tau, l.ln_kept * kLog2E,
+          all ? -3.4028234663852886e38f : token_logit(l.last),
+          all || (uint32_t)l.last == 0 ? INT32_MAX : token_index(l.last)};
 }
 
 template <class D>
 __device__ __forceinline__ float logit_at(const void* logits, int64_t ld, int64_t row, int64_t v) {
   return D::value(read_global(static_cast<const typename D::Raw*>(logits), row * ld + v));
+}
+
+__device__ __forceinline__ Sequence sequence_of(const VerifyArgs& a, int64_t b) {
+  const SelectArgs& r = a.rows;
+  const float tau = r.temperatures ? read_global(r.temperatures, b) : r.temperature;
+  return {b, r.draft_counts ? read_global(r.draft_counts, b) : r.drafts, -1,
+          tau == 0.0f ? 1.0 : 1.0 / (double)tau};
 }
 
 // How far a sequence's drafts are accepted: lane j looks at position j. Every
@@ -67,13 +88,7 @@ template <class D>
 __device__ __forceinline__ Sequence judge(const VerifyArgs& a, int64_t b) {
   const SelectArgs& r = a.rows;
   const int lane = threadIdx.x & 63;
-  Sequence s;
-  s.b = b;
-  s.count = r.draft_counts ? read_global(r.draft_counts, b) : r.drafts;
-  const float tau = r.temperatures ? read_global(r.temperatures, b) : r.temperature;
-  s.greedy = tau == 0.0f;
-  s.inv_tau = s.greedy ? 1.0 : 1.0 / (double)tau;
-  s.accepted = -1;
+  Sequence s = sequence_of(a, b);
   if (s.count < 0 || s.count > r.drafts) return s;
   const int width = r.drafts + 1;
   bool bad = lane == 63 && isnan(read_global(a.u, b * width + r.drafts)), passed = false;
@@ -131,18 +146,22 @@ struct Weights {
       gone = read_global(a.draft_ids, d);  // the draft's whole probability
     }
   }
-  __device__ __forceinline__ double of(float z, float y, int v) const {
-    if (!p.keeps(z, v) || v == gone) return 0.0;
-    const double w = p.prob(z);
-    return draft && q.keeps(y, v) ? fmax(w - q.prob(y), 0.0) : w;
-  }
-  // The weights of the tokens from v on, kVec of them; 0 behind the row.
+  // The weights of the tokens from v on, kVec of them; 0 behind the row. A wave
+  // whose tokens are all below the last kept one forms no exponentials.
   __device__ __forceinline__ void group(int v, double (&w)[D::kVec]) const {
     const Group<D> z = load_group<D>(target, v, V);
     Group<D> y = z;
     if (draft) y = load_group<D>(draft, v, V);
 #pragma unroll
-    for (int i = 0; i < D::kVec; ++i) w[i] = v + i < V ? of(z.get(i), y.get(i), v + i) : 0.0;
+    for (int i = 0; i < D::kVec; ++i) {
+      const float a = z.get(i), b = y.get(i);
+      w[i] = 0.0;
+      if (__ballot(p.near(a)) == 0) continue;
+      const bool kept = p.keeps(a, v + i) && v + i != gone;
+      w[i] = kept ? p.prob(a) : 0.0;
+      if (!draft || __ballot(kept && q.near(b)) == 0) continue;
+      w[i] = kept && q.keeps(b, v + i) ? fmax(w[i] - q.prob(b), 0.0) : w[i];
+    }
   }
 };
 
@@ -166,20 +185,6 @@ __device__ __forceinline__ double chunk_sum(const Weights<D>& w, int chunk, doub
   for (int i = 1; i < kVerifyWaves; ++i) s += words[i];
   __syncthreads();
   return s;
-}
-
-template <class D>
-__global__ __launch_bounds__(kVerifyThreads) void residual_kernel(VerifyArgs a, int parts) {
-  __shared__ double words[kVerifyWaves];
-  const int64_t b = blockIdx.x / (uint32_t)parts;
-  const Sequence s = judge<D>(a, b);
-  if (s.accepted < 0) return;
-  const Weights<D> w(a, s, false);
-  const int chunks = (a.rows.V + kVerifyChunk - 1) / kVerifyChunk;
-  for (int c = (int)(blockIdx.x % (uint32_t)parts); c < chunks; c += parts) {
-    const double sum = chunk_sum(w, c, words);
-    if (threadIdx.x == 0) a.chunk_sums[b * chunks + c] = sum;
-  }
 }
 
 // Exclusive prefix sum over the workgroup.
@@ -270,31 +275,14 @@ __device__ __forceinline__ int draw(const Weights<D>& w, double u, int chunks, F
   return sh.token != INT32_MAX ? sh.token : sh.last;
 }
 
+// A sequence's outputs, its chunks' sums in LDS.
 template <class D>
-__global__ __launch_bounds__(kVerifyThreads) void final_kernel(VerifyArgs a) {
-  __shared__ FinalShared sh;
+__device__ __forceinline__ void finish(const VerifyArgs& a, const Sequence& s, int chunks,
+                                       FinalShared& sh) {
   const SelectArgs& r = a.rows;
-  const int64_t b = blockIdx.x;
   const int tid = threadIdx.x, width = r.drafts + 1;
-  const Sequence s = judge<D>(a, b);
-  const int64_t out = b * width + tid;
-  if (s.accepted < 0) {
-    if (tid < width) {
-      a.out_tokens[out] = -1;
-      a.out_logprob[out] = NAN;
-      if (a.out_processed) a.out_processed[out] = NAN;
-    }
-    if (tid == 0) {
-      a.out_accepted[b] = -1;
-      if (a.bad_rows) atomicAdd(a.bad_rows, 1);
-    }
-    return;
-  }
-  const int chunks = (r.V + kVerifyChunk - 1) / kVerifyChunk;
   const double u =
-      fmin(fmax((double)read_global(a.u, b * width + r.drafts), 0.0), 1.0 - 0x1p-24);
-  if (tid < chunks) sh.sums[tid] = a.chunk_sums[b * chunks + tid];
-  __syncthreads();
+      fmin(fmax((double)read_global(a.u, s.b * width + r.drafts), 0.0), 1.0 - 0x1p-24);
   int token = draw(Weights<D>(a, s, false), u, chunks, sh);
   if (token < 0) {
     // The target has nothing beyond the draft: a token of the target's own.
@@ -310,34 +298,76 @@ __global__ __launch_bounds__(kVerifyThreads) void final_kernel(VerifyArgs a) {
     float logprob = 0.0f, processed = 0.0f;
     int64_t t = -1;
     if (tid <= s.accepted) {
-      t = tid < s.accepted ? read_global(a.draft_ids, b * r.drafts + tid) : token;
-      const int64_t row = target_row(a, b, tid);
+      t = tid < s.accepted ? read_global(a.draft_ids, s.b * r.drafts + tid) : token;
+      const int64_t row = target_row(a, s.b, tid);
       const SelectLimit l = r.limits[row];
-      const Dist p = {l.base, s.inv_tau, l.ln_kept, l.last};
-      const double gap = p.gap(logit_at<D>(r.logits, r.ld, row, t));
+      const double gap = ((double)logit_at<D>(r.logits, r.ld, row, t) - l.base) * s.inv_tau;
       logprob = (float)(gap - l.ln_all);
       processed = (float)(gap - l.ln_kept);
     }
+    const int64_t out = s.b * width + tid;
     a.out_tokens[out] = t;
     a.out_logprob[out] = logprob;
     if (a.out_processed) a.out_processed[out] = processed;
   }
-  if (tid == 0) a.out_accepted[b] = s.accepted;
+  if (tid == 0) a.out_accepted[s.b] = s.accepted;
+}
+
+template <class D>
+__global__ __launch_bounds__(kVerifyThreads) void residual_kernel(VerifyArgs a, int parts) {
+  __shared__ double words[kVerifyWaves];
+  const int64_t b = blockIdx.x / (uint32_t)parts;
+  const int part = (int)(blockIdx.x % (uint32_t)parts);
+  const Sequence s = judge<D>(a, b);
+  if (part == 0 && threadIdx.x == 0) a.verdicts[b] = s.accepted;
+  if (s.accepted < 0) return;
+  const int chunks = (a.rows.V + kVerifyChunk - 1) / kVerifyChunk;
+  const Weights<D> w(a, s, false);
+  for (int c = part; c < chunks; c += parts) {
+    const double sum = chunk_sum(w, c, words);
+    if (threadIdx.x == 0) a.chunk_sums[b * chunks + c] = sum;
+  }
+}
+
+template <class D>
+__global__ __launch_bounds__(kVerifyThreads) void final_kernel(VerifyArgs a) {
+  __shared__ FinalShared sh;
+  const SelectArgs& r = a.rows;
+  const int64_t b = blockIdx.x;
+  const int tid = threadIdx.x, width = r.drafts + 1;
+  const int chunks = (r.V + kVerifyChunk - 1) / kVerifyChunk;
+  const int accepted = read_global(a.verdicts, b);
+  if (accepted < 0) {
+    if (tid < width) {
+      a.out_tokens[b * width + tid] = -1;
+      a.out_logprob[b * width + tid] = NAN;
+      if (a.out_processed) a.out_processed[b * width + tid] = NAN;
+    }
+    if (tid == 0) {
+      a.out_accepted[b] = -1;
+      if (a.bad_rows) atomicAdd(a.bad_rows, 1);
+    }
+    return;
+  }
+  Sequence s = sequence_of(a, b);
+  s.accepted = accepted;
+  if (tid < chunks) sh.sums[tid] = read_global(a.chunk_sums, b * chunks + tid);
+  __syncthreads();
+  finish<D>(a, s, chunks, sh);
 }
 
 template <class D>
 hipError_t launch(const VerifyArgs& a, hipStream_t stream) {
   const SelectArgs& r = a.rows;
-  const SelectWays ways = select_ways(r);
   hipError_t e;
-  if (ways.lists || r.slices > 1) {
-    collect_kernel<D, kLimit><<<dim3((uint32_t)(r.N * r.slices)), kThreads, 0, stream>>>(r);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
-  }
+  collect_kernel<D, kLimit><<<dim3((uint32_t)(r.whole_blocks + r.N * r.slices)), kThreads, 0,
+                              stream>>>(r);
+  if ((e = hipGetLastError()) != hipSuccess) return e;
   row_kernel<D, kLimit><<<dim3((uint32_t)r.N), kThreads, 0, stream>>>(r);
   if ((e = hipGetLastError()) != hipSuccess) return e;
   const int64_t chunks = (r.V + kVerifyChunk - 1) / kVerifyChunk;
-  const int64_t parts = std::max<int64_t>(1, std::min(chunks, kVerifyPlaces / r.seqs));
+  const int64_t each = (chunks * r.seqs + kVerifyPlaces - 1) / kVerifyPlaces;
+  const int64_t parts = (chunks + each - 1) / each;
   residual_kernel<D><<<dim3((uint32_t)(r.seqs * parts)), kVerifyThreads, 0, stream>>>(a,
                                                                                     (int)parts);
   if ((e = hipGetLastError()) != hipSuccess) return e;
@@ -347,14 +377,9 @@ hipError_t launch(const VerifyArgs& a, hipStream_t stream) {
 
 size_t up(size_t b) { return (b + 255) / 256 * 256; }
 
-VerifyWorkspace layout_of(size_t select, int64_t rows, int64_t seqs, int64_t V) {
-  VerifyWorkspace w;
-  w.off_select = 0;
-  w.off_limits = up(select);
-  w.off_sums = w.off_limits + up((size_t)rows * sizeof(SelectLimit));
-  w.total = w.off_sums +
-            up((size_t)seqs * (size_t)((V + kVerifyChunk - 1) / kVerifyChunk) * sizeof(double));
-  return w;
+int64_t row_chunks(int64_t V, int32_t dtype) {
+  const int64_t chunk = (int64_t)kThreads * kGroups * (16 / dtype_bytes(dtype));
+  return (V + chunk - 1) / chunk;
 }
 
 }  // namespace
@@ -362,7 +387,15 @@ VerifyWorkspace layout_of(size_t select, int64_t rows, int64_t seqs, int64_t V) 
 VerifyWorkspace verify_workspace_layout(int64_t seqs, int64_t drafts, int64_t V, int32_t dtype) {
   // (Without a draft model fewer rows have limits; the layout is the same.)
   const int64_t rows = seqs * (2 * drafts + 1);
-  return layout_of(select_workspace_most(rows, V, dtype), rows, seqs, V);
+  VerifyWorkspace w;
+  w.off_select = 0;
+  w.off_limits = up(select_workspace_most(rows, V, dtype));
+  w.off_whole = w.off_limits + up((size_t)rows * sizeof(SelectLimit));
+  w.off_sums = w.off_whole + up((size_t)(rows * row_chunks(V, dtype) * kWaves) * sizeof(Part));
+  w.off_verdicts = w.off_sums + up((size_t)seqs * (size_t)((V + kVerifyChunk - 1) / kVerifyChunk) *
+                               sizeof(double));
+  w.total = w.off_verdicts + up((size_t)seqs * sizeof(int32_t));
+  return w;
 }
 
 hipError_t launch_verify(VerifyArgs a, void* workspace, hipStream_t stream) {
@@ -371,8 +404,11 @@ hipError_t launch_verify(VerifyArgs a, void* workspace, hipStream_t stream) {
   char* base = static_cast<char*>(workspace);
   r.N = r.seqs * (r.drafts + 1) + (r.draft_logits ? r.seqs * r.drafts : 0);
   r.limits = reinterpret_cast<SelectLimit*>(base + w.off_limits);
+  r.whole = reinterpret_cast<SelectPart*>(base + w.off_whole);
+  a.verdicts = reinterpret_cast<int32_t*>(base + w.off_verdicts);
   a.chunk_sums = reinterpret_cast<double*>(base + w.off_sums);
   place_select(r, base + w.off_select);
+  r.whole_blocks = (int32_t)std::min(kWholePlaces, r.N * row_chunks(r.V, r.dtype));
   switch (r.dtype) {
     case LP_F32: return launch<F32>(a, stream);
     case LP_BF16: return launch<BF16>(a, stream);
