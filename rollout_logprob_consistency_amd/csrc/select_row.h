@@ -805,61 +805,73 @@ __device__ __forceinline__ void collect_buckets(const Row<D>& row, S& sh, int c0
 
 constexpr double kLog2E = 1.4426950408889634;
 
-// The sum of 2^((z - m) c) over a wave's part of a chunk, and m: the part's
-// maximum, or without `top` that of its first groups, which spares an instruction
-// an element, and fp64 has room for 700 nats more. Formed again where it does not
-// suffice or a logit is not finite. The wave's groups from `groups` on lie behind
-// the row.
+// The sum of 2^((z - m) c) over a wave's part of a chunk, and m: the maximum where
+// it is wanted (`top`), else 0, as fp64 has room for 2^1000 either way. Where that
+// does not suffice, or a logit is not finite, the sum is formed again. The wave's
+// groups from `groups` on lie behind the row.
 template <class D>
-__device__ __forceinline__ Part whole_part(Group<D> (&g)[kGroups], int groups, double c, bool top) {
-  float m = g[0].get(0);
-#pragma unroll
-  for (int i = 1; i < D::kVec; ++i) m = fmaxf(m, g[0].get(i));
-  auto maximum = [&] LP_INLINE {
-    bool odd = false;
-#pragma unroll
-    for (int j = 0; j < kGroups; ++j) {
-      g[j].fresh();
-#pragma unroll
-      for (int i = 0; i < D::kVec; ++i) {
-        m = fmaxf(m, g[j].get(i));
-        odd |= !(g[j].get(i) < INFINITY);
-      }
-    }
-    return odd;
-  };
-  if (top) maximum();
-  m = wave_max_f32(m);
-  double b = (double)m * c, s = 0.0;
+struct Groups {
+  Group<D> g[kGroups];
+};
+
+template <class D, class F>
+__device__ __forceinline__ double sum_groups(Group<D> (&g)[kGroups], int groups, F weight) {
+  double s = 0.0;
 #pragma unroll
   for (int j = 0; j < kGroups; ++j) {
     if (j >= groups) break;
     g[j].fresh();
 #pragma unroll
     for (int i = 0; i < D::kVec; ++i) {
-      s += exp2_f64(fma((double)g[j].get(i), c, -b));
+      s += weight(g[j].get(i));
       if (i % 4 == 3) __builtin_amdgcn_sched_barrier(0);  // bounds the registers in use
     }
   }
-  s = wave_sum(s);
-  if (!(s < 0x1p1000)) {
-    const bool odd = __ballot(maximum()) != 0;
-    m = wave_max_f32(m);
-    b = m == -INFINITY ? 0.0 : (double)m * c;
-    s = 0.0;
+  return wave_sum(s);
+}
+
+template <class D>
+__device__ __forceinline__ float max_groups(Group<D> (&g)[kGroups], bool& odd) {
+  float m = -INFINITY;
+  odd = false;
 #pragma unroll
-    for (int j = 0; j < kGroups; ++j) {
-      g[j].fresh();
+  for (int j = 0; j < kGroups; ++j) {
+    g[j].fresh();
 #pragma unroll
-      for (int i = 0; i < D::kVec; ++i) {
-        const float z = g[j].get(i);
-        s += z == -INFINITY ? 0.0 : exp2_f64(fma((double)z, c, -b));
-        if (i % 4 == 3) __builtin_amdgcn_sched_barrier(0);
-      }
+    for (int i = 0; i < D::kVec; ++i) {
+      m = fmaxf(m, g[j].get(i));
+      odd |= !(g[j].get(i) < INFINITY);
     }
-    s = odd ? (double)NAN : wave_sum(s);
   }
-  return {m, s};
+  odd = __ballot(odd) != 0;
+  return wave_max_f32(m);
+}
+
+// From the maximum of all, masked tokens left out; out of line, as it is rare.
+template <class D>
+__device__ __noinline__ Part whole_again(Groups<D> v, double c) {
+  bool odd;
+  const float m = max_groups<D>(v.g, odd);
+  const double b = m == -INFINITY ? 0.0 : (double)m * c;
+  const double s = sum_groups<D>(v.g, kGroups, [&](float z) LP_INLINE {
+    return z == -INFINITY ? 0.0 : exp2_f64(fma((double)z, c, -b));
+  });
+  return {m, odd ? (double)NAN : s};
+}
+
+template <class D>
+__device__ __forceinline__ Part whole_part(Groups<D>& v, int groups, double c, bool top) {
+  Part p = {0.0f, 0.0};
+  if (top) {
+    bool odd;
+    p.m = max_groups<D>(v.g, odd);
+    const double b = (double)p.m * c;
+    p.s = sum_groups<D>(v.g, groups,
+                        [&](float z) LP_INLINE { return exp2_f64(fma((double)z, c, -b)); });
+  } else {
+    p.s = sum_groups<D>(v.g, groups, [&](float z) LP_INLINE { return exp2_f64((double)z * c); });
+  }
+  return p.s > 0x1p-1000 && p.s < 0x1p1000 ? p : whole_again(v, c);
 }
 
 __device__ __forceinline__ bool is_whole(const Settings& s) {
@@ -894,13 +906,17 @@ __device__ __forceinline__ void whole_rows(const SelectArgs& a, int block) {
       const int c0 = (int)max(lo - n * chunks, (int64_t)0);
       const int c1 = (int)min(hi - n * chunks, (int64_t)chunks);
       SelectPart* parts = a.whole + n * chunks * kWaves + wave;
-      row.for_chunks(c0, c1, [&](Group<D>(&g)[kGroups], int k) LP_INLINE {
+      Groups<D> v, next;
+      row.load(v.g, c0);
+      for (int k = c0; k < c1; ++k) {
+        if (k + 1 < c1) row.load(next.g, k + 1);
         const int left = row.V - k * chunk_of<D>() - wave * 64 * D::kVec;
         Part p = {-INFINITY, 0.0};
         if (left > 0)
-          p = whole_part<D>(g, (left - 1) / (kThreads * D::kVec) + 1, c, min_ps >> i & 1);
+          p = whole_part<D>(v, (left - 1) / (kThreads * D::kVec) + 1, c, min_ps >> i & 1);
         if (lane == 0) parts[k * kWaves] = p;
-      });
+        v = next;
+      }
     }
   }
 }
@@ -1682,8 +1698,8 @@ __device__ __noinline__ void list_by_buckets(SelectArgs a, Settings st, int64_t 
   else finish_draw<kJob>(a, st, n, sh.list, want, ln_all, sh);
 }
 
-// A row's parts joined by a wave: its maximum (of a kWhole row, one that suffices
-// as a base), and the sum of all weights from there. NaN: there is none.
+// A row's parts joined by a wave: its maximum (of a kWhole row, what suffices as a
+// base), and the sum of all weights from there. NaN: there is none.
 struct Whole {
   float top;
   double sum;
