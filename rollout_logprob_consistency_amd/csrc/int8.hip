@@ -183,20 +183,44 @@ __global__ __launch_bounds__(64 * kStreamWaves) void stream_kernel(Int8Args a) {
   for (int j = 0; j < kNT; ++j)
 #pragma unroll
     for (int i = 0; i < kTiles; ++i) acc[j][i] = i32x4{0, 0, 0, 0};
-  for (int k = wave; k < nk; k += kStreamWaves) {
+  // Two stages in registers: one in flight while the other is multiplied. Behind
+  // the wave's last stage that one is read again, so that every turn issues the
+  // same loads.
+  struct Stage {
+    i32x4 w[kTiles][2], x[kNT][2];
+  };
+  const int mine = (nk - wave + kStreamWaves - 1) / kStreamWaves;  // 0: none
+  auto issue = [&](Stage& s, int i) __attribute__((always_inline)) {
+    const int k = min(wave + kStreamWaves * i, nk - 1);
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      i32x4 x[kNT];
+    for (int i = 0; i < kTiles; ++i)
 #pragma unroll
-      for (int j = 0; j < kNT; ++j) x[j] = load(xres, xoff[j] + 64 * c, k);
+      for (int c = 0; c < 2; ++c) s.w[i][c] = load(wres, woff[i] + 64 * c, k);
 #pragma unroll
-      for (int i = 0; i < kTiles; ++i) {
-        const i32x4 w = load(wres, woff[i] + 64 * c, k);
+    for (int j = 0; j < kNT; ++j)
 #pragma unroll
-        for (int j = 0; j < kNT; ++j) acc[j][i] = mma(w, x[j], acc[j][i]);
-      }
-    }
+      for (int c = 0; c < 2; ++c) s.x[j][c] = load(xres, xoff[j] + 64 * c, k);
+    __builtin_amdgcn_sched_barrier(0);  // (left alone, loads sink down to their first use)
+  };
+  auto multiply = [&](const Stage& s) __attribute__((always_inline)) {
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+      for (int i = 0; i < kTiles; ++i)
+#pragma unroll
+        for (int j = 0; j < kNT; ++j) acc[j][i] = mma(s.w[i][c], s.x[j][c], acc[j][i]);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  Stage even, odd;
+  issue(even, 0);
+  int i = 0;
+  for (; i + 2 <= mine; i += 2) {
+    issue(odd, i + 1);
+    multiply(even);
+    issue(even, i + 2);
+    multiply(odd);
   }
+  if (i < mine) multiply(even);
 #pragma unroll
   for (int j = 0; j < kNT; ++j)
 #pragma unroll
