@@ -9,7 +9,8 @@ hazards around its inline-assembly MFMAs (isa_check.py); a violation fails
 the build. The comparison kernel's assembly is checked for ds_bpermute (its
 reductions use DPP, ds_swizzle and readlane). These files' and int8.hip's buffer
 -> LDS copies (inline assembly) are checked for VALU writes of their SGPR
-operands fewer than 5 wait states before them.
+operands fewer than 5 wait states before them, and int8.hip's tile kernels for
+registers parked in accumulators.
 """
 
 from __future__ import annotations
@@ -130,7 +131,8 @@ def check_compare_isa(objdir: str, extra: list[str] | None = None, verbose: bool
 
 
 def check_int8_isa(objdir: str, extra: list[str] | None = None, verbose: bool = False) -> None:
-    """Compile int8.hip to device assembly and check its buffer -> LDS copies."""
+    """Compile int8.hip to device assembly and check its tile kernels: their
+    buffer -> LDS copies, and that no register is parked in an accumulator."""
     from rollout_logprob_consistency_amd import isa_check
     src = os.path.join(CSRC, "int8.hip")
     out = os.path.join(objdir, "int8.device.s")
@@ -140,9 +142,13 @@ def check_int8_isa(objdir: str, extra: list[str] | None = None, verbose: bool = 
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"hipcc -S failed for {src}:\n{r.stdout}\n{r.stderr}")
-    problems = isa_check.check_lds_dma_sgpr(open(out).read(), "tile_kernel")
+    text = open(out).read()
+    problems = isa_check.check_lds_dma_sgpr(text, "tile_kernel")
     if problems:
         raise RuntimeError("buffer -> LDS copy SGPR hazard check failed:\n" + "\n".join(problems[:20]))
+    problems = isa_check.check_no_parked_registers(text, "tile_kernel")
+    if problems:
+        raise RuntimeError("accumulator check failed:\n" + "\n".join(problems))
 
 
 if __name__ == "__main__":

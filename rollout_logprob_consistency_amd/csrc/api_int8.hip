@@ -88,6 +88,7 @@ lp_status lp_logits_int8(const int8_t* x, int64_t ldx, const float* x_scale, con
   bool go;
   const lp_status st = product_args(x, ldx, x_scale, w, ldw, w_scale, T, H, V, &a, &go);
   if (st != LP_OK || !go) return st;
+  if (ld_out > lp::kInt8StrideMax) return LP_EUNSUPPORTED;
   const lp::Int8Workspace ws = lp::int8_workspace_layout(T, H, 0);
   if (!out || !aligned(out, (uintptr_t)lp::dtype_bytes(dtype)) ||
       !workspace_ok(workspace, workspace_bytes, ws))
@@ -128,7 +129,6 @@ lp_status lp_score_int8(const int8_t* x, int64_t ldx, const float* x_scale, cons
   a.scale2 = (float)(1.4426950408889634 / (double)temperature);
   a.part_m = reinterpret_cast<float*>(base + ws.off_m);
   a.part_s = reinterpret_cast<float*>(base + ws.off_s);
-  a.tval = reinterpret_cast<float*>(base + ws.off_t);
   a.out_lp = out_logprob;
   a.out_lse = out_lse;
   a.bad_rows = bad_rows;

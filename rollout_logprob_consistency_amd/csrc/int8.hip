@@ -10,15 +10,16 @@
 // behind it, which block_lse and the merge fix.
 //
 // Placement. A block is 128 vocabulary rows by 16 tokens of a wave: eight MFMA
-// tiles, whose row m of tile i is vocabulary row 32 (m / 4) + 4 i + m % 4. An
-// MFMA's result has the token l & 15 and the rows 4 (l >> 4) + r, r < 4, in
-// lane l; so lane l holds the 32 vocabulary rows from 32 (l >> 4) on, one after
-// the other: logits are stored in whole 16-byte words, and the reduction over
-// the vocabulary is mostly inside a lane.
+// tiles, whose row m of tile i is vocabulary row
+//   32 (i / 2) + 8 (m / 4) + 4 (i % 2) + m % 4.
+// An MFMA's result has the token l & 15 and the rows 4 (l >> 4) + r, r < 4, in
+// lane l; so lane l holds four runs of eight vocabulary rows, run q from
+// 32 q + 8 (l >> 4) on: a run of 16-bit logits is one 16-byte store, the four
+// lanes of a token store 64 bytes side by side, and the reduction over the
+// vocabulary is mostly inside a lane.
 #include <math.h>
 
 #include <algorithm>
-#include <type_traits>
 
 #include "int8_internal.h"
 #include "tile_common.h"
@@ -49,7 +50,12 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc_of(const void* base, int6
 
 // The row of W that lane l's fragment of tile i holds, from the block's first.
 __device__ __forceinline__ int fragment_row(int lane, int i) {
-  return 32 * ((lane & 15) >> 2) + 4 * i + (lane & 3);
+  return 32 * (i >> 1) + 8 * ((lane & 15) >> 2) + 4 * (i & 1) + (lane & 3);
+}
+// The vocabulary row of a lane's k-th result (tile k / 4, register k % 4), from
+// the block's first; rows ascend with k. lg = lane >> 4.
+__device__ __forceinline__ int result_row(int lg, int k) {
+  return 32 * (k >> 3) + 8 * lg + (k & 7);
 }
 
 // ---- Scores -----------------------------------------------------------------
@@ -63,24 +69,28 @@ __device__ __forceinline__ float logit(int sum, float xs, float ws) {
   return z;
 }
 
-// Maximum and sum of exp2(z scale2 - maximum) of a block for the lane's token,
-// z(k) its logit of the lane's k-th row (-inf behind the vocabulary): over the
-// lane's rows in ascending order, then the lanes l ^ 16 and l ^ 32, which end
-// with the same bits. A NaN or +inf logit makes the sum NaN.
-template <class Z>
-__device__ __forceinline__ void block_lse(Z z, float scale2, float& m_out, float& s_out) {
-  float m = -INFINITY;
+// Maximum of z = y f (log2 units) and sum of 2^(z - maximum) of a block for the
+// lane's token, y[k] the lane's k-th row's (-inf f behind the vocabulary): over the
+// lane's rows in ascending order, then the lanes l ^ 16 and l ^ 32, which end with
+// the same bits. A NaN or +inf logit makes the sum NaN.
+__device__ __forceinline__ void block_lse(const float (&y)[kPerLane], float f, float& m_out,
+                                          float& s_out) {
+  float hi = y[0], lo = y[0];
 #pragma unroll
-  for (int k = 0; k < kPerLane; ++k) m = fmaxf(m, z(k));
+  for (int k = 1; k < kPerLane; ++k) {
+    hi = fmaxf(hi, y[k]);
+    lo = fminf(lo, y[k]);
+  }
+  float m = (f < 0.0f ? lo : hi) * f;
   m = fmaxf(m, xor_lane<16>(m));
   m = fmaxf(m, xor_lane<32>(m));
-  const float m2 = m * scale2, base = m == -INFINITY ? 0.0f : m2;
+  const float base = m == -INFINITY ? 0.0f : m;
   float s = 0.0f;
 #pragma unroll
-  for (int k = 0; k < kPerLane; ++k) s += fast_exp2(__builtin_fmaf(z(k), scale2, -base));
+  for (int k = 0; k < kPerLane; ++k) s += fast_exp2(__builtin_fmaf(y[k], f, -base));
   s += xor_lane<16>(s);
   s += xor_lane<32>(s);
-  m_out = m2;
+  m_out = m;
   s_out = s;
 }
 
@@ -93,57 +103,143 @@ __device__ __forceinline__ void lse_fold(float& M, float& S, float m, float s) {
 
 // ---- What a wave does with a block's sums -----------------------------------
 
-// acc[i][r]: the sum of the lane's token and vocabulary row v0 + 32 lg + 4 i + r
-// of the block that starts at v0.
-template <class D>
-__device__ __forceinline__ void store_logits(const Int8Args& a, const i32x4 (&acc)[kTiles], int v0,
-                                             int t, int lg) {
-  if (t >= a.T) return;
-  const int v = v0 + 32 * lg;
-  const float xs = a.x_scale[t];
-  typename D::Raw* p = static_cast<typename D::Raw*>(a.out) + (int64_t)t * a.ld_out;
+// The scales of a lane's rows of the block that starts at v0; rows behind V take
+// the last one's.
+struct RowScales {
+  float s[kPerLane];
+};
+__device__ __forceinline__ RowScales row_scales(const Int8Args& a, int v0, int lg) {
+  RowScales w;
+  if (v0 + kInt8BlockV <= a.V) {
+    const Global<const Words> p = (Global<const Words>)(const Words*)(a.w_scale + v0 + 8 * lg);
 #pragma unroll
-  for (int k0 = 0; k0 < kPerLane; k0 += D::kVec) {
-    if (v + k0 >= a.V) break;
-    Group<D> g = {};
-#pragma unroll
-    for (int e = 0; e < D::kVec; ++e) {
-      const int k = k0 + e;
-      const float ws = read_global(a.w_scale, min(v + k, a.V - 1));
-      g.set(e, D::round(logit(acc[k / 4][k % 4], xs, ws)));
+    for (int q = 0; q < kTiles; ++q) {
+      const Words x = p[8 * (q >> 1) + (q & 1)];
+      w.s[4 * q] = __uint_as_float(x.x);
+      w.s[4 * q + 1] = __uint_as_float(x.y);
+      w.s[4 * q + 2] = __uint_as_float(x.z);
+      w.s[4 * q + 3] = __uint_as_float(x.w);
     }
-    store_group<D>(p, v + k0, a.V, g);
-  }
-}
-
-__device__ __forceinline__ float rounded(float z, bool bf16) {
-  return bf16 ? (float)(__bf16)z : z;
-}
-
-__device__ __forceinline__ void store_partial(const Int8Args& a, const i32x4 (&acc)[kTiles], int v0,
-                                              int t, int lg) {
-  const int v = v0 + 32 * lg;
-  const float xs = a.x_scale[min(t, a.T - 1)];
-  auto z = [&](int k) __attribute__((always_inline)) {
-    const float ws = read_global(a.w_scale, min(v + k, a.V - 1));
-    const float x = rounded(logit(acc[k / 4][k % 4], xs, ws), a.bf16_logits);
-    return v + k < a.V ? x : -INFINITY;
-  };
-  float m, s;
-  block_lse(z, a.scale2, m, s);
-  if (t >= a.T) return;
-  const int64_t at = a.ids[t] - v;
-  if (at >= 0 && at < kPerLane && v + at < a.V) {
-    float x = 0.0f;
+  } else {
 #pragma unroll
-    for (int k = 0; k < kPerLane; ++k) x = k == (int)at ? z(k) : x;
-    a.tval[t] = x * a.scale2;
+    for (int k = 0; k < kPerLane; ++k)
+      w.s[k] = read_global(a.w_scale, min(v0 + result_row(lg, k), a.V - 1));
   }
-  if (lg == 0) {
-    const int64_t o = (int64_t)(v0 / kInt8BlockV) * a.T + t;
-    a.part_m[o] = m;
-    a.part_s[o] = s;
+  return w;
+}
+
+// What a kernel makes of the sums: logits of type D, or scores, of logits in fp32
+// or rounded to bf16 first.
+template <class D>
+struct Logits {
+  using Type = D;
+};
+struct Scores {};
+struct RoundedScores {};
+
+// What of the outputs a wave's block reaches, as a buffer: lanes without a token,
+// or a token without a place, store behind its end, which drops it. So no lane is
+// ever masked while the accumulators are taken out; in a masked region the compiler
+// has parked registers in freed accumulators for the lanes at work alone (the build
+// looks that no accumulator is written but by an MFMA).
+struct Place {
+  uint8_t* p;
+  uint32_t bytes;
+  uint32_t token;  // the lane's token's offset
+};
+
+// Of the block that starts at v0, for the 16 tokens from t0 on (or `tokens`, 16 by
+// 16); lane: in its row of 16.
+template <class D>
+__device__ __forceinline__ Place place_of(Logits<D>, const Int8Args& a, int v0, int t0, int tokens,
+                                          int lane) {
+  constexpr int kSize = sizeof(typename D::Raw);
+  const int rows = min(a.T - t0, tokens);
+  return {static_cast<uint8_t*>(a.out) + ((int64_t)t0 * a.ld_out + v0) * kSize,
+          rows > 0 ? (uint32_t)(((int64_t)(rows - 1) * a.ld_out + a.V - v0) * kSize) : 0u,
+          (uint32_t)((lane & 15) * a.ld_out) * kSize};
+}
+template <class Out>
+__device__ __forceinline__ Place place_of(Out, const Int8Args&, int, int, int, int) {
+  return {};
+}
+
+// The block that starts at v0, for 16 tokens from t on, the j-th 16 of the place's;
+// sums[k] is the lane's k-th sum, xs its token's scale.
+template <class D>
+__device__ __forceinline__ void finish_block(Logits<D>, const Int8Args& a, const Place& at, int j,
+                                             const int (&sums)[kPerLane], const RowScales& w,
+                                             int v0, int, float xs, int lg) {
+  constexpr int kSize = sizeof(typename D::Raw);
+  typedef uint32_t Quad __attribute__((ext_vector_type(4)));
+  const __amdgpu_buffer_rsrc_t r = row_rsrc(at.p, at.bytes);
+  const uint32_t off = at.token + (uint32_t)(16 * j * a.ld_out) * kSize + 8 * lg * kSize;
+  if (v0 + kInt8BlockV <= a.V) {
+#pragma unroll
+    for (int k0 = 0; k0 < kPerLane; k0 += D::kVec) {
+      Group<D> g = {};
+#pragma unroll
+      for (int e = 0; e < D::kVec; ++e) g.set(e, D::round(logit(sums[k0 + e], xs, w.s[k0 + e])));
+      __builtin_amdgcn_raw_buffer_store_b128(Quad{g.w[0], g.w[1], g.w[2], g.w[3]}, r,
+                                             off + result_row(0, k0) * kSize, 0, 0);
+    }
+  } else {
+    int left = a.V - v0 - 8 * lg;
+    asm volatile("" : "+v"(left));  // (or all tokens' comparisons are made, and kept, at once)
+#pragma unroll
+    for (int k = 0; k < kPerLane; ++k) {
+      const typename D::Raw z = D::round(logit(sums[k], xs, w.s[k]));
+      const uint32_t o = result_row(0, k) < left ? off + result_row(0, k) * kSize : 0xFFFFFFFCu;
+      if constexpr (kSize == 4) __builtin_amdgcn_raw_buffer_store_b32(z, r, o, 0, 0);
+      else __builtin_amdgcn_raw_buffer_store_b16(z, r, o, 0, 0);
+    }
   }
+}
+
+// A partial of the block; lanes that have none store behind the plane's end.
+__device__ __forceinline__ void store_partial(const Int8Args& a, const float (&y)[kPerLane],
+                                              float f, int v0, int t, int lg) {
+  float m, s;
+  block_lse(y, f, m, s);
+  const int64_t plane = (int64_t)(v0 / kInt8BlockV) * a.T;
+  const uint32_t bytes = (uint32_t)a.T * 4, at = lg == 0 ? (uint32_t)t * 4 : bytes;
+  __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(m), row_rsrc(a.part_m + plane, bytes), at,
+                                        0, 0);
+  __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(s), row_rsrc(a.part_s + plane, bytes), at,
+                                        0, 0);
+}
+
+__device__ __forceinline__ void mask_tail(const Int8Args& a, float (&y)[kPerLane], float f, int v0,
+                                          int lg) {
+  if (v0 + kInt8BlockV <= a.V) return;
+  const float none = f < 0.0f ? INFINITY : -INFINITY;
+  int left = a.V - v0 - 8 * lg;
+  asm volatile("" : "+v"(left));  // (or all tokens' comparisons are made, and kept, at once)
+#pragma unroll
+  for (int k = 0; k < kPerLane; ++k) y[k] = result_row(0, k) < left ? y[k] : none;
+}
+
+// A token's scale is left to the end (y = S w_scale, z = y x_scale), which spares
+// a product a logit.
+__device__ __forceinline__ float score_of(Scores, int sum, float, float ws) {
+  return (float)sum * ws;
+}
+__device__ __forceinline__ float factor_of(Scores, float xs, float scale2) { return xs * scale2; }
+__device__ __forceinline__ float score_of(RoundedScores, int sum, float xs, float ws) {
+  return (float)(__bf16)logit(sum, xs, ws);
+}
+__device__ __forceinline__ float factor_of(RoundedScores, float, float scale2) { return scale2; }
+
+template <class Out>
+__device__ __forceinline__ void finish_block(Out out, const Int8Args& a, const Place&, int,
+                                             const int (&sums)[kPerLane], const RowScales& w,
+                                             int v0, int t, float xs, int lg) {
+  const float f = factor_of(out, xs, a.scale2);
+  float y[kPerLane];
+#pragma unroll
+  for (int k = 0; k < kPerLane; ++k) y[k] = score_of(out, sums[k], xs, w.s[k]);
+  mask_tail(a, y, f, v0, lg);
+  store_partial(a, y, f, v0, t, lg);
 }
 
 // ---- Streaming kernel ---------------------------------------------------------
@@ -153,7 +249,7 @@ __device__ __forceinline__ void store_partial(const Int8Args& a, const i32x4 (&a
 // tiles. Fragments go from memory straight into registers.
 constexpr int kStreamWaves = 4;
 
-template <int kNT, class D>  // D: the logits' type, or void for scores
+template <int kNT, class Out>
 __global__ __launch_bounds__(64 * kStreamWaves) void stream_kernel(Int8Args a) {
   __shared__ int red[kStreamWaves][kNT][kPerLane][64];
   const int lane = threadIdx.x & 63, lcol = lane & 15, lg = lane >> 4;
@@ -221,23 +317,24 @@ __global__ __launch_bounds__(64 * kStreamWaves) void stream_kernel(Int8Args a) {
     multiply(odd);
   }
   if (i < mine) multiply(even);
+  const RowScales scales = row_scales(a, v0, lg);
+  const Place place = place_of(Out(), a, v0, t0, 16 * kNT, lane);
 #pragma unroll
   for (int j = 0; j < kNT; ++j)
 #pragma unroll
     for (int k = 0; k < kPerLane; ++k) red[wave][j][k][lane] = acc[j][k / 4][k % 4];
   __syncthreads();
   for (int j = wave; j < kNT; j += kStreamWaves) {
-    i32x4 sum[kTiles];
+    int sums[kPerLane];
 #pragma unroll
     for (int k = 0; k < kPerLane; ++k) {
-      int s = 0;
+      sums[k] = 0;
 #pragma unroll
-      for (int w = 0; w < kStreamWaves; ++w) s += red[w][j][k][lane];
-      sum[k / 4][k % 4] = s;
+      for (int w = 0; w < kStreamWaves; ++w) sums[k] += red[w][j][k][lane];
     }
     const int t = t0 + 16 * j + lcol;
-    if constexpr (std::is_void_v<D>) store_partial(a, sum, v0, t, lg);
-    else store_logits<D>(a, sum, v0, t, lg);
+    finish_block(Out(), a, place, j, sums, scales, v0, t, read_global(a.x_scale, min(t, a.T - 1)),
+                 lg);
   }
 }
 
@@ -247,7 +344,10 @@ __global__ __launch_bounds__(64 * kStreamWaves) void stream_kernel(Int8Args a) {
 // two alternating LDS buffers of 64 KiB; the 16-byte chunks of a row are
 // permuted (swz_w, swz_x) so that the fragment reads meet no bank conflicts. One
 // barrier a stage: the MFMAs of a stage's second half are carried across it, and
-// the next stage's copies are spread over the whole stage.
+// the next stage's copies are spread over the whole stage. A workgroup stays on
+// its CU and takes tile after tile: during a tile's last stage the next one's
+// first is copied, so that the sums' scales, roundings and stores (15 % of a tile
+// of 4 096 hidden elements) are all that the MFMAs wait for.
 constexpr int kTileRows = 256;                  // of W, and tokens
 constexpr int kTileThreads = 256;
 constexpr int kUnitB = kTileRows * kInt8StageK; // 32 KiB of either operand
@@ -255,57 +355,69 @@ constexpr int kBufferB = 2 * kUnitB;
 constexpr int kUnitCopies = kUnitB / 1024 / 4;  // 1-KiB copies per wave (8)
 constexpr int kGroupV = 4;                      // vocabulary tiles per scheduling group
 constexpr int kSlotsPerCopy = 6;                // MFMAs from one copy to the next
+constexpr int kCus = 256;
 static_assert(kSlotsPerCopy * 2 * kUnitCopies < 2 * kTiles * kTiles, "copies fit in a stage");
 
 // Physical chunk of logical chunk c in LDS row `row`; its own inverse. A wave's
 // read takes the chunks 4 h + (l >> 4) of sixteen rows: of X consecutive ones, of
-// W those of fragment_row, 32 a + 4 i + b with a, b < 4.
+// W those of fragment_row, 8 a + b from some multiple of 4 on, a, b < 4.
 __device__ __forceinline__ int swz_x(int row, int c) { return c ^ (row & 7); }
 __device__ __forceinline__ int swz_w(int row, int c) {
-  return c ^ ((row & 3) | ((row >> 3) & 4));
+  return c ^ ((row & 3) | ((row >> 1) & 4));
 }
 
-template <class D>  // the logits' type, or void for scores
+// Where a tile lies: its operands' first bytes, and how many there are from there.
+struct TileAt {
+  const int8_t *w, *x;
+  uint32_t w_bytes, x_bytes;
+  int v0, t0;
+};
+__device__ __forceinline__ TileAt tile_at(const Int8Args& a, int tile, int n_vt, int n_tt, int nk) {
+  int vt, tt;
+  tile_of(tile, n_vt, n_tt, kGroupV, vt, tt);
+  TileAt t;
+  t.v0 = __builtin_amdgcn_readfirstlane(vt) * kTileRows;
+  t.t0 = __builtin_amdgcn_readfirstlane(tt) * kTileRows;
+  t.w = a.w + (int64_t)t.v0 * a.ldw;
+  t.x = a.x + (int64_t)t.t0 * a.ldx;
+  t.w_bytes = span_bytes((uint64_t)((int64_t)(a.V - t.v0 - 1) * a.ldw + (a.H + 15) / 16 * 16));
+  t.x_bytes =
+      span_bytes((uint64_t)((int64_t)(a.T - t.t0 - 1) * a.ldx + (int64_t)nk * kInt8StageK));
+  return t;
+}
+
+template <class Out>
 __global__ __launch_bounds__(kTileThreads, 1) void tile_kernel(Int8Args a, int n_vt, int n_tt) {
   __shared__ __attribute__((aligned(1024))) char ring[2 * kBufferB];
-  int vt, tt;
-  tile_of(blockIdx.x, n_vt, n_tt, kGroupV, vt, tt);
-  vt = __builtin_amdgcn_readfirstlane(vt);
-  tt = __builtin_amdgcn_readfirstlane(tt);
-  const int v0 = vt * kTileRows, t0 = tt * kTileRows;
   const int lane = threadIdx.x & 63, lcol = lane & 15, lg = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave & 1, wn = wave >> 1;
+  const int nk = (a.H + kInt8StageK - 1) / kInt8StageK;
+  const int n_tiles = n_vt * n_tt;
 
   // Copy j of a unit: wave w fills rows 8 (4 j + w) .. + 7, lane l the physical
-  // chunk l & 7 of row l >> 3 of them. Bit 5 of a row is j's lowest bit, so odd
-  // copies of W take the other half of a row. Rows behind the matrices read as
-  // zeros (the resources end there) and their results are not stored.
-  const int nk = (a.H + kInt8StageK - 1) / kInt8StageK;
-  const int64_t w_bytes = (int64_t)(a.V - v0 - 1) * a.ldw + (a.H + 15) / 16 * 16;
-  const int64_t x_bytes = (int64_t)(a.T - t0 - 1) * a.ldx + (int64_t)nk * kInt8StageK;
-  const __amdgpu_buffer_rsrc_t wres = rsrc_of(a.w + (int64_t)v0 * a.ldw, w_bytes);
-  const __amdgpu_buffer_rsrc_t xres = rsrc_of(a.x + (int64_t)t0 * a.ldx, x_bytes);
+  // chunk l & 7 of row l >> 3 of them. Rows behind the matrices read as zeros
+  // (the resources end there) and their results are not stored.
   const uint32_t ldw = (uint32_t)a.ldw, ldx = (uint32_t)a.ldx;
-  const uint32_t row = (uint32_t)(8 * wave + (lane >> 3));
-  const uint32_t offW0 = row * ldw + 16 * swz_w(lane >> 3, lane & 7);
-  const uint32_t offW1 = row * ldw + 16 * (swz_w(lane >> 3, lane & 7) ^ 4);
-  const uint32_t offX = row * ldx + 16 * swz_x(lane >> 3, lane & 7);
+  const int row = 8 * wave + (lane >> 3);
+  const uint32_t offW = (uint32_t)row * ldw + 16 * swz_w(row, lane & 7);
+  const uint32_t offX = (uint32_t)row * ldx + 16 * swz_x(row, lane & 7);
   const uint32_t lds0 =
       __builtin_amdgcn_readfirstlane((uint32_t)reinterpret_cast<uintptr_t>((lds_char*)ring));
-// Copy c (0 .. 15, W's first) of stage k into buffer b. A stage behind the last
-// one copies that again, into the buffer that nothing reads any more.
-#define COPY(c_, k_, b_)                                                                      \
+  const uint32_t stepW = 32 * ldw, stepX = 32 * ldx;
+  uint32_t voff = offW;
+// Copy c (0 .. 15 in order, W's first) of the stage at byte off_ of a row into
+// buffer b. The offset of the rows goes from copy to copy (one register, by an add
+// that the compiler cannot turn into sixteen).
+#define COPY(c_, wres_, xres_, off_, b_)                                                      \
   do {                                                                                        \
     const bool w_ = (c_) < kUnitCopies;                                                       \
     const uint32_t j_ = (uint32_t)((c_) & (kUnitCopies - 1));                                 \
-    uint32_t voff_;                                                                           \
-    asm volatile("v_add_u32 %0, %1, %2"                                                       \
-                 : "=v"(voff_)                                                                \
-                 : "s"(j_ * 32 * (w_ ? ldw : ldx)), "v"(w_ ? ((j_ & 1) ? offW1 : offW0) : offX)); \
-    copy_lds(w_ ? wres : xres,                                                                \
+    if (j_ == 0) voff = w_ ? offW : offX;                                                     \
+    else asm volatile("v_add_u32 %0, %1, %0" : "+v"(voff) : "s"(w_ ? stepW : stepX));         \
+    copy_lds(w_ ? (wres_) : (xres_),                                                          \
              lds0 + (uint32_t)(b_) * kBufferB + (w_ ? 0u : (uint32_t)kUnitB) + (4 * j_ + wave) * 1024, \
-             voff_, (uint32_t)min((k_), nk - 1) * kInt8StageK);                                \
+             voff, (off_));                                                                   \
   } while (0)
 
   // Fragment reads of half h (64 codes) of a stage.
@@ -313,12 +425,13 @@ __global__ __launch_bounds__(kTileThreads, 1) void tile_kernel(Int8Args a, int n
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const int wr = wm * kInt8BlockV + fragment_row(lane, 0), xr = wn * 128 + lcol;
-    // Tile i adds 4 i rows, which swz_w sees in none of its bits.
+    // Tile i adds 32 (i / 2) + 4 (i % 2) rows, none of the bits that swz_w sees.
     rdW[h] = (uint32_t)(wr * kInt8StageK + 16 * swz_w(wr, 4 * h + lg));
     rdX[h] = (uint32_t)(kUnitB + xr * kInt8StageK + 16 * swz_x(xr, 4 * h + lg));
   }
-#define RD_W(i_, h_, b_) \
-  *reinterpret_cast<const i32x4*>(ring + (rdW[(h_)] + (uint32_t)(b_) * kBufferB) + (i_) * 4 * kInt8StageK)
+#define RD_W(i_, h_, b_)                                                                  \
+  *reinterpret_cast<const i32x4*>(ring + (rdW[(h_)] + (uint32_t)(b_) * kBufferB) +        \
+                                  (32 * ((i_) >> 1) + 4 * ((i_) & 1)) * kInt8StageK)
 #define RD_X(j_, h_, b_) \
   *reinterpret_cast<const i32x4*>(ring + (rdX[(h_)] + (uint32_t)(b_) * kBufferB) + (j_) * 16 * kInt8StageK)
 #define FENCE() __builtin_amdgcn_sched_barrier(0)
@@ -327,10 +440,10 @@ __global__ __launch_bounds__(kTileThreads, 1) void tile_kernel(Int8Args a, int n
   // (z_: from zero sums), while the next step's fragments are read from half rh_
   // of buffer rb_: X tiles 2 g and 2 g + 1 into nx_ during group g < 4, W tile g
   // into fw[g] behind group g, its last use. A stage (two steps, slots from p0_
-  // on) issues its copies of stage ck_ into buffer cb_. The order is fixed.
+  // on) issues the copies of the stage that follows. The order is fixed.
   i32x4 acc[kTiles][kTiles];  // [W tile][X tile]
   i32x4 fw[kTiles], fx0[kTiles], fx1[kTiles];
-#define STEP(do_mma_, z_, do_rd_, mx_, nx_, rh_, rb_, p0_, ck_, cb_)                          \
+#define STEP(do_mma_, z_, do_rd_, mx_, nx_, rh_, rb_, p0_)                                    \
   do {                                                                                        \
     _Pragma("unroll") for (int u = 0; u < kTiles * kTiles; ++u) {                             \
       const int g_ = u >> 3, j_ = u & 7;                                                      \
@@ -342,46 +455,89 @@ __global__ __launch_bounds__(kTileThreads, 1) void tile_kernel(Int8Args a, int n
       if ((do_rd_) && j_ == 7) fw[g_] = RD_W(g_, (rh_), (rb_));                               \
       const int pu_ = (p0_) + u;                                                              \
       if (pu_ % kSlotsPerCopy == 1 && pu_ / kSlotsPerCopy < 2 * kUnitCopies)                  \
-        COPY(pu_ / kSlotsPerCopy, (ck_), (cb_));                                              \
+        COPY(pu_ / kSlotsPerCopy, wres, xres, off, b ^ 1);                                    \
       FENCE();                                                                                \
     }                                                                                         \
   } while (0)
+// The beginning of stage k: it has landed and every wave is done with the buffer
+// that the next one goes into. That is the same tile's, or the next tile's first
+// (the last tile's own once more, which nothing reads).
+#define STAGE(k_)                                                                             \
+  __builtin_amdgcn_s_waitcnt(0x0070); /* vmcnt(0) lgkmcnt(0) */                               \
+  __syncthreads();                                                                            \
+  uint32_t off = (uint32_t)((k_) + 1) * kInt8StageK;                                          \
+  if ((k_) + 1 == nk) {                                                                       \
+    at = tile_at(a, after < n_tiles ? after : tile, n_vt, n_tt, nk);                          \
+    off = 0u;                                                                                 \
+  }                                                                                           \
+  const __amdgpu_buffer_rsrc_t wres = make_rsrc(at.w, at.w_bytes);                            \
+  const __amdgpu_buffer_rsrc_t xres = make_rsrc(at.x, at.x_bytes);                            \
+  FENCE()
 
-#pragma unroll
-  for (int c = 0; c < 2 * kUnitCopies; ++c) COPY(c, 0, 0);
-  __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0) lgkmcnt(0)
-  __syncthreads();
-  FENCE();
   constexpr int kHalf = kTiles * kTiles;
-  STEP(false, false, true, fx1, fx0, 0, 0, 0, 1, 1);
-  STEP(true, true, true, fx0, fx1, 1, 0, kHalf, 1, 1);
-  for (int k = 1; k < nk; ++k) {
-    const int b = k & 1;
-    __builtin_amdgcn_s_waitcnt(0x0070);
-    __syncthreads();
-    FENCE();
-    STEP(true, false, true, fx1, fx0, 0, b, 0, k + 1, b ^ 1);
-    STEP(true, false, true, fx0, fx1, 1, b, kHalf, k + 1, b ^ 1);
+  TileAt at = tile_at(a, blockIdx.x, n_vt, n_tt, nk);
+  int b = 0;
+  {
+    const __amdgpu_buffer_rsrc_t wres = make_rsrc(at.w, at.w_bytes);
+    const __amdgpu_buffer_rsrc_t xres = make_rsrc(at.x, at.x_bytes);
+#pragma unroll
+    for (int c = 0; c < 2 * kUnitCopies; ++c) COPY(c, wres, xres, 0u, 0);
   }
-  STEP(true, false, false, fx1, fx0, 0, 0, 4 * kHalf, 0, 0);
+  for (int tile = blockIdx.x; tile < n_tiles; tile += gridDim.x) {
+    const int after = tile + (int)gridDim.x;
+    const int v0 = at.v0, t0 = at.t0;
+    {
+      STAGE(0);
+      STEP(false, false, true, fx1, fx0, 0, b, 0);
+      STEP(true, true, true, fx0, fx1, 1, b, kHalf);
+    }
+    for (int k = 1; k < nk; ++k) {
+      b ^= 1;
+      STAGE(k);
+      STEP(true, false, true, fx1, fx0, 0, b, 0);
+      STEP(true, false, true, fx0, fx1, 1, b, kHalf);
+    }
+    // The epilogue's scales, in flight over the last step. What follows from the
+    // lane is formed anew, and a token's part is kept apart from the next one's:
+    // next to the accumulators there are no registers for all of it at once.
+    const int vb = v0 + wm * kInt8BlockV;
+    int lane_e;
+    asm volatile("v_mbcnt_lo_u32_b32 %0, -1, 0\n\tv_mbcnt_hi_u32_b32 %0, -1, %0" : "=v"(lane_e));
+    const int lg_e = lane_e >> 4, t_e = t0 + wn * 128 + (lane_e & 15);
+    const bool there = vb < a.V;
+    RowScales scales = {};
+    float xs[kTiles];
+    if (there) scales = row_scales(a, vb, lg_e);
+#pragma unroll
+    for (int j = 0; j < kTiles; ++j) xs[j] = read_global(a.x_scale, min(t_e + 16 * j, a.T - 1));
+    {
+      // (Slots behind a stage's copies.)
+      const __amdgpu_buffer_rsrc_t wres = make_rsrc(at.w, at.w_bytes), xres = wres;
+      const uint32_t off = 0;
+      STEP(true, false, false, fx1, fx0, 0, b, 4 * kHalf);
+    }
+    b ^= 1;
+    if (there) {
+      const Place place = place_of(Out(), a, vb, t0 + wn * 128, 128, lane_e);
+#pragma unroll
+      for (int j = 0; j < kTiles; ++j) {
+        __builtin_amdgcn_sched_barrier(0);
+        int t = t_e + 16 * j;
+        asm volatile("" : "+v"(t));
+        int sums[kPerLane];
+#pragma unroll
+        for (int k = 0; k < kPerLane; ++k) sums[k] = acc[k >> 2][j][k & 3];
+        finish_block(Out(), a, place, j, sums, scales, vb, t, xs[j], lg_e);
+      }
+    }
+  }
   __builtin_amdgcn_s_waitcnt(0x0070);  // the last copies land before the LDS is given back
+#undef STAGE
 #undef STEP
 #undef COPY
 #undef RD_W
 #undef RD_X
 #undef FENCE
-
-  const int vb = v0 + wm * kInt8BlockV;
-  if (vb >= a.V) return;
-#pragma unroll
-  for (int j = 0; j < kTiles; ++j) {
-    const int t = t0 + wn * 128 + 16 * j + lcol;
-    i32x4 sum[kTiles];
-#pragma unroll
-    for (int i = 0; i < kTiles; ++i) sum[i] = acc[i][j];
-    if constexpr (std::is_void_v<D>) store_partial(a, sum, vb, t, lg);
-    else store_logits<D>(a, sum, vb, t, lg);
-  }
 }
 
 // ---- Merge ------------------------------------------------------------------
@@ -390,10 +546,38 @@ __global__ __launch_bounds__(kTileThreads, 1) void tile_kernel(Int8Args a, int n
 // on the vocabulary alone.
 constexpr int kSegs = 16;
 
+// The target's logit is formed here, once more: its sum is exact, so it has the
+// bits that it has in its block.
+__device__ __forceinline__ int row_sum(const Int8Args& a, int64_t t, int64_t id) {
+  const Global<const Words> x = (Global<const Words>)(const Words*)(a.x + t * a.ldx);
+  const Global<const Words> w = (Global<const Words>)(const Words*)(a.w + id * a.ldw);
+  int s = 0;
+  for (int i = threadIdx.x & 63; i < (a.H + 15) / 16; i += 64) {
+    const Words p = x[i], q = w[i];
+    s = __builtin_amdgcn_sdot4((int)p.x, (int)q.x, s, false);
+    s = __builtin_amdgcn_sdot4((int)p.y, (int)q.y, s, false);
+    s = __builtin_amdgcn_sdot4((int)p.z, (int)q.z, s, false);
+    s = __builtin_amdgcn_sdot4((int)p.w, (int)q.w, s, false);
+  }
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) s += __shfl_xor(s, d);
+  return s;
+}
+
+template <class Out>
 __global__ __launch_bounds__(64 * kSegs) void merge_kernel(Int8Args a) {
-  __shared__ float seg_m[kSegs][64], seg_s[kSegs][64];
+  __shared__ float seg_m[kSegs][64], seg_s[kSegs][64], target[64];
   const int lane = threadIdx.x & 63, seg = threadIdx.x >> 6;
   const int64_t t = (int64_t)blockIdx.x * 64 + lane;
+  for (int i = seg; i < 64; i += kSegs) {
+    const int64_t mine = (int64_t)blockIdx.x * 64 + i;
+    if (mine >= a.T) break;
+    const int64_t id = a.ids[mine];
+    if (id < 0 || id >= a.V) continue;
+    const float xs = a.x_scale[mine];
+    const float z = score_of(Out(), row_sum(a, mine, id), xs, a.w_scale[id]);
+    if (lane == 0) target[i] = z * factor_of(Out(), xs, a.scale2);
+  }
   const int blocks = (a.V + kInt8BlockV - 1) / kInt8BlockV;
   const int per = (blocks + kSegs - 1) / kSegs;
   const int lo = min(blocks, seg * per), hi = min(blocks, lo + per);
@@ -410,7 +594,7 @@ __global__ __launch_bounds__(64 * kSegs) void merge_kernel(Int8Args a) {
   const int64_t id = a.ids[t];
   const bool ok = id >= 0 && id < a.V;
   const float lse2 = M + fast_log2(S);
-  a.out_lp[t] = ok ? (a.tval[t] - lse2) * kLn2 : NAN;
+  a.out_lp[t] = ok ? (target[lane] - lse2) * kLn2 : NAN;
   if (a.out_lse) a.out_lse[t] = lse2 * kLn2;
   if (!ok && a.bad_rows) atomicAdd(a.bad_rows, 1);
 }
@@ -430,24 +614,37 @@ __global__ __launch_bounds__(256) void stage_kernel(Int8Args a, int64_t row) {
   }
 }
 
+// launch(Out()) for what the call wants.
+template <class F>
+void with_output(const Int8Args& a, F launch) {
+  if (!a.out) {
+    if (a.bf16_logits) launch(RoundedScores());
+    else launch(Scores());
+  } else if (a.dtype == LP_F32) {
+    launch(Logits<F32>());
+  } else if (a.dtype == LP_BF16) {
+    launch(Logits<BF16>());
+  } else {
+    launch(Logits<F16>());
+  }
+}
+
 template <int kNT>
 void stream(const Int8Args& a, hipStream_t s) {
   const dim3 grid((uint32_t)((a.V + kInt8BlockV - 1) / kInt8BlockV),
                   (uint32_t)((a.T + 16 * kNT - 1) / (16 * kNT)));
   const int threads = 64 * kStreamWaves;
-  if (!a.out) stream_kernel<kNT, void><<<grid, threads, 0, s>>>(a);
-  else if (a.dtype == LP_F32) stream_kernel<kNT, F32><<<grid, threads, 0, s>>>(a);
-  else if (a.dtype == LP_BF16) stream_kernel<kNT, BF16><<<grid, threads, 0, s>>>(a);
-  else stream_kernel<kNT, F16><<<grid, threads, 0, s>>>(a);
+  with_output(a, [&](auto out) {
+    stream_kernel<kNT, decltype(out)><<<grid, threads, 0, s>>>(a);
+  });
 }
 
 void tiles(const Int8Args& a, hipStream_t s) {
   const int n_vt = (a.V + kTileRows - 1) / kTileRows, n_tt = (a.T + kTileRows - 1) / kTileRows;
-  const dim3 grid((uint32_t)n_vt * (uint32_t)n_tt);
-  if (!a.out) tile_kernel<void><<<grid, kTileThreads, 0, s>>>(a, n_vt, n_tt);
-  else if (a.dtype == LP_F32) tile_kernel<F32><<<grid, kTileThreads, 0, s>>>(a, n_vt, n_tt);
-  else if (a.dtype == LP_BF16) tile_kernel<BF16><<<grid, kTileThreads, 0, s>>>(a, n_vt, n_tt);
-  else tile_kernel<F16><<<grid, kTileThreads, 0, s>>>(a, n_vt, n_tt);
+  const dim3 grid((uint32_t)std::min<int64_t>((int64_t)n_vt * n_tt, kCus));
+  with_output(a, [&](auto out) {
+    tile_kernel<decltype(out)><<<grid, kTileThreads, 0, s>>>(a, n_vt, n_tt);
+  });
 }
 
 }  // namespace
@@ -459,8 +656,7 @@ Int8Workspace int8_workspace_layout(int64_t T, int64_t H, int64_t V) {
   w.off_staged = 0;
   w.off_m = up((size_t)T * (size_t)int8_staged_row(H));
   w.off_s = w.off_m + up(plane);
-  w.off_t = w.off_s + up(plane);
-  w.total = V > 0 ? w.off_t + up((size_t)T * sizeof(float)) : w.off_m;
+  w.total = V > 0 ? w.off_s + up(plane) : w.off_m;
   return w;
 }
 
@@ -485,7 +681,9 @@ hipError_t launch_int8(Int8Args a, hipStream_t stream_) {
   else if (a.T <= 64) stream<4>(a, stream_);
   else tiles(a, stream_);
   if ((e = hipGetLastError()) != hipSuccess || a.out) return e;
-  merge_kernel<<<dim3((uint32_t)((a.T + 63) / 64)), 64 * kSegs, 0, stream_>>>(a);
+  const dim3 grid((uint32_t)((a.T + 63) / 64));
+  if (a.bf16_logits) merge_kernel<RoundedScores><<<grid, 64 * kSegs, 0, stream_>>>(a);
+  else merge_kernel<Scores><<<grid, 64 * kSegs, 0, stream_>>>(a);
   return hipGetLastError();
 }
 

@@ -42,7 +42,6 @@ struct Int8Args {
   float scale2;          // log2(e) / temperature
   float* part_m;         // [blocks][T] maximum of z, log2 units
   float* part_s;         // [blocks][T] sum of exp2(z - maximum)
-  float* tval;           // [T] the target's z, log2 units
   float* out_lp;         // [T]
   float* out_lse;        // [T] or null
   int32_t* bad_rows;     // or null
@@ -53,8 +52,8 @@ struct Int8Args {
 constexpr int64_t int8_staged_row(int64_t H) {
   return (H + kInt8StageK - 1) / kInt8StageK * kInt8StageK;
 }
-// Largest row stride that the kernels read: 256 rows stay inside 32-bit byte
-// offsets.
+// Largest row stride that the kernels read or write: 256 rows of codes, and 128
+// of logits, stay inside 32-bit byte offsets.
 constexpr int64_t kInt8StrideMax = int64_t(1) << 22;
 // Whether the kernels can read x where it lies: whole stages of 16-byte
 // aligned rows.
@@ -64,7 +63,7 @@ inline bool int8_reads_in_place(const int8_t* x, int64_t ldx, int64_t H) {
 }
 
 struct Int8Workspace {
-  size_t off_staged, off_m, off_s, off_t, total;
+  size_t off_staged, off_m, off_s, total;
 };
 // V = 0: rows of logits, no partials.
 Int8Workspace int8_workspace_layout(int64_t T, int64_t H, int64_t V);

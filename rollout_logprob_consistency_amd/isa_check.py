@@ -148,6 +148,23 @@ def check_no_bpermute(asm: str, name_part: str = "compare_kernel") -> list[str]:
     return problems
 
 
+def check_no_parked_registers(asm: str, name_part: str) -> list[str]:
+    """Problems: a missing kernel, or an accumulator written by anything but an
+    MFMA (v_accvgpr_write), or scratch memory, inside it. A tile kernel's sums
+    fill the accumulators and start from an MFMA's constant 0, so such a write is
+    a register that the compiler parks; it has parked one in a region that masks
+    lanes and taken it out for all of them."""
+    bodies = kernel_bodies(asm, name_part)
+    if not bodies:
+        return [f"no kernel matching {name_part!r} in the assembly"]
+    problems = []
+    for name, body in bodies.items():
+        n = len(re.findall(r"^\s*(?:v_accvgpr_write|scratch_(?:load|store))", body, re.M))
+        if n:
+            problems.append(f"{name}: {n} accumulator write(s) or scratch access(es)")
+    return problems
+
+
 # ---------------------------------------------------------------------------
 # Buffer -> LDS copies written as inline assembly (both tile kernels' operand
 # stages, the comparison kernel's window ring): the compiler inserts no wait
