@@ -541,10 +541,14 @@ __global__ __launch_bounds__(kTileThreads, 1) void tile_kernel(Int8Args a, int n
 }
 
 // ---- Merge ------------------------------------------------------------------
-// A workgroup joins 64 tokens' partials: wave w folds the blocks of segment w
-// in ascending order, then the segments are folded in order. The bounds depend
-// on the vocabulary alone.
-constexpr int kSegs = 16;
+// A workgroup joins 16 tokens' partials: the blocks are cut into 64 segments, whose
+// bounds depend on the vocabulary alone, four for each of 16 waves (lane l: token
+// l & 15, segment 4 wave + (l >> 4)). A segment is folded in ascending order, with
+// the loads of eight blocks in flight at a time, then a wave's four, then the waves.
+constexpr int kMergeTokens = 16;
+constexpr int kMergeWaves = 16;
+constexpr int kSegments = 4 * kMergeWaves;
+constexpr int kMergeLoads = 8;
 
 // The target's logit is formed here, once more: its sum is exact, so it has the
 // bits that it has in its block.
@@ -565,32 +569,57 @@ __device__ __forceinline__ int row_sum(const Int8Args& a, int64_t t, int64_t id)
 }
 
 template <class Out>
-__global__ __launch_bounds__(64 * kSegs) void merge_kernel(Int8Args a) {
-  __shared__ float seg_m[kSegs][64], seg_s[kSegs][64], target[64];
-  const int lane = threadIdx.x & 63, seg = threadIdx.x >> 6;
-  const int64_t t = (int64_t)blockIdx.x * 64 + lane;
-  for (int i = seg; i < 64; i += kSegs) {
-    const int64_t mine = (int64_t)blockIdx.x * 64 + i;
-    if (mine >= a.T) break;
+__global__ __launch_bounds__(64 * kMergeWaves) void merge_kernel(Int8Args a) {
+  __shared__ float wave_m[kMergeWaves][kMergeTokens], wave_s[kMergeWaves][kMergeTokens];
+  __shared__ float target[kMergeTokens];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t t0 = (int64_t)blockIdx.x * kMergeTokens, t = t0 + (lane & 15);
+  static_assert(kMergeTokens == kMergeWaves, "a target for each wave");
+  const int64_t mine = t0 + wave;
+  if (mine < a.T) {
     const int64_t id = a.ids[mine];
-    if (id < 0 || id >= a.V) continue;
-    const float xs = a.x_scale[mine];
-    const float z = score_of(Out(), row_sum(a, mine, id), xs, a.w_scale[id]);
-    if (lane == 0) target[i] = z * factor_of(Out(), xs, a.scale2);
+    if (id >= 0 && id < a.V) {
+      const float xs = a.x_scale[mine];
+      const float z = score_of(Out(), row_sum(a, mine, id), xs, a.w_scale[id]);
+      if (lane == 0) target[wave] = z * factor_of(Out(), xs, a.scale2);
+    }
   }
   const int blocks = (a.V + kInt8BlockV - 1) / kInt8BlockV;
-  const int per = (blocks + kSegs - 1) / kSegs;
-  const int lo = min(blocks, seg * per), hi = min(blocks, lo + per);
+  const int per = (blocks + kSegments - 1) / kSegments;
+  const int lo = min(blocks, (4 * wave + (lane >> 4)) * per), hi = min(blocks, lo + per);
+  const int64_t at = min(t, (int64_t)a.T - 1);
   float M = -INFINITY, S = 0.0f;
-  if (t < a.T)
-    for (int b = lo; b < hi; ++b)
-      lse_fold(M, S, a.part_m[(int64_t)b * a.T + t], a.part_s[(int64_t)b * a.T + t]);
-  seg_m[seg][lane] = M;
-  seg_s[seg][lane] = S;
-  __syncthreads();
-  if (seg != 0 || t >= a.T) return;
+  for (int b = 0; b < per; b += kMergeLoads) {
+    float m[kMergeLoads], s[kMergeLoads];
 #pragma unroll
-  for (int g = 1; g < kSegs; ++g) lse_fold(M, S, seg_m[g][lane], seg_s[g][lane]);
+    for (int i = 0; i < kMergeLoads; ++i) {
+      const bool there = lo + b + i < hi;
+      const int64_t o = (int64_t)min(lo + b + i, blocks - 1) * a.T + at;
+      m[i] = read_global(a.part_m, o);
+      s[i] = read_global(a.part_s, o);
+      m[i] = there ? m[i] : -INFINITY;
+      s[i] = there ? s[i] : 0.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < kMergeLoads; ++i) lse_fold(M, S, m[i], s[i]);
+  }
+  // (Either lane of a pair adds the same two products, in its own order.)
+  auto pair = [&](float m, float s) __attribute__((always_inline)) {
+    const float Mn = fmaxf(M, m), base = Mn == -INFINITY ? 0.0f : Mn;
+    const float p = S * fast_exp2(M - base), q = s * fast_exp2(m - base);
+    S = p + q;
+    M = Mn;
+  };
+  pair(xor_lane<16>(M), xor_lane<16>(S));
+  pair(xor_lane<32>(M), xor_lane<32>(S));
+  if (lane < kMergeTokens) {
+    wave_m[wave][lane] = M;
+    wave_s[wave][lane] = S;
+  }
+  __syncthreads();
+  if (threadIdx.x >= kMergeTokens || t >= a.T) return;
+#pragma unroll
+  for (int g = 1; g < kMergeWaves; ++g) lse_fold(M, S, wave_m[g][lane], wave_s[g][lane]);
   const int64_t id = a.ids[t];
   const bool ok = id >= 0 && id < a.V;
   const float lse2 = M + fast_log2(S);
@@ -663,7 +692,7 @@ Int8Workspace int8_workspace_layout(int64_t T, int64_t H, int64_t V) {
 bool int8_grid_ok(int64_t T, int64_t V) {
   const int64_t blocks = (V + kInt8BlockV - 1) / kInt8BlockV, tiles = (T + 63) / 64;
   return tiles <= 65535 && blocks * tiles <= kMaxDispatchItems / (64 * kStreamWaves) &&
-         tiles <= kMaxDispatchItems / (64 * kSegs);
+         (T + kMergeTokens - 1) / kMergeTokens <= kMaxDispatchItems / (64 * kMergeWaves);
 }
 
 hipError_t launch_int8(Int8Args a, hipStream_t stream_) {
@@ -681,9 +710,9 @@ hipError_t launch_int8(Int8Args a, hipStream_t stream_) {
   else if (a.T <= 64) stream<4>(a, stream_);
   else tiles(a, stream_);
   if ((e = hipGetLastError()) != hipSuccess || a.out) return e;
-  const dim3 grid((uint32_t)((a.T + 63) / 64));
-  if (a.bf16_logits) merge_kernel<RoundedScores><<<grid, 64 * kSegs, 0, stream_>>>(a);
-  else merge_kernel<Scores><<<grid, 64 * kSegs, 0, stream_>>>(a);
+  const dim3 grid((uint32_t)((a.T + kMergeTokens - 1) / kMergeTokens));
+  if (a.bf16_logits) merge_kernel<RoundedScores><<<grid, 64 * kMergeWaves, 0, stream_>>>(a);
+  else merge_kernel<Scores><<<grid, 64 * kMergeWaves, 0, stream_>>>(a);
   return hipGetLastError();
 }
 
