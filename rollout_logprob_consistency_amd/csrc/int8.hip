@@ -242,6 +242,17 @@ __device__ __forceinline__ void finish_block(Out out, const Int8Args& a, const P
   store_partial(a, y, f, v0, t, lg);
 }
 
+// The stage that a block of vocabulary rows, or a group of tiles, begins with; it
+// goes round from there. Rows of a power of two of bytes lie on the same few
+// channels at the same place, and workgroups that start together stay together (one
+// row of the 151 936 x 4 096 head 138 us from the first stage on, 114 us from a
+// KiB further for each block; rows of 4 224 bytes 115 us either way). The sums are
+// integers: their order is free.
+constexpr int kRotate = 8;
+__device__ __forceinline__ int first_stage(int block, int nk) {
+  return (int)((uint32_t)block * (uint32_t)kRotate % (uint32_t)nk);
+}
+
 // ---- Streaming kernel ---------------------------------------------------------
 // A workgroup takes one block of vocabulary rows and 16 kNT tokens; its four
 // waves take the K stages in turn (the integer sums may be split anyhow), and
@@ -286,8 +297,10 @@ __global__ __launch_bounds__(64 * kStreamWaves) void stream_kernel(Int8Args a) {
     i32x4 w[kTiles][2], x[kNT][2];
   };
   const int mine = (nk - wave + kStreamWaves - 1) / kStreamWaves;  // 0: none
+  const int first = first_stage(blockIdx.x, nk);
   auto issue = [&](Stage& s, int i) __attribute__((always_inline)) {
-    const int k = min(wave + kStreamWaves * i, nk - 1);
+    int k = min(wave + kStreamWaves * i, nk - 1) + first;
+    k -= k >= nk ? nk : 0;
 #pragma unroll
     for (int i = 0; i < kTiles; ++i)
 #pragma unroll
@@ -339,24 +352,21 @@ __global__ __launch_bounds__(64 * kStreamWaves) void stream_kernel(Int8Args a) {
 }
 
 // ---- Tile kernel --------------------------------------------------------------
-// Four waves compute 256 vocabulary rows x 256 tokens, 128 x 128 each: 256
-// accumulators in the AGPRs. K stages of 128 bytes go from memory straight into
-// two alternating LDS buffers of 64 KiB; the 16-byte chunks of a row are
+// Four waves compute 256 vocabulary rows x 32 kJ tokens, 128 x 16 kJ each: with
+// kJ = 8, 256 accumulators in the AGPRs. K stages of 128 bytes go from memory
+// straight into two alternating LDS buffers of up to 64 KiB; the 16-byte chunks of a row are
 // permuted (swz_w, swz_x) so that the fragment reads meet no bank conflicts. One
 // barrier a stage: the MFMAs of a stage's second half are carried across it, and
 // the next stage's copies are spread over the whole stage. A workgroup stays on
 // its CU and takes tile after tile: during a tile's last stage the next one's
 // first is copied, so that the sums' scales, roundings and stores (15 % of a tile
 // of 4 096 hidden elements) are all that the MFMAs wait for.
-constexpr int kTileRows = 256;                  // of W, and tokens
+constexpr int kTileRows = 256;                      // of W
 constexpr int kTileThreads = 256;
-constexpr int kUnitB = kTileRows * kInt8StageK; // 32 KiB of either operand
-constexpr int kBufferB = 2 * kUnitB;
-constexpr int kUnitCopies = kUnitB / 1024 / 4;  // 1-KiB copies per wave (8)
-constexpr int kGroupV = 4;                      // vocabulary tiles per scheduling group
-constexpr int kSlotsPerCopy = 6;                // MFMAs from one copy to the next
+constexpr int kUnitB = kTileRows * kInt8StageK;     // 32 KiB of W
+constexpr int kUnitCopies = kUnitB / 1024 / 4;      // 1-KiB copies per wave (8)
+constexpr int kGroupV = 4;                          // vocabulary tiles per scheduling group
 constexpr int kCus = 256;
-static_assert(kSlotsPerCopy * 2 * kUnitCopies < 2 * kTiles * kTiles, "copies fit in a stage");
 
 // Physical chunk of logical chunk c in LDS row `row`; its own inverse. A wave's
 // read takes the chunks 4 h + (l >> 4) of sixteen rows: of X consecutive ones, of
@@ -370,14 +380,16 @@ __device__ __forceinline__ int swz_w(int row, int c) {
 struct TileAt {
   const int8_t *w, *x;
   uint32_t w_bytes, x_bytes;
-  int v0, t0;
+  int v0, t0, first;
 };
+template <int kTokens>
 __device__ __forceinline__ TileAt tile_at(const Int8Args& a, int tile, int n_vt, int n_tt, int nk) {
   int vt, tt;
   tile_of(tile, n_vt, n_tt, kGroupV, vt, tt);
   TileAt t;
   t.v0 = __builtin_amdgcn_readfirstlane(vt) * kTileRows;
-  t.t0 = __builtin_amdgcn_readfirstlane(tt) * kTileRows;
+  t.t0 = __builtin_amdgcn_readfirstlane(tt) * kTokens;
+  t.first = first_stage(t.v0 / (kTileRows * kGroupV), nk);
   t.w = a.w + (int64_t)t.v0 * a.ldw;
   t.x = a.x + (int64_t)t.t0 * a.ldx;
   t.w_bytes = span_bytes((uint64_t)((int64_t)(a.V - t.v0 - 1) * a.ldw + (a.H + 15) / 16 * 16));
@@ -386,8 +398,16 @@ __device__ __forceinline__ TileAt tile_at(const Int8Args& a, int tile, int n_vt,
   return t;
 }
 
-template <class Out>
-__global__ __launch_bounds__(kTileThreads, 1) void tile_kernel(Int8Args a, int n_vt, int n_tt) {
+// kJ = 2 leaves room for two workgroups a CU.
+template <int kJ, class Out>
+__global__ __launch_bounds__(kTileThreads, kJ == 2 ? 2 : 1) void tile_kernel(Int8Args a, int n_vt,
+                                                                            int n_tt) {
+  constexpr int kTokens = 32 * kJ, kCopies = kUnitCopies + kJ;
+  constexpr int kBufferB = kUnitB + kTokens * kInt8StageK;
+  constexpr int kHalf = kTiles * kJ;                        // MFMAs of a step
+  constexpr int kSlotsPerCopy = (2 * kHalf - 2) / kCopies;  // from one copy to the next
+  constexpr int kEvery = kSlotsPerCopy < 6 ? kSlotsPerCopy : 6;
+  constexpr int kPerGroup = (kJ + 3) / 4;                   // X reads of a group
   __shared__ __attribute__((aligned(1024))) char ring[2 * kBufferB];
   const int lane = threadIdx.x & 63, lcol = lane & 15, lg = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -406,13 +426,13 @@ __global__ __launch_bounds__(kTileThreads, 1) void tile_kernel(Int8Args a, int n
       __builtin_amdgcn_readfirstlane((uint32_t)reinterpret_cast<uintptr_t>((lds_char*)ring));
   const uint32_t stepW = 32 * ldw, stepX = 32 * ldx;
   uint32_t voff = offW;
-// Copy c (0 .. 15 in order, W's first) of the stage at byte off_ of a row into
-// buffer b. The offset of the rows goes from copy to copy (one register, by an add
-// that the compiler cannot turn into sixteen).
+// Copy c (in order, W's first) of the stage at byte off_ of a row into buffer b.
+// The offset of the rows goes from copy to copy (one register, by an add that the
+// compiler cannot turn into one for each).
 #define COPY(c_, wres_, xres_, off_, b_)                                                      \
   do {                                                                                        \
     const bool w_ = (c_) < kUnitCopies;                                                       \
-    const uint32_t j_ = (uint32_t)((c_) & (kUnitCopies - 1));                                 \
+    const uint32_t j_ = (uint32_t)(w_ ? (c_) : (c_) - kUnitCopies);                           \
     if (j_ == 0) voff = w_ ? offW : offX;                                                     \
     else asm volatile("v_add_u32 %0, %1, %0" : "+v"(voff) : "s"(w_ ? stepW : stepX));         \
     copy_lds(w_ ? (wres_) : (xres_),                                                          \
@@ -424,7 +444,7 @@ __global__ __launch_bounds__(kTileThreads, 1) void tile_kernel(Int8Args a, int n
   uint32_t rdW[2], rdX[2];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    const int wr = wm * kInt8BlockV + fragment_row(lane, 0), xr = wn * 128 + lcol;
+    const int wr = wm * kInt8BlockV + fragment_row(lane, 0), xr = wn * 16 * kJ + lcol;
     // Tile i adds 32 (i / 2) + 4 (i % 2) rows, none of the bits that swz_w sees.
     rdW[h] = (uint32_t)(wr * kInt8StageK + 16 * swz_w(wr, 4 * h + lg));
     rdX[h] = (uint32_t)(kUnitB + xr * kInt8StageK + 16 * swz_x(xr, 4 * h + lg));
@@ -436,26 +456,31 @@ __global__ __launch_bounds__(kTileThreads, 1) void tile_kernel(Int8Args a, int n
   *reinterpret_cast<const i32x4*>(ring + (rdX[(h_)] + (uint32_t)(b_) * kBufferB) + (j_) * 16 * kInt8StageK)
 #define FENCE() __builtin_amdgcn_sched_barrier(0)
 
-  // One step: eight groups (W tile g with X tiles 0 .. 7) on fw and mx_, 64 codes
+  // One step: eight groups (W tile g with all X tiles) on fw and mx_, 64 codes
   // (z_: from zero sums), while the next step's fragments are read from half rh_
-  // of buffer rb_: X tiles 2 g and 2 g + 1 into nx_ during group g < 4, W tile g
-  // into fw[g] behind group g, its last use. A stage (two steps, slots from p0_
-  // on) issues the copies of the stage that follows. The order is fixed.
-  i32x4 acc[kTiles][kTiles];  // [W tile][X tile]
-  i32x4 fw[kTiles], fx0[kTiles], fx1[kTiles];
+  // of buffer rb_: X tiles into nx_ during groups 0 .. 3, W tile g into fw[g]
+  // behind group g, its last use. A stage (two steps, slots from p0_ on) issues the
+  // copies of the stage that follows. The order is fixed.
+  i32x4 acc[kTiles][kJ];  // [W tile][X tile]
+  i32x4 fw[kTiles], fx0[kJ], fx1[kJ];
 #define STEP(do_mma_, z_, do_rd_, mx_, nx_, rh_, rb_, p0_)                                    \
   do {                                                                                        \
-    _Pragma("unroll") for (int u = 0; u < kTiles * kTiles; ++u) {                             \
-      const int g_ = u >> 3, j_ = u & 7;                                                      \
+    _Pragma("unroll") for (int u = 0; u < kHalf; ++u) {                                       \
+      const int g_ = u / kJ, j_ = u % kJ;                                                     \
       if (do_mma_)                                                                            \
         acc[g_][j_] = mma(fw[g_], mx_[j_], (z_) ? i32x4{0, 0, 0, 0} : acc[g_][j_]);           \
-      if ((do_rd_) && g_ < 4 && j_ == 2) nx_[2 * (g_ & 3)] = RD_X(2 * (g_ & 3), (rh_), (rb_)); \
-      if ((do_rd_) && g_ < 4 && j_ == 5)                                                      \
-        nx_[2 * (g_ & 3) + 1] = RD_X(2 * (g_ & 3) + 1, (rh_), (rb_));                         \
-      if ((do_rd_) && j_ == 7) fw[g_] = RD_W(g_, (rh_), (rb_));                               \
+      if ((do_rd_) && j_ == kJ / 4 && kPerGroup * g_ < kJ) {                                  \
+        const int x_ = kPerGroup * g_ < kJ ? kPerGroup * g_ : 0;                              \
+        nx_[x_] = RD_X(x_, (rh_), (rb_));                                                     \
+      }                                                                                       \
+      if ((do_rd_) && kPerGroup == 2 && j_ == kJ / 4 + 3 && 2 * g_ + 1 < kJ) {                \
+        const int x_ = 2 * g_ + 1 < kJ ? 2 * g_ + 1 : 0;                                      \
+        nx_[x_] = RD_X(x_, (rh_), (rb_));                                                     \
+      }                                                                                       \
+      if ((do_rd_) && j_ == kJ - 1) fw[g_] = RD_W(g_, (rh_), (rb_));                          \
       const int pu_ = (p0_) + u;                                                              \
-      if (pu_ % kSlotsPerCopy == 1 && pu_ / kSlotsPerCopy < 2 * kUnitCopies)                  \
-        COPY(pu_ / kSlotsPerCopy, wres, xres, off, b ^ 1);                                    \
+      if (pu_ % kEvery == 1 && pu_ / kEvery < kCopies)                                        \
+        COPY(pu_ / kEvery, wres, xres, off, b ^ 1);                                           \
       FENCE();                                                                                \
     }                                                                                         \
   } while (0)
@@ -465,23 +490,24 @@ __global__ __launch_bounds__(kTileThreads, 1) void tile_kernel(Int8Args a, int n
 #define STAGE(k_)                                                                             \
   __builtin_amdgcn_s_waitcnt(0x0070); /* vmcnt(0) lgkmcnt(0) */                               \
   __syncthreads();                                                                            \
-  uint32_t off = (uint32_t)((k_) + 1) * kInt8StageK;                                          \
-  if ((k_) + 1 == nk) {                                                                       \
-    at = tile_at(a, after < n_tiles ? after : tile, n_vt, n_tt, nk);                          \
-    off = 0u;                                                                                 \
+  int following = (k_) + 1;                                                                   \
+  if (following == nk) {                                                                      \
+    at = tile_at<kTokens>(a, after < n_tiles ? after : tile, n_vt, n_tt, nk);                 \
+    following = 0;                                                                            \
   }                                                                                           \
+  following += at.first;                                                                      \
+  const uint32_t off = (uint32_t)(following >= nk ? following - nk : following) * kInt8StageK; \
   const __amdgpu_buffer_rsrc_t wres = make_rsrc(at.w, at.w_bytes);                            \
   const __amdgpu_buffer_rsrc_t xres = make_rsrc(at.x, at.x_bytes);                            \
   FENCE()
 
-  constexpr int kHalf = kTiles * kTiles;
-  TileAt at = tile_at(a, blockIdx.x, n_vt, n_tt, nk);
+  TileAt at = tile_at<kTokens>(a, blockIdx.x, n_vt, n_tt, nk);
   int b = 0;
   {
     const __amdgpu_buffer_rsrc_t wres = make_rsrc(at.w, at.w_bytes);
     const __amdgpu_buffer_rsrc_t xres = make_rsrc(at.x, at.x_bytes);
 #pragma unroll
-    for (int c = 0; c < 2 * kUnitCopies; ++c) COPY(c, wres, xres, 0u, 0);
+    for (int c = 0; c < kCopies; ++c) COPY(c, wres, xres, (uint32_t)at.first * kInt8StageK, 0);
   }
   for (int tile = blockIdx.x; tile < n_tiles; tile += gridDim.x) {
     const int after = tile + (int)gridDim.x;
@@ -503,13 +529,13 @@ __global__ __launch_bounds__(kTileThreads, 1) void tile_kernel(Int8Args a, int n
     const int vb = v0 + wm * kInt8BlockV;
     int lane_e;
     asm volatile("v_mbcnt_lo_u32_b32 %0, -1, 0\n\tv_mbcnt_hi_u32_b32 %0, -1, %0" : "=v"(lane_e));
-    const int lg_e = lane_e >> 4, t_e = t0 + wn * 128 + (lane_e & 15);
+    const int lg_e = lane_e >> 4, t_e = t0 + wn * 16 * kJ + (lane_e & 15);
     const bool there = vb < a.V;
     RowScales scales = {};
-    float xs[kTiles];
+    float xs[kJ];
     if (there) scales = row_scales(a, vb, lg_e);
 #pragma unroll
-    for (int j = 0; j < kTiles; ++j) xs[j] = read_global(a.x_scale, min(t_e + 16 * j, a.T - 1));
+    for (int j = 0; j < kJ; ++j) xs[j] = read_global(a.x_scale, min(t_e + 16 * j, a.T - 1));
     {
       // (Slots behind a stage's copies.)
       const __amdgpu_buffer_rsrc_t wres = make_rsrc(at.w, at.w_bytes), xres = wres;
@@ -518,9 +544,9 @@ __global__ __launch_bounds__(kTileThreads, 1) void tile_kernel(Int8Args a, int n
     }
     b ^= 1;
     if (there) {
-      const Place place = place_of(Out(), a, vb, t0 + wn * 128, 128, lane_e);
+      const Place place = place_of(Out(), a, vb, t0 + wn * 16 * kJ, 16 * kJ, lane_e);
 #pragma unroll
-      for (int j = 0; j < kTiles; ++j) {
+      for (int j = 0; j < kJ; ++j) {
         __builtin_amdgcn_sched_barrier(0);
         int t = t_e + 16 * j;
         asm volatile("" : "+v"(t));
@@ -668,11 +694,13 @@ void stream(const Int8Args& a, hipStream_t s) {
   });
 }
 
+template <int kJ>
 void tiles(const Int8Args& a, hipStream_t s) {
-  const int n_vt = (a.V + kTileRows - 1) / kTileRows, n_tt = (a.T + kTileRows - 1) / kTileRows;
-  const dim3 grid((uint32_t)std::min<int64_t>((int64_t)n_vt * n_tt, kCus));
+  const int n_vt = (a.V + kTileRows - 1) / kTileRows, n_tt = (a.T + 32 * kJ - 1) / (32 * kJ);
+  const int places = kJ == 2 ? 2 * kCus : kCus;
+  const dim3 grid((uint32_t)std::min<int64_t>((int64_t)n_vt * n_tt, places));
   with_output(a, [&](auto out) {
-    tile_kernel<decltype(out)><<<grid, kTileThreads, 0, s>>>(a, n_vt, n_tt);
+    tile_kernel<kJ, decltype(out)><<<grid, kTileThreads, 0, s>>>(a, n_vt, n_tt);
   });
 }
 
@@ -705,10 +733,25 @@ hipError_t launch_int8(Int8Args a, hipStream_t stream_) {
     a.x = a.staged;
     a.ldx = row;
   }
+  // Up to 16 tokens by streams (over 151 936 tokens, 16 rows 120 us, by tiles 131),
+  // and more where their workgroups (one a CU) all run at once, as splitting K
+  // shortens what each has to do: streams and tiles, heads of 4 096 hidden elements,
+  // 64 rows over 32 003 tokens 38 and 42 us, 512 over 4 000 29 and 46, 1 000 over
+  // 1 000 30 and 50; and beyond, 100 rows over 32 003 64 and 48, 1 000 over 4 000 57
+  // and 49, 64 over 151 936 173 and 139. Tiles are as few as tokens by 256 make them,
+  // and as narrow as that leaves them: 320 rows over 151 936 by two of 160 239 us, of
+  // 256 270 us, by three of 128 295 us.
+  const int64_t streams = (a.V + kInt8BlockV - 1) / kInt8BlockV * ((a.T + 63) / 64);
+  const int64_t n_tt = (a.T + 255) / 256;
+  const int64_t width = ((a.T + n_tt - 1) / n_tt + 31) / 32;  // of a tile, by 32 tokens
   if (a.T <= 16) stream<1>(a, stream_);
-  else if (a.T <= 32) stream<2>(a, stream_);
-  else if (a.T <= 64) stream<4>(a, stream_);
-  else tiles(a, stream_);
+  else if (streams <= kCus && a.T <= 32) stream<2>(a, stream_);
+  else if (streams <= kCus) stream<4>(a, stream_);
+  else if (width <= 2) tiles<2>(a, stream_);
+  else if (width <= 4) tiles<4>(a, stream_);
+  else if (width <= 5) tiles<5>(a, stream_);
+  else if (width <= 6) tiles<6>(a, stream_);
+  else tiles<8>(a, stream_);
   if ((e = hipGetLastError()) != hipSuccess || a.out) return e;
   const dim3 grid((uint32_t)((a.T + kMergeTokens - 1) / kMergeTokens));
   if (a.bf16_logits) merge_kernel<RoundedScores><<<grid, 64 * kMergeWaves, 0, stream_>>>(a);
