@@ -67,16 +67,20 @@ def quantize_int8(x: torch.Tensor, *, out: torch.Tensor | None = None,
     r, h, _, ld, code = _rows("x", x, None)
     dev, h16 = x.device, (h + 15) // 16 * 16
     if out is None:
-        out = torch.empty((r, h16), dtype=torch.int8, device=dev)[:, :h]
-    elif not isinstance(out, torch.Tensor) or out.device != dev or tuple(out.shape) != (r, h):
-        raise ValueError(f"out must be [{r}, {h}] on x's device")
-    _, _, ldq = _aligned_codes("out", out)
-    end = out.storage_offset() + (r - 1) * ldq + h16 if r else 0
-    if out.untyped_storage().nbytes() < end:
-        raise ValueError("out needs room for whole 16-byte groups in its last row")
+        out, ldq = torch.empty((r, h16), dtype=torch.int8, device=dev), h16
+        if h != h16:
+            out = out[:, :h]
+    else:
+        if not isinstance(out, torch.Tensor) or out.device != dev or tuple(out.shape) != (r, h):
+            raise ValueError(f"out must be [{r}, {h}] on x's device")
+        _, _, ldq = _aligned_codes("out", out)
+        if out.untyped_storage().nbytes() < (out.storage_offset() + (r - 1) * ldq + h16 if r else 0):
+            raise ValueError("out needs room for whole 16-byte groups in its last row")
     if scale is None:
         scale = torch.empty(r, dtype=torch.float32, device=dev)
-    ps = _like("scale", scale, (r,), torch.float32, dev)
+        ps = scale.data_ptr()
+    else:
+        ps = _like("scale", scale, (r,), torch.float32, dev)
     count = _bad_rows(bad_rows, check, dev)
     _call(lib().lp_quantize_int8, dev,
           (x.data_ptr(), ld, code, r, h, out.data_ptr(), ldq, ps,
@@ -114,15 +118,17 @@ def logits_int8(x: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, w_scale
     """
     t, h, v, dev, ptrs = _operands(x, x_scale, w, w_scale)
     if out is None:
-        if dtype not in _DTYPES:
+        code, ld = _DTYPES.get(dtype), v
+        if code is None:
             raise ValueError(f"dtype must be float32, bfloat16 or float16, got {dtype}")
         out = torch.empty((t, v), dtype=dtype, device=dev)
-    elif not isinstance(out, torch.Tensor) or out.device != dev or tuple(out.shape) != (t, v):
-        raise ValueError(f"out must be [{t}, {v}] on x's device")
-    elif out.requires_grad:
-        raise ValueError("out must not require gradients")
-    _, _, _, ld, code = _rows("out", out, None)
-    torch.autograd.graph.increment_version(out)
+    else:
+        if not isinstance(out, torch.Tensor) or out.device != dev or tuple(out.shape) != (t, v):
+            raise ValueError(f"out must be [{t}, {v}] on x's device")
+        if out.requires_grad:
+            raise ValueError("out must not require gradients")
+        _, _, _, ld, code = _rows("out", out, None)
+        torch.autograd.graph.increment_version(out)
     L = lib()
     ws = _workspace(workspace, L.lp_logits_int8_workspace_bytes(t, h), dev)
     _call(L.lp_logits_int8, dev,
@@ -148,7 +154,9 @@ def score_int8(x: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, w_scale:
     pi = _like("ids", ids, (t,), torch.int64, dev)
     if out is None:
         out = torch.empty(t, dtype=torch.float32, device=dev)
-    po = _like("out", out, (t,), torch.float32, dev)
+        po = out.data_ptr()
+    else:
+        po = _like("out", out, (t,), torch.float32, dev)
     pl = None if lse is None else _like("lse", lse, (t,), torch.float32, dev)
     L = lib()
     ws = _workspace(workspace, L.lp_score_int8_workspace_bytes(t, h, vt), dev)
