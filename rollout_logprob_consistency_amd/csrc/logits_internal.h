@@ -302,13 +302,17 @@ struct SelectArgs {
 struct SelectWorkspace {
   size_t off_counts, off_parts, off_keys, off_masses, off_bucket_counts, off_facts, total;
 };
-SelectWorkspace select_workspace_layout(int64_t N, int64_t V, int32_t dtype);
+// Rows are cut where there are few: into `places` slices at most, over all rows.
+constexpr int64_t kSelectPlaces = 512;  // see select.hip
+SelectWorkspace select_workspace_layout(int64_t N, int64_t V, int32_t dtype,
+                                        int64_t places = kSelectPlaces);
 // Bytes that serve every number of rows up to N (fewer rows are cut into more
 // slices, so one layout may be larger than that of more rows).
-size_t select_workspace_most(int64_t N, int64_t V, int32_t dtype);
+size_t select_workspace_most(int64_t N, int64_t V, int32_t dtype,
+                             int64_t places = kSelectPlaces);
 
 // Sets the slices and the workspace's parts.
-void place_select(SelectArgs& a, void* workspace);
+void place_select(SelectArgs& a, void* workspace, int64_t places);
 // Which ways the draw's rows can take, as far as the host sees the settings.
 struct SelectWays {
   bool lists, buckets;
@@ -330,7 +334,7 @@ struct VerifyArgs {
   float* out_processed;     // [seqs, drafts + 1] or null
   int32_t* bad_rows;        // or null
   // Set by launch_verify.
-  double* chunk_sums;       // [seqs][chunks]
+  double* sums;             // [seqs][stretches] of the last token's weights
   int32_t* verdicts;        // [seqs] what out_accepted gets
 };
 

@@ -51,15 +51,13 @@ hipError_t launch(const SelectArgs& a, bool lists, bool buckets, hipStream_t str
 // rows 40, 40, 42 and 44, 400 rows 42, 41, 42 and 51; draws over rows of 151 936, 64
 // bf16 rows by top-k 20 30, 30, 27 and 27, 300 rows 55, 55, 52 and 53, 512 rows 61, 61,
 // 61 and 73; 64 fp32 rows by nucleus 93, 96, 97 and 103.
-constexpr int64_t kSelectPlaces = 512;
-static_assert(kSelectPlaces <= kMaxSlices, "slices of one row");
+static_assert(LP_SELECT_MAX_VOCAB / chunk_of<F32>() <= kMaxSlices, "slices of one row");
 static int64_t select_chunks(int64_t V, int32_t dtype) {
   const int64_t chunk = (int64_t)kThreads * kGroups * (16 / dtype_bytes(dtype));
   return (V + chunk - 1) / chunk;
 }
-static int64_t select_slices(int64_t N, int64_t V, int32_t dtype) {
-  return std::max<int64_t>(
-      1, std::min(select_chunks(V, dtype), kSelectPlaces / std::max<int64_t>(N, 1)));
+static int64_t select_slices(int64_t N, int64_t V, int32_t dtype, int64_t places) {
+  return std::max<int64_t>(1, std::min(select_chunks(V, dtype), places / std::max<int64_t>(N, 1)));
 }
 
 // A count per row or slice; parts of `cut_rows` rows and the rest of `cut_slices`
@@ -77,26 +75,26 @@ static SelectWorkspace layout_of(size_t counts, size_t cut_rows, size_t cut_slic
   return w;
 }
 
-SelectWorkspace select_workspace_layout(int64_t N, int64_t V, int32_t dtype) {
-  const int64_t slices = select_slices(N, V, dtype);
+SelectWorkspace select_workspace_layout(int64_t N, int64_t V, int32_t dtype, int64_t places) {
+  const int64_t slices = select_slices(N, V, dtype, places);
   const size_t all = (size_t)(N * slices);
   return layout_of(all, slices > 1 ? (size_t)N : 0, slices > 1 ? all : 0, select_chunks(V, dtype));
 }
 
-size_t select_workspace_most(int64_t N, int64_t V, int32_t dtype) {
+size_t select_workspace_most(int64_t N, int64_t V, int32_t dtype, int64_t places) {
   // Every term of layout_of at its largest over 1 .. N rows.
   const int64_t chunks = select_chunks(V, dtype);
-  const int64_t cut_rows = chunks > 1 ? std::min(N, kSelectPlaces / 2) : 0;
-  const int64_t cut_slices = std::min(kSelectPlaces, cut_rows * chunks);
+  const int64_t cut_rows = chunks > 1 ? std::min(N, places / 2) : 0;
+  const int64_t cut_slices = std::min(places, cut_rows * chunks);
   return layout_of((size_t)std::max(N, cut_slices), (size_t)cut_rows, (size_t)cut_slices,
                    (size_t)chunks)
       .total;
 }
 
-void place_select(SelectArgs& a, void* workspace) {
-  const SelectWorkspace w = select_workspace_layout(a.N, a.V, a.dtype);
+void place_select(SelectArgs& a, void* workspace, int64_t places) {
+  const SelectWorkspace w = select_workspace_layout(a.N, a.V, a.dtype, places);
   char* base = static_cast<char*>(workspace);
-  a.slices = (int32_t)select_slices(a.N, a.V, a.dtype);
+  a.slices = (int32_t)select_slices(a.N, a.V, a.dtype, places);
   a.counts = reinterpret_cast<uint32_t*>(base + w.off_counts);
   a.parts = reinterpret_cast<SelectPart*>(base + w.off_parts);
   a.keys = reinterpret_cast<uint64_t*>(base + w.off_keys);
@@ -113,7 +111,7 @@ SelectWays select_ways(const SelectArgs& a) {
 }
 
 hipError_t launch_select(SelectArgs a, void* workspace, hipStream_t stream) {
-  place_select(a, workspace);
+  place_select(a, workspace, kSelectPlaces);
   const bool top = a.u == nullptr;
   const SelectWays ways = select_ways(a);
   const bool lists = top ? a.top_k <= kShortTop : ways.lists, buckets = !top && ways.buckets;

@@ -731,6 +731,7 @@ struct CollectShared {
   Part parts[kMaxParts];
   double wave_f64[kWaves], shared_f64;
   float wave_f32[kWaves];
+  uint32_t wave_u32[kWaves];  // kLimit
   uint32_t n_list, found;
   RowFacts facts;
 };
@@ -878,33 +879,58 @@ __device__ __forceinline__ bool is_whole(const Settings& s) {
   return s.kind == kWhole || s.kind == kWholeMinP;
 }
 
-// Workgroup `block` of whole_blocks: an equal share of all rows' chunks, whatever
-// rows they belong to, the next one's loads in flight. Lane i looks up the
-// settings of the share's i-th row.
+// Workgroup `block` of whole_blocks: an equal share of those rows' chunks, whatever
+// rows they belong to, the next one's loads in flight. Every workgroup lists the
+// rows for itself (up to as many as `list` holds; more are taken as they come, the
+// others among them). Lane i looks up the settings of the share's i-th row.
 template <class D>
-__device__ __forceinline__ void whole_rows(const SelectArgs& a, int block) {
+__device__ __forceinline__ void whole_rows(const SelectArgs& a, int block, CollectShared& sh) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int chunks = (a.V + chunk_of<D>() - 1) / chunk_of<D>();
-  const int64_t items = a.N * chunks;
+  uint32_t* list = reinterpret_cast<uint32_t*>(sh.list);
+  constexpr int64_t kMost = 2 * kShort;  // of half a key's size
+  const bool listed = a.N <= kMost;
+  int64_t rows = a.N;
+  if (listed) {
+    constexpr int kEach = kMost / kThreads;
+    const int each = ((int)a.N + kThreads - 1) / kThreads, base = (int)threadIdx.x * each;
+    uint32_t mine = 0, count = 0;
+    for (int i = 0; i < each; ++i)
+      if (base + i < a.N && !skipped<kLimit>(a, base + i) &&
+          is_whole(settings_of<kLimit>(a, base + i)))
+        mine |= 1u << i;
+    static_assert(kEach <= 32, "a bit for each of a thread's rows");
+    uint32_t at = block_scan((uint32_t)__popc(mine), sh.wave_u32, &count);
+    for (int i = 0; i < each; ++i)
+      if (mine >> i & 1) list[at++] = (uint32_t)(base + i);
+    rows = count;
+    __syncthreads();
+  }
+  const int64_t items = rows * chunks;
   const int64_t lo = items * block / a.whole_blocks, hi = items * (block + 1) / a.whole_blocks;
   for (int64_t r0 = lo / chunks; r0 * chunks < hi; r0 += 64) {
-    bool mine = (r0 + lane) * chunks < hi && !skipped<kLimit>(a, r0 + lane);
+    bool mine = (r0 + lane) * chunks < hi;
     double scale = 0.0;
     bool min_p = false;
+    int row_of = 0;
     if (mine) {
-      const Settings st = settings_of<kLimit>(a, r0 + lane);
-      mine = is_whole(st);
-      min_p = st.kind == kWholeMinP;
-      scale = kLog2E / (double)st.tau;
+      row_of = listed ? (int)list[r0 + lane] : (int)(r0 + lane);
+      mine = listed || !skipped<kLimit>(a, row_of);
+      if (mine) {
+        const Settings st = settings_of<kLimit>(a, row_of);
+        mine = is_whole(st);
+        min_p = st.kind == kWholeMinP;
+        scale = kLog2E / (double)st.tau;
+      }
     }
     const uint64_t min_ps = __ballot(min_p);
-    for (uint64_t rows = __ballot(mine); rows; rows &= rows - 1) {
-      const int i = __ffsll((long long)rows) - 1;
-      const int64_t n = r0 + i;
+    for (uint64_t rest = __ballot(mine); rest; rest &= rest - 1) {
+      const int i = __ffsll((long long)rest) - 1;
+      const int64_t n = lane_value(row_of, i);
       const double c = lane_value(scale, i);
       const Row<D> row = row_at<D, kLimit>(a, n);
-      const int c0 = (int)max(lo - n * chunks, (int64_t)0);
-      const int c1 = (int)min(hi - n * chunks, (int64_t)chunks);
+      const int c0 = (int)max(lo - (r0 + i) * chunks, (int64_t)0);
+      const int c1 = (int)min(hi - (r0 + i) * chunks, (int64_t)chunks);
       SelectPart* parts = a.whole + n * chunks * kWaves + wave;
       Groups<D> v, next;
       row.load(v.g, c0);
@@ -929,7 +955,7 @@ __global__ __launch_bounds__(kThreads, 6) void collect_kernel(SelectArgs a) {
   uint32_t block = blockIdx.x;
   if constexpr (kJob == kLimit) {
     if (block < (uint32_t)a.whole_blocks) {
-      whole_rows<D>(a, (int)block);
+      whole_rows<D>(a, (int)block, sh);
       return;
     }
     block -= (uint32_t)a.whole_blocks;

@@ -10,9 +10,10 @@
 // the draw's own kernels. Two more launches end the call: residual_kernel judges
 // the drafts (each workgroup for itself: a few loads, against a launch more) and
 // sums the weights of the one row, or two, that a sequence's last token is drawn
-// from by chunks; final_kernel finds the chunk and the token in it. (One launch
-// whose last workgroup of a sequence ends it took longer: 147 us against 91 us for
-// 128 sequences of 151 936, as the fences that it needs empty the L2 caches.)
+// from, by stretches of a wave's width; final_kernel finds the stretch and the
+// token in it. (One launch whose last workgroup of a sequence ends it took longer:
+// 147 us against 91 us for 128 sequences of 151 936, as the fences that it needs
+// empty the L2 caches.)
 #include <algorithm>
 
 #include "select_row.h"
@@ -22,11 +23,22 @@ namespace {
 
 constexpr int kVerifyThreads = 256;
 constexpr int kVerifyWaves = kVerifyThreads / 64;
-constexpr int kVerifyChunk = 4096;  // tokens summed at once
-constexpr int kEach = kVerifyChunk / kVerifyThreads;
+// Tokens of a stretch: one group a lane.
+template <class D>
+constexpr int kStretch = 64 * D::kVec;
+constexpr int kMostStretches = LP_SELECT_MAX_VOCAB / kStretch<F32>;
+constexpr int kSumsPerThread = kMostStretches / kVerifyThreads;
+int64_t stretches_of(int64_t V, int32_t dtype) {
+  const int64_t n = 64 * (16 / dtype_bytes(dtype));
+  return (V + n - 1) / n;
+}
 // Workgroups that run at once: of residual_kernel six on each of 256 CUs, of
 // collect_kernel three.
 constexpr int64_t kVerifyPlaces = 1536;
+// Slices of all rows. More of them shorten the longest row's way (64 sequences of 4
+// drafts, settings of their own: 239 us with the draw's 512) until joining them
+// takes longer (190 us with 640, 183 with 1 280, 190 with 2 560).
+constexpr int64_t kLimitPlaces = 1280;
 constexpr int64_t kWholePlaces = 768;
 static_assert(LP_VERIFY_MAX_DRAFTS < 64, "a wave holds a sequence's positions");
 
@@ -146,45 +158,65 @@ struct Weights {
       gone = read_global(a.draft_ids, d);  // the draft's whole probability
     }
   }
-  // The weights of the tokens from v on, kVec of them; 0 behind the row. A wave
-  // whose tokens are all below the last kept one forms no exponentials.
-  __device__ __forceinline__ void group(int v, double (&w)[D::kVec]) const {
-    const Group<D> z = load_group<D>(target, v, V);
-    Group<D> y = z;
-    if (draft) y = load_group<D>(draft, v, V);
+  // A lane's logits of a stretch, and their weights; 0 behind the row. A wave whose
+  // tokens are all below the last kept one forms no exponentials.
+  struct Loaded {
+    Group<D> z, y;
+    int v;
+  };
+  __device__ __forceinline__ Loaded load(int stretch) const {
+    Loaded l;
+    l.v = stretch * kStretch<D> + (int)(threadIdx.x & 63) * D::kVec;
+    l.z = load_group<D>(target, l.v, V);
+    l.y = l.z;
+    if (draft) l.y = load_group<D>(draft, l.v, V);
+    return l;
+  }
+  __device__ __forceinline__ void weigh(const Loaded& l, double (&w)[D::kVec]) const {
 #pragma unroll
     for (int i = 0; i < D::kVec; ++i) {
-      const float a = z.get(i), b = y.get(i);
+      const float a = l.z.get(i), b = l.y.get(i);  // (-inf behind the row)
       w[i] = 0.0;
       if (__ballot(p.near(a)) == 0) continue;
-      const bool kept = p.keeps(a, v + i) && v + i != gone;
+      const bool kept = p.keeps(a, l.v + i) && l.v + i != gone;
       w[i] = kept ? p.prob(a) : 0.0;
       if (!draft || __ballot(kept && q.near(b)) == 0) continue;
-      w[i] = kept && q.keeps(b, v + i) ? fmax(w[i] - q.prob(b), 0.0) : w[i];
+      w[i] = kept && q.keeps(b, l.v + i) ? fmax(w[i] - q.prob(b), 0.0) : w[i];
+    }
+  }
+  __device__ __forceinline__ double sum(const Loaded& l) const {
+    double x[D::kVec], s = 0.0;
+    weigh(l, x);
+#pragma unroll
+    for (int i = 0; i < D::kVec; ++i) s += x[i];
+    return wave_sum(s);
+  }
+  // The sums of the stretches first, first + step, ..., the next one's logits in
+  // flight.
+  __device__ __forceinline__ void sums(int first, int step, double* out) const {
+    const int n = (V + kStretch<D> - 1) / kStretch<D>;
+    if (first >= n) return;
+    Loaded now = load(first);
+    for (int i = first; i < n; i += step) {
+      Loaded next = now;
+      if (i + step < n) next = load(i + step);
+      const double s = sum(now);
+      if ((threadIdx.x & 63) == 0) out[i] = s;
+      now = next;
     }
   }
 };
 
-// The sum of a chunk's weights, every thread's groups in order, then the threads.
 template <class D>
-__device__ __forceinline__ double chunk_sum(const Weights<D>& w, int chunk, double* words) {
-  double s = 0.0;
-#pragma unroll
-  for (int j = 0; j < kEach / D::kVec; ++j) {
-    const int v = chunk * kVerifyChunk + (j * kVerifyThreads + (int)threadIdx.x) * D::kVec;
-    double x[D::kVec];
-    w.group(v, x);
-#pragma unroll
-    for (int i = 0; i < D::kVec; ++i) s += x[i];
-  }
-  s = wave_sum(s);
-  if ((threadIdx.x & 63) == 0) words[threadIdx.x >> 6] = s;
-  __syncthreads();
-  s = words[0];
-#pragma unroll
-  for (int i = 1; i < kVerifyWaves; ++i) s += words[i];
-  __syncthreads();
-  return s;
+__global__ __launch_bounds__(kVerifyThreads) void residual_kernel(VerifyArgs a, int parts) {
+  const int64_t b = blockIdx.x / (uint32_t)parts;
+  const int part = (int)(blockIdx.x % (uint32_t)parts);
+  const Sequence s = judge<D>(a, b);
+  if (part == 0 && threadIdx.x == 0) a.verdicts[b] = s.accepted;
+  if (s.accepted < 0) return;
+  const int64_t n = (a.rows.V + kStretch<D> - 1) / kStretch<D>;
+  Weights<D>(a, s, false)
+      .sums(part * kVerifyWaves + (threadIdx.x >> 6), parts * kVerifyWaves, a.sums + b * n);
 }
 
 // Exclusive prefix sum over the workgroup.
@@ -212,87 +244,98 @@ __device__ __forceinline__ double scan(double v, double* words, double* total) {
 }
 
 struct FinalShared {
-  double words[kVerifyWaves], sums[LP_SELECT_MAX_VOCAB / kVerifyChunk];
-  double before;
-  int chunk, token, last;
+  double words[kVerifyWaves], before;
+  int stretch, last, token;
 };
 
-// The least token through which the chunks' weights pass u times their sum; -1
-// where all weigh nothing. Where rounding leaves none, the last that weighs.
+// The least token through which the weights pass u times their sum, from the
+// stretches' sums; -1 where all weigh nothing. Where rounding leaves none, the last
+// that weighs.
 template <class D>
-__device__ __forceinline__ int draw(const Weights<D>& w, double u, int chunks, FinalShared& sh) {
-  constexpr int kMost = LP_SELECT_MAX_VOCAB / kVerifyChunk;
-  static_assert(kMost <= kVerifyThreads, "a chunk for each thread");
-  const int tid = threadIdx.x;
-  const double mine = tid < chunks ? sh.sums[tid] : 0.0;
-  double total;
-  const double before = scan(mine, sh.words, &total);
+__device__ __forceinline__ int draw(const Weights<D>& w, double u, const double* sums,
+                                    FinalShared& sh) {
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int n = (w.V + kStretch<D> - 1) / kStretch<D>;
+  const int each = (n + kVerifyThreads - 1) / kVerifyThreads;
+  double mine[kSumsPerThread], sum = 0.0, total;
+  int last = -1;
+#pragma unroll
+  for (int i = 0; i < kSumsPerThread; ++i) {
+    mine[i] = i < each && tid * each + i < n ? sums[tid * each + i] : 0.0;
+    sum += mine[i];
+    last = mine[i] > 0.0 ? tid * each + i : last;
+  }
+  if (tid == 0) {
+    sh.stretch = INT32_MAX;
+    sh.last = -1;
+  }
+  double before = scan(sum, sh.words, &total);
   if (!(total > 0.0)) return -1;
   const double want = u * total;
-  if (tid == 0) {
-    sh.chunk = kMost;
-    sh.last = -1;
-    sh.token = INT32_MAX;
+  int first = INT32_MAX;
+  double at = before;
+#pragma unroll
+  for (int i = 0; i < kSumsPerThread; ++i) {
+    if (first == INT32_MAX && mine[i] > 0.0 && before + mine[i] > want) {
+      first = tid * each + i;
+      at = before;
+    }
+    before += mine[i];
   }
+  if (first != INT32_MAX) atomicMin(&sh.stretch, first);
+  if (last >= 0) atomicMax(&sh.last, last);
   __syncthreads();
-  if (mine > 0.0) {
-    atomicMax(&sh.last, tid);
-    if (before + mine > want) atomicMin(&sh.chunk, tid);
-  }
+  const int stretch = sh.stretch != INT32_MAX ? sh.stretch : sh.last;
+  if (first == stretch) sh.before = at;
+  else if (sh.stretch == INT32_MAX && tid == 0) sh.before = total;  // rounding: its last token
   __syncthreads();
-  const int chunk = sh.chunk < kMost ? sh.chunk : sh.last;
-  if (tid == chunk) sh.before = before;
-  __syncthreads();
-  if (tid == 0) sh.last = -1;
-  __syncthreads();
-  double base = sh.before;
+  if (tid < 64) {
+    double x[D::kVec], s = 0.0;
+    const auto l = w.load(stretch);
+    w.weigh(l, x);
 #pragma unroll
-  for (int j = 0; j < kEach / D::kVec; ++j) {
-    const int v = chunk * kVerifyChunk + (j * kVerifyThreads + tid) * D::kVec;
-    double x[D::kVec], sum = 0.0;
-    w.group(v, x);
+    for (int i = 0; i < D::kVec; ++i) s += x[i];
+    double c = s;
 #pragma unroll
-    for (int i = 0; i < D::kVec; ++i) sum += x[i];
-    double all;
-    double c = base + scan(sum, sh.words, &all);
-    base += all;
-#pragma unroll
-    for (int i = D::kVec - 1; i >= 0; --i)
-      if (x[i] > 0.0) {
-        atomicMax(&sh.last, v + i);
-        break;
-      }
+    for (int d = 1; d < 64; d <<= 1) {
+      const double o = __shfl_up(c, d);
+      if (lane >= d) c += o;
+    }
+    c += sh.before - s;
+    int hit = -1, some = -1;
 #pragma unroll
     for (int i = 0; i < D::kVec; ++i) {
       c += x[i];
-      if (x[i] > 0.0 && c > want) {
-        atomicMin(&sh.token, v + i);
-        break;
+      if (x[i] > 0.0) {
+        some = l.v + i;
+        if (hit < 0 && c > want) hit = l.v + i;
       }
     }
+    const uint64_t hits = __ballot(hit >= 0), any = __ballot(some >= 0);
+    const int token = hits ? __shfl(hit, __ffsll((long long)hits) - 1)
+                           : __shfl(some, any ? 63 - __clzll((long long)any) : 0);
+    if (lane == 0) sh.token = token;
   }
   __syncthreads();
-  return sh.token != INT32_MAX ? sh.token : sh.last;
+  return sh.token;
 }
 
-// A sequence's outputs, its chunks' sums in LDS.
+// A sequence's outputs.
 template <class D>
-__device__ __forceinline__ void finish(const VerifyArgs& a, const Sequence& s, int chunks,
-                                       FinalShared& sh) {
+__device__ __forceinline__ void finish(const VerifyArgs& a, const Sequence& s, FinalShared& sh) {
   const SelectArgs& r = a.rows;
   const int tid = threadIdx.x, width = r.drafts + 1;
   const double u =
       fmin(fmax((double)read_global(a.u, s.b * width + r.drafts), 0.0), 1.0 - 0x1p-24);
-  int token = draw(Weights<D>(a, s, false), u, chunks, sh);
+  double* sums = a.sums + s.b * ((r.V + kStretch<D> - 1) / kStretch<D>);
+  int token = draw(Weights<D>(a, s, false), u, sums, sh);
   if (token < 0) {
     // The target has nothing beyond the draft: a token of the target's own.
     const Weights<D> w(a, s, true);
-    for (int c = 0; c < chunks; ++c) {
-      const double sum = chunk_sum(w, c, sh.words);
-      if (tid == 0) sh.sums[c] = sum;
-    }
     __syncthreads();
-    token = draw(w, u, chunks, sh);
+    w.sums(tid >> 6, kVerifyWaves, sums);
+    __syncthreads();
+    token = draw(w, u, sums, sh);
   }
   if (tid < width) {
     float logprob = 0.0f, processed = 0.0f;
@@ -314,28 +357,11 @@ __device__ __forceinline__ void finish(const VerifyArgs& a, const Sequence& s, i
 }
 
 template <class D>
-__global__ __launch_bounds__(kVerifyThreads) void residual_kernel(VerifyArgs a, int parts) {
-  __shared__ double words[kVerifyWaves];
-  const int64_t b = blockIdx.x / (uint32_t)parts;
-  const int part = (int)(blockIdx.x % (uint32_t)parts);
-  const Sequence s = judge<D>(a, b);
-  if (part == 0 && threadIdx.x == 0) a.verdicts[b] = s.accepted;
-  if (s.accepted < 0) return;
-  const int chunks = (a.rows.V + kVerifyChunk - 1) / kVerifyChunk;
-  const Weights<D> w(a, s, false);
-  for (int c = part; c < chunks; c += parts) {
-    const double sum = chunk_sum(w, c, words);
-    if (threadIdx.x == 0) a.chunk_sums[b * chunks + c] = sum;
-  }
-}
-
-template <class D>
 __global__ __launch_bounds__(kVerifyThreads) void final_kernel(VerifyArgs a) {
   __shared__ FinalShared sh;
   const SelectArgs& r = a.rows;
   const int64_t b = blockIdx.x;
   const int tid = threadIdx.x, width = r.drafts + 1;
-  const int chunks = (r.V + kVerifyChunk - 1) / kVerifyChunk;
   const int accepted = read_global(a.verdicts, b);
   if (accepted < 0) {
     if (tid < width) {
@@ -351,9 +377,7 @@ __global__ __launch_bounds__(kVerifyThreads) void final_kernel(VerifyArgs a) {
   }
   Sequence s = sequence_of(a, b);
   s.accepted = accepted;
-  if (tid < chunks) sh.sums[tid] = read_global(a.chunk_sums, b * chunks + tid);
-  __syncthreads();
-  finish<D>(a, s, chunks, sh);
+  finish<D>(a, s, sh);
 }
 
 template <class D>
@@ -365,9 +389,10 @@ hipError_t launch(const VerifyArgs& a, hipStream_t stream) {
   if ((e = hipGetLastError()) != hipSuccess) return e;
   row_kernel<D, kLimit><<<dim3((uint32_t)r.N), kThreads, 0, stream>>>(r);
   if ((e = hipGetLastError()) != hipSuccess) return e;
-  const int64_t chunks = (r.V + kVerifyChunk - 1) / kVerifyChunk;
-  const int64_t each = (chunks * r.seqs + kVerifyPlaces - 1) / kVerifyPlaces;
-  const int64_t parts = (chunks + each - 1) / each;
+  // Four stretches at a time; as many turns for every workgroup as for the others.
+  const int64_t turns = (stretches_of(r.V, r.dtype) + kVerifyWaves - 1) / kVerifyWaves;
+  const int64_t each = (turns * r.seqs + kVerifyPlaces - 1) / kVerifyPlaces;
+  const int64_t parts = (turns + each - 1) / each;
   residual_kernel<D><<<dim3((uint32_t)(r.seqs * parts)), kVerifyThreads, 0, stream>>>(a,
                                                                                     (int)parts);
   if ((e = hipGetLastError()) != hipSuccess) return e;
@@ -389,11 +414,11 @@ VerifyWorkspace verify_workspace_layout(int64_t seqs, int64_t drafts, int64_t V,
   const int64_t rows = seqs * (2 * drafts + 1);
   VerifyWorkspace w;
   w.off_select = 0;
-  w.off_limits = up(select_workspace_most(rows, V, dtype));
+  w.off_limits = up(select_workspace_most(rows, V, dtype, kLimitPlaces));
   w.off_whole = w.off_limits + up((size_t)rows * sizeof(SelectLimit));
   w.off_sums = w.off_whole + up((size_t)(rows * row_chunks(V, dtype) * kWaves) * sizeof(Part));
-  w.off_verdicts = w.off_sums + up((size_t)seqs * (size_t)((V + kVerifyChunk - 1) / kVerifyChunk) *
-                               sizeof(double));
+  w.off_verdicts =
+      w.off_sums + up((size_t)(seqs * stretches_of(V, dtype)) * sizeof(double));
   w.total = w.off_verdicts + up((size_t)seqs * sizeof(int32_t));
   return w;
 }
@@ -406,8 +431,8 @@ hipError_t launch_verify(VerifyArgs a, void* workspace, hipStream_t stream) {
   r.limits = reinterpret_cast<SelectLimit*>(base + w.off_limits);
   r.whole = reinterpret_cast<SelectPart*>(base + w.off_whole);
   a.verdicts = reinterpret_cast<int32_t*>(base + w.off_verdicts);
-  a.chunk_sums = reinterpret_cast<double*>(base + w.off_sums);
-  place_select(r, base + w.off_select);
+  a.sums = reinterpret_cast<double*>(base + w.off_sums);
+  place_select(r, base + w.off_select, kLimitPlaces);
   r.whole_blocks = (int32_t)std::min(kWholePlaces, r.N * row_chunks(r.V, r.dtype));
   switch (r.dtype) {
     case LP_F32: return launch<F32>(a, stream);
