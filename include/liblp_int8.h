@@ -108,7 +108,9 @@ lp_status lp_logits_int8(const int8_t* x, int64_t ldx, const float* x_scale,
  *
  * Precision: exponentials and sums are fp32, per 128 vocabulary rows and
  * joined in a fixed order; as lp_score, within about 1e-5 nats at logits of
- * ordinary size.
+ * ordinary size. Logits in fp32 are taken as (S w_scale) x_scale here, so
+ * |S w_scale| has to stay below fp32's largest number and
+ * w_scale above its smallest normal one.
  *
  * Layout and errors as for lp_logits_int8, target_ids [T] int64, out_logprob
  * and out_lse [T] fp32; LP_EINVAL for a temperature that is not positive and

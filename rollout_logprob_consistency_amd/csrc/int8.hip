@@ -209,9 +209,13 @@ __device__ __forceinline__ void store_partial(const Int8Args& a, const float (&y
                                         0, 0);
 }
 
-__device__ __forceinline__ void mask_tail(const Int8Args& a, float (&y)[kPerLane], float f, int v0,
+// Rows behind the vocabulary get weight 0. Where the token's scale is 0, its factor
+// becomes the smallest one: 0 times infinity would be NaN, and |y| 2^-149 stays
+// below 2^-21.
+__device__ __forceinline__ void mask_tail(const Int8Args& a, float (&y)[kPerLane], float& f, int v0,
                                           int lg) {
   if (v0 + kInt8BlockV <= a.V) return;
+  f = f == 0.0f ? 0x1p-149f : f;
   const float none = f < 0.0f ? INFINITY : -INFINITY;
   int left = a.V - v0 - 8 * lg;
   asm volatile("" : "+v"(left));  // (or all tokens' comparisons are made, and kept, at once)
@@ -234,7 +238,7 @@ template <class Out>
 __device__ __forceinline__ void finish_block(Out out, const Int8Args& a, const Place&, int,
                                              const int (&sums)[kPerLane], const RowScales& w,
                                              int v0, int t, float xs, int lg) {
-  const float f = factor_of(out, xs, a.scale2);
+  float f = factor_of(out, xs, a.scale2);
   float y[kPerLane];
 #pragma unroll
   for (int k = 0; k < kPerLane; ++k) y[k] = score_of(out, sums[k], xs, w.s[k]);

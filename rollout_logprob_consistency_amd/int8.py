@@ -76,11 +76,13 @@ def quantize_int8(x: torch.Tensor, *, out: torch.Tensor | None = None,
         _, _, ldq = _aligned_codes("out", out)
         if out.untyped_storage().nbytes() < (out.storage_offset() + (r - 1) * ldq + h16 if r else 0):
             raise ValueError("out needs room for whole 16-byte groups in its last row")
+        torch.autograd.graph.increment_version(out)
     if scale is None:
         scale = torch.empty(r, dtype=torch.float32, device=dev)
         ps = scale.data_ptr()
     else:
         ps = _like("scale", scale, (r,), torch.float32, dev)
+        torch.autograd.graph.increment_version(scale)
     count = _bad_rows(bad_rows, check, dev)
     _call(lib().lp_quantize_int8, dev,
           (x.data_ptr(), ld, code, r, h, out.data_ptr(), ldq, ps,
@@ -157,6 +159,7 @@ def score_int8(x: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, w_scale:
         po = out.data_ptr()
     else:
         po = _like("out", out, (t,), torch.float32, dev)
+        torch.autograd.graph.increment_version(out)
     pl = None if lse is None else _like("lse", lse, (t,), torch.float32, dev)
     L = lib()
     ws = _workspace(workspace, L.lp_score_int8_workspace_bytes(t, h, vt), dev)

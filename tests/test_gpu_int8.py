@@ -128,6 +128,12 @@ def codes(rng, rows, h, pad=0, lead=0, low=-127):
 SIZES = [(1, 1, 1), (1, 128, 64), (2, 127, 129), (3, 257, 33), (16, 300, 256), (17, 129, 100),
          (31, 515, 1001), (33, 1000, 384), (64, 640, 128), (65, 700, 130), (100, 1025, 640),
          (129, 384, 17), (257, 513, 256), (300, 2049, 72), (513, 1300, 200)]
+# More work than the CUs take at once by streams: tiles of 64, 128, 160, 192 and 256
+# tokens, one, two and three of them, rows of one stage and more, ends inside a tile
+# and a block.
+SIZES += [(17, 33000, 33), (64, 32897, 200), (100, 17000, 129), (150, 11100, 128),
+          (190, 11009, 300), (200, 8300, 16), (256, 8321, 257), (300, 6600, 385),
+          (384, 6001, 100), (513, 4000, 520), (700, 3001, 72), (2000, 1152, 500)]
 
 
 @pytest.mark.parametrize("dtype", list(TYPES))
@@ -143,7 +149,8 @@ def test_logits_bit_for_bit(dtype, t, v, h):
 
 
 @pytest.mark.parametrize("pad,lead", [(0, 1), (1, 0), (5, 3), (16, 16), (112, 0)])
-@pytest.mark.parametrize("t,v,h", [(5, 300, 128), (40, 260, 256), (150, 400, 300), (300, 300, 512)])
+@pytest.mark.parametrize("t,v,h", [(5, 300, 128), (40, 260, 256), (150, 400, 300), (300, 300, 512),
+                                   (50, 33000, 128), (140, 11111, 200)])
 def test_hidden_states_lie_anywhere(t, v, h, pad, lead):
     rng = np.random.default_rng(7)
     x, xs, qx, sx = codes(rng, t, h, pad, lead)
@@ -152,22 +159,39 @@ def test_hidden_states_lie_anywhere(t, v, h, pad, lead):
     assert np.array_equal(lp.logits_int8(x, xs, w, ws, dtype=torch.float32).cpu().numpy(), want)
 
 
-@pytest.mark.parametrize("t", [3, 40, 200])
+@pytest.mark.parametrize("t,v", [(3, 333), (40, 333), (200, 333), (70, 17005), (135, 11205),
+                                 (180, 11205), (520, 4101)])
 @pytest.mark.parametrize("dtype", list(TYPES))
-def test_logits_into_a_wider_buffer(t, dtype):
+def test_logits_into_a_wider_buffer(t, v, dtype):
     """Rows of any stride and alignment; the columns around them stay."""
     rng = np.random.default_rng(t)
     x, xs, qx, sx = codes(rng, t, 96)
-    w, ws, qw, sw = codes(rng, 333, 96)
+    w, ws, qw, sw = codes(rng, v, 96)
     want = torch.from_numpy(oracle.logits_f32(qx, sx, qw, sw)).to(TYPES[dtype])
-    for columns, lead in ((333, 0), (340, 0), (351, 1), (384, 5)):
+    for columns, lead in ((v, 0), (v + 7, 0), (v + 18, 1), (v + 51, 5)):
         buf = torch.full((lead + t * columns + 64,), -7.0, dtype=TYPES[dtype], device=DEV)
         rows = buf[lead:lead + t * columns].view(t, columns)
-        got = lp.logits_int8(x, xs, w, ws, out=rows[:, :333])
+        got = lp.logits_int8(x, xs, w, ws, out=rows[:, :v])
         assert got.data_ptr() == rows.data_ptr()
-        assert same_bits(rows[:, :333].cpu(), want)
-        assert (rows[:, 333:] == -7).all() and (buf[:lead] == -7).all()
+        assert same_bits(rows[:, :v].cpu(), want)
+        assert (rows[:, v:] == -7).all() and (buf[:lead] == -7).all()
         assert (buf[lead + t * columns:] == -7).all()
+
+
+def test_the_widest_rows():
+    """Rows 2^22 fp32 columns apart: a wave's 128 tokens span 2 GiB."""
+    rng = np.random.default_rng(22)
+    t, v, ld = 250, 8500, 1 << 22
+    x, xs, qx, sx = codes(rng, t, 64)
+    w, ws, qw, sw = codes(rng, v, 64)
+    rows = torch.empty(t, ld, device=DEV)
+    rows[:, v:v + 200].fill_(-7)
+    lp.logits_int8(x, xs, w, ws, out=rows[:, :v])
+    assert np.array_equal(rows[:, :v].cpu().numpy(), oracle.logits_f32(qx, sx, qw, sw))
+    assert (rows[:, v:v + 200] == -7).all()
+    lp.logits_int8(x[:5], xs[:5], w, ws, out=rows[7:12, 100:v + 100])
+    assert np.array_equal(rows[7:12, 100:v + 100].cpu().numpy(),
+                          oracle.logits_f32(qx[:5], sx[:5], qw, sw))
 
 
 def test_the_largest_sums():
@@ -184,9 +208,9 @@ def test_the_largest_sums():
 
 def test_scales_that_are_no_numbers():
     rng = np.random.default_rng(5)
-    for t in (4, 70, 200):
+    for t, v in ((4, 300), (70, 300), (200, 300), (70, 16500), (140, 11100), (200, 8301)):
         x, xs, qx, sx = codes(rng, t, 64)
-        w, ws, qw, sw = codes(rng, 300, 64)
+        w, ws, qw, sw = codes(rng, v, 64)
         xs[1], ws[7], ws[200] = float("nan"), float("inf"), 0.0
         sx[1], sw[7], sw[200] = np.nan, np.inf, 0.0
         got = lp.logits_int8(x, xs, w, ws, dtype=torch.float32).cpu().numpy()
@@ -209,9 +233,10 @@ def score_bound(z, temperature, v, scores):
     and log2(e) / temperature and its product two more (5 e |z| / tau, for the
     target and for the sum's terms); a term of the sum is one exponential
     (2 e, and e of its argument, at most |2 z| / tau) and a block's 31 + 2 sums;
-    joining takes 4 roundings and an exponential a step, over ceil(blocks / 16)
-    blocks and 16 segments; logarithm, difference and the last product 4 e of
-    the scores' size."""
+    joining takes 4 roundings and an exponential a step, over ceil(blocks / 64)
+    blocks of a segment, two pairs of segments and 15 more, of which those without
+    a block cost nothing (at most ceil(blocks / 16) + 16 in all); logarithm,
+    difference and the last product 4 e of the scores' size."""
     e = 2.0 ** -24
     size = np.abs(z).max() / temperature
     steps = -(-(-(-v // LP_INT8_BLOCK)) // 16) + 16
@@ -236,7 +261,8 @@ def test_scores(t, v, h, temperature):
     assert np.abs(lse.cpu().numpy() - want_lse).max() <= bound
 
 
-@pytest.mark.parametrize("t,v,h", [(5, 1000, 64), (40, 700, 256), (300, 1500, 128)])
+@pytest.mark.parametrize("t,v,h", [(5, 1000, 64), (40, 700, 256), (300, 1500, 128), (60, 32900, 64),
+                                   (150, 11300, 300), (520, 4001, 128)])
 def test_scores_of_bf16_logits(t, v, h):
     rng = np.random.default_rng(t)
     x, xs, qx, sx = codes(rng, t, h)
@@ -271,15 +297,37 @@ def test_targets_outside_the_vocabulary():
             lp.score_int8(x, xs, w, ws, ids, check=True)
 
 
+def test_negative_scales():
+    """Scales are any numbers: the smallest sum then is the largest logit."""
+    rng = np.random.default_rng(8)
+    for t, v in ((9, 400), (100, 400), (150, 11100)):
+        x, xs, qx, sx = codes(rng, t, 64)
+        w, ws, qw, sw = codes(rng, v, 64)
+        xs[::2] *= -1
+        xs[3] = 0
+        ws[::3] *= -1
+        sx, sw = xs.cpu().numpy(), ws.cpu().numpy()
+        got = lp.logits_int8(x, xs, w, ws, dtype=torch.float32).cpu().numpy()
+        assert np.array_equal(got, oracle.logits_f32(qx, sx, qw, sw))
+        ids = rng.integers(0, v, t)
+        for rounded in (False, True):
+            z = torch.from_numpy(oracle.logits_f32(qx, sx, qw, sw))
+            z = z.bfloat16().double().numpy() if rounded else oracle.logits(qx, sx, qw, sw)
+            out = lp.score_int8(x, xs, w, ws, dev(ids, torch.int64), bf16_logits=rounded)
+            want, _ = oracle.log_softmax_at(z, ids)
+            assert np.abs(out.cpu().numpy() - want).max() <= score_bound(z, 1.0, v, want)
+
+
 def test_a_rows_bits_do_not_depend_on_its_batch():
     rng = np.random.default_rng(11)
+    v = 20011
     x, xs, _, _ = codes(rng, 700, 384)
-    w, ws, _, _ = codes(rng, 3000, 384)
-    ids = dev(rng.integers(0, 3000, 700), torch.int64)
+    w, ws, _, _ = codes(rng, v, 384)
+    ids = dev(rng.integers(0, v, 700), torch.int64)
     z = lp.logits_int8(x, xs, w, ws, dtype=torch.float32)
     s = lp.score_int8(x, xs, w, ws, ids)
     for lo, hi in ((0, 1), (5, 12), (3, 19), (10, 40), (100, 164), (0, 65), (50, 200), (10, 300),
-                   (0, 513), (699, 700)):
+                   (0, 513), (2, 140), (30, 190), (17, 700), (699, 700)):
         assert same_bits(lp.logits_int8(x[lo:hi], xs[lo:hi], w, ws, dtype=torch.float32), z[lo:hi])
         assert same_bits(lp.score_int8(x[lo:hi], xs[lo:hi], w, ws, ids[lo:hi]), s[lo:hi])
 
