@@ -5,7 +5,8 @@
 //
 // Two ways through a row, chosen by its settings alone:
 //
-// By a short list (top_k in [1, 420], the greedy draw, min-p alone, and up to 420
+// By a short list (top_k in [1, 420] (200 for distributions), the greedy draw, min-p
+// alone, and up to 420
 // top logits): collect_kernel reads the row once, keeps the tokens that can still
 // be among the first in a list in LDS, and sums exp(z - m) per wave and chunk for
 // the log-sum-exp, which log_sum corrects by the listed tokens. The list is
@@ -56,6 +57,12 @@ constexpr int kShort = 2048;          // ... by a workgroup of collect_kernel
 // rows: 300 101 and 137, 420 112 and 140, 460 282 and 145, 512 778 and 150; 64 rows:
 // 420 79 and 81, 460 144 and 82; one row: 420 60 and 77, 512 62 and 80.
 constexpr int kShortTop = 420;
+// A row's limits need no draw, and by buckets no second list then: up to 200 they
+// go by lists (lists and buckets, bf16 drafts over 151 936: 64 sequences of up to 4,
+// top-k 100 118 and 147 us, 200 134 and 136, 300 164 and 140, 400 180 and 138; one
+// sequence of 4, 100 45 and 52, 200 55 and 53, 400 72 and 55; 128 of 7, 200 317 and
+// 394, 400 412 and 403).
+constexpr int kShortLimit = 200;
 constexpr int kListMax = LP_TOP_MAX;  // tokens that a slice leaves
 constexpr int kMaxSlices = 512;       // of a row
 constexpr uint32_t kOverflow = 0xFFFFFFFFu;    // a slice's count: take the buckets
@@ -513,7 +520,8 @@ __device__ __forceinline__ Settings settings_of(const SelectArgs& a, int64_t n) 
   s.k = s.greedy ? 1u : (uint32_t)max(s.top_k, 0);
   s.kind = kBuckets_;
   if (!s.bad) {
-    if (s.greedy || (s.top_k > 0 && s.top_k <= kShortTop)) s.kind = kTopK;
+    if (s.greedy || (s.top_k > 0 && s.top_k <= (kJob == kLimit ? kShortLimit : kShortTop)))
+      s.kind = kTopK;
     else if (s.top_k <= 0 && s.top_p >= 1.0f && s.min_p > 0.0f && s.min_p <= 1.0f) s.kind = kMinP;
     if (kJob == kLimit && s.kind == kMinP) s.kind = kWholeMinP;
     if (kJob == kLimit && s.kind == kBuckets_ && s.top_k <= 0 && s.top_p >= 1.0f &&
