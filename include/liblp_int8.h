@@ -50,7 +50,7 @@ extern "C" {
  *
  * Layout: q [R, H] with row stride ldq, a multiple of 16, and 16-byte aligned,
  * as the products below take it; the codes behind H up to the next multiple of
- * 16 are written as zeros. Errors: LP_EINVAL for R < 0, H < 1, ldx < H, ldq < H
+ * 16 are written as zeros; q and scale lie apart from x. Errors: LP_EINVAL for R < 0, H < 1, ldx < H, ldq < H
  * or not a multiple of 16, an unknown dtype, NULL or misaligned pointers;
  * LP_EUNSUPPORTED for R or H above 2^31 - 1 or more rows than one dispatch
  * holds (16 777 215). R == 0 does nothing.

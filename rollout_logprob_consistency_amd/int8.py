@@ -9,7 +9,8 @@ and every arithmetic step runs in the library's kernels.
 
 A matrix in 8 bits is int8 codes [rows, H] with unit column stride and one fp32
 scale per row. The head's rows start at multiples of 16 bytes, as quantize_int8
-lays them out; hidden states may lie anywhere. The results carry no derivative.
+lays them out, and its last one has room for whole groups of 16; hidden states may
+lie anywhere. Outputs lie apart from the inputs. The results carry no derivative.
 Scratch memory is allocated per call unless `workspace` is given (a uint8 tensor
 of the library's *_workspace_bytes, 256-byte aligned); calls that may overlap,
 captured graphs among them, must not share one. `bad_rows` (int32 [1]) is a
@@ -47,6 +48,9 @@ def _aligned_codes(name: str, t: torch.Tensor):
     if ld % 16 or t.data_ptr() % 16:
         raise ValueError(f"{name}'s rows must start at multiples of 16 bytes "
                          "(as quantize_int8 lays them out)")
+    last = t.storage_offset() + (rows - 1) * ld + (h + 15) // 16 * 16
+    if rows and t.untyped_storage().nbytes() < last:
+        raise ValueError(f"{name} needs room for whole 16-byte groups in its last row")
     return rows, h, ld
 
 
@@ -74,8 +78,6 @@ def quantize_int8(x: torch.Tensor, *, out: torch.Tensor | None = None,
         if not isinstance(out, torch.Tensor) or out.device != dev or tuple(out.shape) != (r, h):
             raise ValueError(f"out must be [{r}, {h}] on x's device")
         _, _, ldq = _aligned_codes("out", out)
-        if out.untyped_storage().nbytes() < (out.storage_offset() + (r - 1) * ldq + h16 if r else 0):
-            raise ValueError("out needs room for whole 16-byte groups in its last row")
         torch.autograd.graph.increment_version(out)
     if scale is None:
         scale = torch.empty(r, dtype=torch.float32, device=dev)
@@ -160,7 +162,10 @@ def score_int8(x: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, w_scale:
     else:
         po = _like("out", out, (t,), torch.float32, dev)
         torch.autograd.graph.increment_version(out)
-    pl = None if lse is None else _like("lse", lse, (t,), torch.float32, dev)
+    pl = None
+    if lse is not None:
+        pl = _like("lse", lse, (t,), torch.float32, dev)
+        torch.autograd.graph.increment_version(lse)
     L = lib()
     ws = _workspace(workspace, L.lp_score_int8_workspace_bytes(t, h, vt), dev)
     count = _bad_rows(bad_rows, check, dev)

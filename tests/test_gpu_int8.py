@@ -31,7 +31,8 @@ def same_bits(a, b):
 @pytest.mark.parametrize("dtype", list(TYPES))
 @pytest.mark.parametrize("r,h,pad,lead", [(1, 1, 0, 0), (3, 15, 1, 1), (5, 16, 0, 0), (2, 17, 3, 5),
                                           (7, 511, 0, 3), (64, 1000, 7, 0), (9, 4096, 0, 0),
-                                          (2, 8200, 5, 2), (300, 64, 0, 0)])
+                                          (2, 8200, 5, 2), (300, 64, 0, 0), (2, 16384, 0, 0),
+                                          (3, 16400, 8, 0), (2, 40003, 1, 3), (1, 3000001, 0, 0)])
 def test_codes_and_scales(dtype, r, h, pad, lead):
     rng = np.random.default_rng(r * 1000 + h)
     z = rng.normal(size=(r, h)) * np.exp(rng.normal(size=(r, 1)))
@@ -332,6 +333,18 @@ def test_a_rows_bits_do_not_depend_on_its_batch():
         assert same_bits(lp.score_int8(x[lo:hi], xs[lo:hi], w, ws, ids[lo:hi]), s[lo:hi])
 
 
+def test_given_outputs_count_as_written():
+    rng = np.random.default_rng(4)
+    x, xs, _, _ = codes(rng, 4, 48)
+    w, ws, _, _ = codes(rng, 9, 48)
+    out, lse, z = torch.empty(4, device=DEV), torch.empty(4, device=DEV), torch.empty(4, 9, device=DEV)
+    q, s = torch.empty(4, 16, dtype=torch.int8, device=DEV), torch.empty(4, device=DEV)
+    lp.score_int8(x, xs, w, ws, torch.zeros(4, dtype=torch.int64, device=DEV), out=out, lse=lse)
+    lp.logits_int8(x, xs, w, ws, out=z)
+    lp.quantize_int8(z, out=q[:, :9], scale=s)
+    assert [t._version for t in (out, lse, z, q, s)] == [1] * 5
+
+
 def test_refusals_on_the_device():
     rng = np.random.default_rng(1)
     x, xs, _, _ = codes(rng, 4, 48)
@@ -345,6 +358,9 @@ def test_refusals_on_the_device():
             lp.logits_int8(*args)
         with pytest.raises(ValueError, match=text):
             lp.score_int8(*args, ids)
+    short = torch.zeros(33, dtype=torch.int8, device=DEV).view(1, 33)
+    with pytest.raises(ValueError, match="last row"):
+        lp.logits_int8(codes(rng, 4, 33)[0], xs, short, ws[:1])
     with pytest.raises(ValueError, match="dtype"):
         lp.logits_int8(x, xs, w, ws, dtype=torch.float64)
     with pytest.raises(ValueError, match="out"):

@@ -60,7 +60,8 @@ def compare(got, want):
 
 SETTINGS = [dict(), dict(temperature=0.7), dict(temperature=1.4, top_p=0.9),
             dict(top_k=20, top_p=0.8), dict(top_k=1), dict(min_p=0.05), dict(temperature=0.0),
-            dict(top_k=500), dict(top_k=200), dict(top_k=201, min_p=0.01), dict(top_k=600, top_p=0.95, min_p=0.01), dict(top_p=0.5, min_p=0.2),
+            dict(top_k=500), dict(top_k=200), dict(top_k=201, min_p=0.01),
+            dict(top_k=600, top_p=0.95, min_p=0.01), dict(top_p=0.5, min_p=0.2),
             dict(top_p=0.0), dict(top_p=0.9, min_p=1.5), dict(temperature=0.2)]
 
 
@@ -111,6 +112,22 @@ def test_ragged_sequences_with_settings_of_their_own(model):
     assert (got[1].cpu().numpy() >= 0).all()
 
 
+@pytest.mark.parametrize("b,d,v", [(1366, 1, 70), (820, 2, 200), (5000, 0, 40), (1000, 3, 2500)])
+def test_thousands_of_rows(b, d, v):
+    """To both sides of 4 096, whole ones and others, some sequences without
+    drafts, and one with a count that is none."""
+    rng = np.random.default_rng(b)
+    how = dict(temperature=rng.choice(np.float32([0, 0.7, 1]), b),
+               top_k=rng.choice(np.int32([0, 0, 0, 9]), b),
+               top_p=rng.choice(np.float32([1, 1, 0.9]), b),
+               min_p=rng.choice(np.float32([0, 0, 0.1]), b))
+    counts = rng.integers(0, d + 1, b).astype(np.int32)
+    counts[17] = d + 1
+    data = batch(b, b, d, v, "bf16", True, **how)
+    got = check(*data, counts, **how)
+    assert (got[1] < 0).nonzero().flatten().tolist() == [17]
+
+
 @pytest.mark.parametrize("how", [dict(), dict(top_p=0.5), dict(top_k=300), dict(top_k=9001),
                                  dict(min_p=0.5), dict(min_p=1.0), dict(top_p=0.7, min_p=0.9),
                                  dict(temperature=0.0), dict(top_k=9001, top_p=0.6)], ids=str)
@@ -140,6 +157,37 @@ def test_masked_tokens(how):
     got = check(zt, yt, np.array([[7], [3]]), np.full((2, 2), 0.5, np.float32), exact, exact_y,
                 **how)
     assert got[0].tolist() == [[7, 8], [9, -1]] and got[1].tolist() == [1, 0]
+
+
+LOWEST = {"fp32": np.finfo(np.float32).min, "bf16": -(2.0 - 2.0 ** -7) * 2.0 ** 127, "fp16": -65504.0}
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("how", [dict(), dict(temperature=0.3, top_p=0.9), dict(top_k=30),
+                                 dict(min_p=0.1), dict(temperature=0.0)], ids=str)
+def test_masks_of_the_lowest_value(dtype, how):
+    """Masks that are finite: behind the language's tokens, in all but one place, and
+    throughout; and rows at the type's other end."""
+    b, d, v = 6, 3, 5003
+    rng = np.random.default_rng(12)
+    z = np.floor(8 * rng.normal(size=(b * (d + 1), v))) / 4
+    low = LOWEST[dtype]
+    z[:, ::3] = low
+    z[5], z[6], z[7] = low, low, -low
+    z[6, 4321] = 1.5
+    z[8, 1:] = low
+    z[9, 2500:] = -np.inf
+    y = z.reshape(b, d + 1, v)[:, :d].reshape(b * d, v).copy()
+    y[rng.random(y.shape) < 0.2] = 0.5
+    y[4] = low
+    zt, z = place(z, dtype)
+    yt, y = place(y, dtype)
+    ids = rng.integers(0, v, (b, d))
+    for i in range(b):
+        for j in range(d):
+            p = oracle.distribution(y[i * d + j], **how)[0]
+            ids[i, j] = rng.choice(v, p=p / p.sum())
+    check(zt, yt, ids, rng.random((b, d + 1)).astype(np.float32), z, y, **how)
 
 
 def test_the_same_rows_are_always_accepted():
