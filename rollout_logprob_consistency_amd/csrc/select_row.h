@@ -856,14 +856,16 @@ __device__ __forceinline__ float max_groups(Group<D> (&g)[kGroups], bool& odd) {
   return wave_max_f32(m);
 }
 
-// From the maximum of all, masked tokens left out; out of line, as it is rare.
+// From the maximum of all, masked tokens left out; out of line, as it is rare. (The
+// difference is taken first: beside a large maximum's product with c, rounded, the
+// exact one inside an fma is far from it.)
 template <class D>
 __device__ __noinline__ Part whole_again(Groups<D> v, double c) {
   bool odd;
   const float m = max_groups<D>(v.g, odd);
-  const double b = m == -INFINITY ? 0.0 : (double)m * c;
+  const double top = m;
   const double s = sum_groups<D>(v.g, kGroups, [&](float z) LP_INLINE {
-    return z == -INFINITY ? 0.0 : exp2_f64(fma((double)z, c, -b));
+    return z == -INFINITY ? 0.0 : exp2_f64(((double)z - top) * c);
   });
   return {m, odd ? (double)NAN : s};
 }
@@ -877,6 +879,7 @@ __device__ __forceinline__ Part whole_part(Groups<D>& v, int groups, double c, b
     const double b = (double)p.m * c;
     p.s = sum_groups<D>(v.g, groups,
                         [&](float z) LP_INLINE { return exp2_f64(fma((double)z, c, -b)); });
+    if (!(fabs(b) < 0x1p16)) p.s = 0.0;  // (b's rounding is 2^-38 at most below that)
   } else {
     p.s = sum_groups<D>(v.g, groups, [&](float z) LP_INLINE { return exp2_f64((double)z * c); });
   }
@@ -1748,7 +1751,7 @@ __device__ __forceinline__ Whole join_whole(const SelectArgs& a, int64_t n, floa
   double sum = 0.0;
   for (int i = lane; i < parts; i += 64) {
     const double s = p[i].s;
-    sum += p[i].m == -INFINITY ? s : s * exp2_f64((double)p[i].m * c - (double)top * c);
+    sum += p[i].m == -INFINITY ? s : s * exp2_f64(((double)p[i].m - (double)top) * c);
   }
   sum = wave_sum(sum);
   return {top, top == -INFINITY ? (double)NAN : sum};
@@ -1780,7 +1783,7 @@ __device__ __forceinline__ void limit_min_p(const SelectArgs& a, const Settings&
   row.zmax = w.top;
   row.inv = kPerNat / (double)st.tau;
   const float least = least_kept(row, fmax(0.0, -log((double)st.min_p) * kPerNat));
-  const double c = kLog2E / (double)st.tau, b = (double)w.top * c;
+  const double c = kLog2E / (double)st.tau, top = w.top;
   double s = 0.0, all;
   row.for_chunks(0, row.chunks(), [&](Group<D>(&g)[kGroups], int) LP_INLINE {
 #pragma unroll
@@ -1789,7 +1792,7 @@ __device__ __forceinline__ void limit_min_p(const SelectArgs& a, const Settings&
       for (int i = 0; i < D::kVec; ++i) {
         const float z = g[j].get(i);
         if (__ballot(z >= least) == 0) continue;
-        s += z >= least ? exp2_f64(fma((double)z, c, -b)) : 0.0;
+        s += z >= least ? exp2_f64(((double)z - top) * c) : 0.0;
       }
   });
   block_scan(s, sh.wave_f64, &all);
