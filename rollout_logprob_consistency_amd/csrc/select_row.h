@@ -809,81 +809,92 @@ __device__ __forceinline__ void collect_buckets(const Row<D>& row, S& sh, int c0
 // ---- Rows that are summed whole (kLimit) ----------------------------------------
 // Where every token is kept, or those that min-p leaves, nothing has to be ordered:
 // a row's weights are summed, in fp64, as what is drawn between two distributions
-// needs digits that fp32's exponentials lose. An element takes 17 instructions,
-// which bounds it: rows of 151 936 bf16 logits, 1 920 of them, take 200 us.
+// needs digits that fp32's exponentials lose (5.5e-11 of a weight are enough: a
+// random number has steps of 2^-24). An element takes 15 instructions,
+// which bounds it: rows of 151 936 bf16 logits, 1 920 of them, take 177 us.
 
 constexpr double kLog2E = 1.4426950408889634;
 
+// The largest of three, or NaN where one is.
+__device__ __forceinline__ float maximum3(float a, float b, float c) {
+  float m;
+  asm("v_maximum3_f32 %0, %1, %2, %3" : "=v"(m) : "v"(a), "v"(b), "v"(c));
+  return m;
+}
+
 // The sum of 2^((z - m) c) over a wave's part of a chunk, and m: the maximum where
 // it is wanted (`top`), else 0, as fp64 has room for 2^1000 either way. Where that
-// does not suffice, or a logit is not finite, the sum is formed again. The wave's
-// groups from `groups` on lie behind the row.
+// does not suffice the sum is formed again. The wave's groups from `groups` on lie
+// behind the row.
 template <class D>
 struct Groups {
   Group<D> g[kGroups];
 };
 
+// (most: the lane's largest logit, or NaN; a lane's two logits at a time.)
 template <class D, class F>
-__device__ __forceinline__ double sum_groups(Group<D> (&g)[kGroups], int groups, F weight) {
+__device__ __forceinline__ double sum_groups(Group<D> (&g)[kGroups], int groups, float& most,
+                                             F weight) {
   double s = 0.0;
+  most = -INFINITY;
 #pragma unroll
   for (int j = 0; j < kGroups; ++j) {
     if (j >= groups) break;
     g[j].fresh();
 #pragma unroll
-    for (int i = 0; i < D::kVec; ++i) {
-      s += weight(g[j].get(i));
-      if (i % 4 == 3) __builtin_amdgcn_sched_barrier(0);  // bounds the registers in use
+    for (int i = 0; i < D::kVec; i += 2) {
+      const float z0 = g[j].get(i), z1 = g[j].get(i + 1);
+      most = maximum3(most, z0, z1);
+      s += weight(z0);
+      s += weight(z1);
+      if (i % 4 == 2) __builtin_amdgcn_sched_barrier(0);  // bounds the registers in use
     }
   }
   return wave_sum(s);
 }
 
 template <class D>
-__device__ __forceinline__ float max_groups(Group<D> (&g)[kGroups], bool& odd) {
+__device__ __forceinline__ float max_groups(Group<D> (&g)[kGroups]) {
   float m = -INFINITY;
-  odd = false;
 #pragma unroll
   for (int j = 0; j < kGroups; ++j) {
     g[j].fresh();
 #pragma unroll
-    for (int i = 0; i < D::kVec; ++i) {
-      m = fmaxf(m, g[j].get(i));
-      odd |= !(g[j].get(i) < INFINITY);
-    }
+    for (int i = 0; i < D::kVec; i += 2) m = maximum3(m, g[j].get(i), g[j].get(i + 1));
   }
-  odd = __ballot(odd) != 0;
   return wave_max_f32(m);
 }
 
-// From the maximum of all, masked tokens left out; out of line, as it is rare. (The
-// difference is taken first: beside a large maximum's product with c, rounded, the
-// exact one inside an fma is far from it.)
+// From the maximum of all; out of line, as it is rare. (The difference is taken
+// first: beside a large maximum's product with c, rounded, the exact one inside an
+// fma is far from it.)
 template <class D>
 __device__ __noinline__ Part whole_again(Groups<D> v, double c) {
-  bool odd;
-  const float m = max_groups<D>(v.g, odd);
+  const float m = max_groups<D>(v.g);
   const double top = m;
-  const double s = sum_groups<D>(v.g, kGroups, [&](float z) LP_INLINE {
+  float most;
+  const double s = sum_groups<D>(v.g, kGroups, most, [&](float z) LP_INLINE {
     return z == -INFINITY ? 0.0 : exp2_f64(((double)z - top) * c);
   });
-  return {m, odd ? (double)NAN : s};
+  return {m, s};
 }
 
 template <class D>
 __device__ __forceinline__ Part whole_part(Groups<D>& v, int groups, double c, bool top) {
   Part p = {0.0f, 0.0};
+  double b = 0.0;
   if (top) {
-    bool odd;
-    p.m = max_groups<D>(v.g, odd);
-    const double b = (double)p.m * c;
-    p.s = sum_groups<D>(v.g, groups,
-                        [&](float z) LP_INLINE { return exp2_f64(fma((double)z, c, -b)); });
-    if (!(fabs(b) < 0x1p16)) p.s = 0.0;  // (b's rounding is 2^-38 at most below that)
-  } else {
-    p.s = sum_groups<D>(v.g, groups, [&](float z) LP_INLINE { return exp2_f64((double)z * c); });
+    p.m = max_groups<D>(v.g);
+    b = -(double)p.m * c;
   }
-  return p.s > 0x1p-1000 && p.s < 0x1p1000 ? p : whole_again(v, c);
+  float most;
+  const double b900 = b + kExp2From;
+  p.s = sum_groups<D>(v.g, groups, most,
+                      [&](float z) LP_INLINE { return exp2_900<7>(fma((double)z, c, b900)); });
+  if (__ballot(!(most < INFINITY))) return {p.m, (double)NAN};
+  if (__ballot(most > -INFINITY) == 0) return {-INFINITY, 0.0};
+  // (b's rounding is 2^-38 at most below 2^16.)
+  return fabs(b) < 0x1p16 && p.s > 0x1p-800 && p.s < 0x1p1000 ? p : whole_again(v, c);
 }
 
 __device__ __forceinline__ bool is_whole(const Settings& s) {

@@ -53,6 +53,12 @@ struct Dist {
   __device__ __forceinline__ bool keeps(float z, int v) const {
     return z > z_last || (z == z_last && v <= v_last);
   }
+  // Whether every token is kept and offset() has its digits: 2^-42 of a weight.
+  __device__ __forceinline__ bool plain() const {
+    return z_last == -3.4028234663852886e38f && v_last == INT32_MAX && fabs(offset()) < 0x1p11;
+  }
+  // prob(z) is 2^(z c + offset()).
+  __device__ __forceinline__ double offset() const { return -base * c - log2_kept; }
   // Of a finite token that it keeps.
   __device__ __forceinline__ double prob(float z) const {
     return exp2_f64(fma((double)z - base, c, -log2_kept));
@@ -139,6 +145,8 @@ struct Weights {
   const typename D::Raw* draft;  // null: there is none
   int64_t gone;                  // the token that weighs nothing, -1: none
   int V;
+  bool plain;  // all tokens are kept, on both sides; then their offsets for exp2_900
+  double p_off, q_off;
 
   // With `whole`, p itself.
   __device__ __forceinline__ Weights(const VerifyArgs& a, const Sequence& s, bool whole) {
@@ -149,13 +157,19 @@ struct Weights {
     draft = nullptr;
     gone = -1;
     V = r.V;
+    plain = p.plain();
+    p_off = p.offset() + kExp2From;
+    q_off = 0.0;
     if (whole || s.accepted == s.count) return;
     const int64_t d = s.b * r.drafts + s.accepted;
     if (r.draft_logits) {
       draft = static_cast<const typename D::Raw*>(r.draft_logits) + d * r.ld_draft;
       q = dist_of(a, s, draft_limit(a, s.b, s.accepted));
+      plain = plain && q.plain();
+      q_off = q.offset() + kExp2From;
     } else {
       gone = read_global(a.draft_ids, d);  // the draft's whole probability
+      plain = false;
     }
   }
   // A lane's logits of a stretch, and their weights; 0 behind the row. A wave whose
@@ -172,7 +186,18 @@ struct Weights {
     if (draft) l.y = load_group<D>(draft, l.v, V);
     return l;
   }
+  // Where every token is kept there is nothing to compare (128 sequences of 151 936
+  // bf16 tokens: 35 us, with the comparisons 60 us).
   __device__ __forceinline__ void weigh(const Loaded& l, double (&w)[D::kVec]) const {
+    if (plain) {
+#pragma unroll
+      for (int i = 0; i < D::kVec; ++i) w[i] = exp2_900<8>(fma((double)l.z.get(i), p.c, p_off));
+      if (!draft) return;
+#pragma unroll
+      for (int i = 0; i < D::kVec; ++i)
+        w[i] = fmax(w[i] - exp2_900<8>(fma((double)l.y.get(i), q.c, q_off)), 0.0);
+      return;
+    }
 #pragma unroll
     for (int i = 0; i < D::kVec; ++i) {
       const float a = l.z.get(i), b = l.y.get(i);  // (-inf behind the row)

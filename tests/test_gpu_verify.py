@@ -159,6 +159,22 @@ def test_masked_tokens(how):
     assert got[0].tolist() == [[7, 8], [9, -1]] and got[1].tolist() == [1, 0]
 
 
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("how", [dict(), dict(min_p=0.1), dict(temperature=0.5)], ids=str)
+def test_rows_that_hold_no_number(dtype, how):
+    """A NaN or an infinity in any place of a row that is summed whole, beside masked
+    tokens: the sequence has no verdict, and its neighbours have theirs."""
+    b, d, v = 9, 1, 9001
+    z, y, ids, u, exact, exact_y = batch(3, b, d, v, dtype, True, masked=0.5, **how)
+    for row, at, value in ((1, 0, np.nan), (4, v - 1, np.nan), (8, 4097, np.inf), (10, 77, -np.nan)):
+        z[row, at] = value
+        exact[row, at] = value
+    y[5, 8000] = exact_y[5, 8000] = np.nan
+    y[7] = exact_y[7] = -np.inf
+    got = check(z, y, ids, u, exact, exact_y, **how)
+    assert (got[1] < 0).nonzero().flatten().tolist() == [0, 2, 4, 5, 7]
+
+
 LOWEST = {"fp32": np.finfo(np.float32).min, "bf16": -(2.0 - 2.0 ** -7) * 2.0 ** 127, "fp16": -65504.0}
 
 
