@@ -358,12 +358,16 @@ __global__ __launch_bounds__(64 * kStreamWaves) void stream_kernel(Int8Args a) {
 // ---- Tile kernel --------------------------------------------------------------
 // Four waves compute 256 vocabulary rows x 32 kJ tokens, 128 x 16 kJ each: with
 // kJ = 8, 256 accumulators in the AGPRs. K stages of 128 bytes go from memory
-// straight into two alternating LDS buffers of up to 64 KiB; the 16-byte chunks of a row are
+// straight into LDS buffers in turn: three of up to 52 KiB up to kJ = 5, so that a
+// stage's copies have a whole stage to land in (heads of 151 936 x 4 096, two buffers
+// and three: 320 rows 243 and 219 us, 128 rows 156 and 144, 64 rows 137 and 131), else
+// two of up to 64 KiB. The 16-byte chunks of a row are
 // permuted (swz_w, swz_x) so that the fragment reads meet no bank conflicts. One
 // barrier a stage: the MFMAs of a stage's second half are carried across it, and
-// the next stage's copies are spread over the whole stage. A workgroup stays on
-// its CU and takes tile after tile: during a tile's last stage the next one's
-// first is copied, so that the sums' scales, roundings and stores (15 % of a tile
+// the copies are spread over the whole stage (1 024 rows with one each 6 MFMAs 573 us,
+// each 3 606, each 2 635). A workgroup stays on
+// its CU and takes tile after tile: during a tile's last stages the next one's
+// first are copied, so that the sums' scales, roundings and stores (15 % of a tile
 // of 4 096 hidden elements) are all that the MFMAs wait for.
 constexpr int kTileRows = 256;                      // of W
 constexpr int kTileThreads = 256;
@@ -402,9 +406,8 @@ __device__ __forceinline__ TileAt tile_at(const Int8Args& a, int tile, int n_vt,
   return t;
 }
 
-// kJ = 2 leaves room for two workgroups a CU.
 template <int kJ, class Out>
-__global__ __launch_bounds__(kTileThreads, kJ == 2 ? 2 : 1) void tile_kernel(Int8Args a, int n_vt,
+__global__ __launch_bounds__(kTileThreads, 1) void tile_kernel(Int8Args a, int n_vt,
                                                                             int n_tt) {
   constexpr int kTokens = 32 * kJ, kCopies = kUnitCopies + kJ;
   constexpr int kBufferB = kUnitB + kTokens * kInt8StageK;
@@ -412,7 +415,10 @@ __global__ __launch_bounds__(kTileThreads, kJ == 2 ? 2 : 1) void tile_kernel(Int
   constexpr int kSlotsPerCopy = (2 * kHalf - 2) / kCopies;  // from one copy to the next
   constexpr int kEvery = kSlotsPerCopy < 6 ? kSlotsPerCopy : 6;
   constexpr int kPerGroup = (kJ + 3) / 4;                   // X reads of a group
-  __shared__ __attribute__((aligned(1024))) char ring[2 * kBufferB];
+  constexpr int kBuffers = kJ <= 5 ? 3 : 2, kAhead = kBuffers - 1;
+  constexpr int kInFlight = (kAhead - 1) * kCopies;  // copies of the stages after the next
+  static_assert(kInFlight < 64, "a counter's width");
+  __shared__ __attribute__((aligned(1024))) char ring[kBuffers * kBufferB];
   const int lane = threadIdx.x & 63, lcol = lane & 15, lg = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave & 1, wn = wave >> 1;
@@ -484,46 +490,61 @@ __global__ __launch_bounds__(kTileThreads, kJ == 2 ? 2 : 1) void tile_kernel(Int
       if ((do_rd_) && j_ == kJ - 1) fw[g_] = RD_W(g_, (rh_), (rb_));                          \
       const int pu_ = (p0_) + u;                                                              \
       if (pu_ % kEvery == 1 && pu_ / kEvery < kCopies)                                        \
-        COPY(pu_ / kEvery, wres, xres, off, b ^ 1);                                           \
+        COPY(pu_ / kEvery, wres, xres, off, b == 0 ? kAhead : b - 1);                         \
       FENCE();                                                                                \
     }                                                                                         \
   } while (0)
-// The beginning of stage k: it has landed and every wave is done with the buffer
-// that the next one goes into. That is the same tile's, or the next tile's first
-// (the last tile's own once more, which nothing reads).
-#define STAGE(k_)                                                                             \
-  __builtin_amdgcn_s_waitcnt(0x0070); /* vmcnt(0) lgkmcnt(0) */                               \
-  __syncthreads();                                                                            \
-  int following = (k_) + 1;                                                                   \
-  if (following == nk) {                                                                      \
-    at = tile_at<kTokens>(a, after < n_tiles ? after : tile, n_vt, n_tt, nk);                 \
-    following = 0;                                                                            \
-  }                                                                                           \
-  following += at.first;                                                                      \
-  const uint32_t off = (uint32_t)(following >= nk ? following - nk : following) * kInt8StageK; \
+// The beginning of a stage: it has landed, and every wave is done with the buffer
+// that the one kAhead stages on goes into. That is the same tile's, or a following
+// one's (behind the last tile the first once more, which nothing reads).
+#define STAGE()                                                                               \
+  __builtin_amdgcn_s_waitcnt(0x0070 | (kInFlight & 15) | (kInFlight >> 4) << 14);             \
+  asm volatile("" ::: "memory");                                                              \
+  FENCE();                                                                                    \
+  __builtin_amdgcn_s_barrier();                                                               \
+  asm volatile("" ::: "memory");                                                              \
+  FENCE();                                                                                    \
+  const int k_ = ahead + at.first;                                                            \
+  const uint32_t off = (uint32_t)(k_ >= nk ? k_ - nk : k_) * kInt8StageK;                     \
   const __amdgpu_buffer_rsrc_t wres = make_rsrc(at.w, at.w_bytes);                            \
   const __amdgpu_buffer_rsrc_t xres = make_rsrc(at.x, at.x_bytes);                            \
+  NEXT();                                                                                     \
   FENCE()
+#define NEXT()                                                                                \
+  if (++ahead == nk) {                                                                        \
+    ahead = 0;                                                                                \
+    after += (int)gridDim.x;                                                                  \
+    at = tile_at<kTokens>(a, after < n_tiles ? after : (int)blockIdx.x, n_vt, n_tt, nk);      \
+  }
 
+  // The stage that is copied next, and its tile.
   TileAt at = tile_at<kTokens>(a, blockIdx.x, n_vt, n_tt, nk);
+  int ahead = 0, after = blockIdx.x;
   int b = 0;
-  {
+#pragma unroll
+  for (int s = 0; s < kAhead; ++s) {
+    const int k_ = ahead + at.first;
+    const uint32_t off = (uint32_t)(k_ >= nk ? k_ - nk : k_) * kInt8StageK;
     const __amdgpu_buffer_rsrc_t wres = make_rsrc(at.w, at.w_bytes);
     const __amdgpu_buffer_rsrc_t xres = make_rsrc(at.x, at.x_bytes);
+    FENCE();
 #pragma unroll
-    for (int c = 0; c < kCopies; ++c) COPY(c, wres, xres, (uint32_t)at.first * kInt8StageK, 0);
+    for (int c = 0; c < kCopies; ++c) COPY(c, wres, xres, off, s);
+    NEXT();
   }
   for (int tile = blockIdx.x; tile < n_tiles; tile += gridDim.x) {
-    const int after = tile + (int)gridDim.x;
-    const int v0 = at.v0, t0 = at.t0;
+    int vt, tt;
+    tile_of(tile, n_vt, n_tt, kGroupV, vt, tt);
+    const int v0 = __builtin_amdgcn_readfirstlane(vt) * kTileRows;
+    const int t0 = __builtin_amdgcn_readfirstlane(tt) * kTokens;
     {
-      STAGE(0);
+      STAGE();
       STEP(false, false, true, fx1, fx0, 0, b, 0);
       STEP(true, true, true, fx0, fx1, 1, b, kHalf);
     }
     for (int k = 1; k < nk; ++k) {
-      b ^= 1;
-      STAGE(k);
+      b = b == kAhead ? 0 : b + 1;
+      STAGE();
       STEP(true, false, true, fx1, fx0, 0, b, 0);
       STEP(true, false, true, fx0, fx1, 1, b, kHalf);
     }
@@ -546,7 +567,7 @@ __global__ __launch_bounds__(kTileThreads, kJ == 2 ? 2 : 1) void tile_kernel(Int
       const uint32_t off = 0;
       STEP(true, false, false, fx1, fx0, 0, b, 4 * kHalf);
     }
-    b ^= 1;
+    b = b == kAhead ? 0 : b + 1;
     if (there) {
       const Place place = place_of(Out(), a, vb, t0 + wn * 16 * kJ, 16 * kJ, lane_e);
 #pragma unroll
@@ -563,6 +584,7 @@ __global__ __launch_bounds__(kTileThreads, kJ == 2 ? 2 : 1) void tile_kernel(Int
   }
   __builtin_amdgcn_s_waitcnt(0x0070);  // the last copies land before the LDS is given back
 #undef STAGE
+#undef NEXT
 #undef STEP
 #undef COPY
 #undef RD_W
@@ -701,8 +723,7 @@ void stream(const Int8Args& a, hipStream_t s) {
 template <int kJ>
 void tiles(const Int8Args& a, hipStream_t s) {
   const int n_vt = (a.V + kTileRows - 1) / kTileRows, n_tt = (a.T + 32 * kJ - 1) / (32 * kJ);
-  const int places = kJ == 2 ? 2 * kCus : kCus;
-  const dim3 grid((uint32_t)std::min<int64_t>((int64_t)n_vt * n_tt, places));
+  const dim3 grid((uint32_t)std::min<int64_t>((int64_t)n_vt * n_tt, kCus));
   with_output(a, [&](auto out) {
     tile_kernel<kJ, decltype(out)><<<grid, kTileThreads, 0, s>>>(a, n_vt, n_tt);
   });
