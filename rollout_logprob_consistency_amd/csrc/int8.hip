@@ -258,7 +258,7 @@ __device__ __forceinline__ int first_stage(int block, int nk) {
 }
 
 // ---- Streaming kernel ---------------------------------------------------------
-// A workgroup takes one block of vocabulary rows and 16 kNT tokens; its four
+// A workgroup takes one block of vocabulary rows and all (16 kNT) tokens; its four
 // waves take the K stages in turn (the integer sums may be split anyhow), and
 // their sums are joined in LDS, each wave finishing a quarter of the token
 // tiles. Fragments go from memory straight into registers.
@@ -269,15 +269,15 @@ __global__ __launch_bounds__(64 * kStreamWaves) void stream_kernel(Int8Args a) {
   __shared__ int red[kStreamWaves][kNT][kPerLane][64];
   const int lane = threadIdx.x & 63, lcol = lane & 15, lg = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int v0 = blockIdx.x * kInt8BlockV, t0 = blockIdx.y * 16 * kNT;
+  const int v0 = blockIdx.x * kInt8BlockV;
   const int nk = (a.H + kInt8StageK - 1) / kInt8StageK;
   // Rows are clamped to the matrices; what they give is not stored. Bytes
   // behind H meet zeros of x.
-  const int rows = a.V - v0, tokens = a.T - t0;
+  const int rows = a.V - v0, tokens = a.T;
   const int64_t w_bytes = (int64_t)(rows - 1) * a.ldw + (a.H + 15) / 16 * 16;
   const int64_t x_bytes = (int64_t)(tokens - 1) * a.ldx + (int64_t)nk * kInt8StageK;
   const __amdgpu_buffer_rsrc_t wres = rsrc_of(a.w + (int64_t)v0 * a.ldw, w_bytes);
-  const __amdgpu_buffer_rsrc_t xres = rsrc_of(a.x + (int64_t)t0 * a.ldx, x_bytes);
+  const __amdgpu_buffer_rsrc_t xres = rsrc_of(a.x, x_bytes);
   uint32_t woff[kTiles], xoff[kNT];
 #pragma unroll
   for (int i = 0; i < kTiles; ++i)
@@ -335,7 +335,7 @@ __global__ __launch_bounds__(64 * kStreamWaves) void stream_kernel(Int8Args a) {
   }
   if (i < mine) multiply(even);
   const RowScales scales = row_scales(a, v0, lg);
-  const Place place = place_of(Out(), a, v0, t0, 16 * kNT, lane);
+  const Place place = place_of(Out(), a, v0, 0, 16 * kNT, lane);
 #pragma unroll
   for (int j = 0; j < kNT; ++j)
 #pragma unroll
@@ -349,7 +349,7 @@ __global__ __launch_bounds__(64 * kStreamWaves) void stream_kernel(Int8Args a) {
 #pragma unroll
       for (int w = 0; w < kStreamWaves; ++w) sums[k] += red[w][j][k][lane];
     }
-    const int t = t0 + 16 * j + lcol;
+    const int t = 16 * j + lcol;
     finish_block(Out(), a, place, j, sums, scales, v0, t, read_global(a.x_scale, min(t, a.T - 1)),
                  lg);
   }
@@ -712,11 +712,9 @@ void with_output(const Int8Args& a, F launch) {
 
 template <int kNT>
 void stream(const Int8Args& a, hipStream_t s) {
-  const dim3 grid((uint32_t)((a.V + kInt8BlockV - 1) / kInt8BlockV),
-                  (uint32_t)((a.T + 16 * kNT - 1) / (16 * kNT)));
-  const int threads = 64 * kStreamWaves;
+  const dim3 grid((uint32_t)((a.V + kInt8BlockV - 1) / kInt8BlockV));
   with_output(a, [&](auto out) {
-    stream_kernel<kNT, decltype(out)><<<grid, threads, 0, s>>>(a);
+    stream_kernel<kNT, decltype(out)><<<grid, 64 * kStreamWaves, 0, s>>>(a);
   });
 }
 
@@ -758,20 +756,24 @@ hipError_t launch_int8(Int8Args a, hipStream_t stream_) {
     a.x = a.staged;
     a.ldx = row;
   }
-  // Up to 16 tokens by streams (over 151 936 tokens, 16 rows 120 us, by tiles 131),
-  // and more where their workgroups (one a CU) all run at once, as splitting K
-  // shortens what each has to do: streams and tiles, heads of 4 096 hidden elements,
-  // 64 rows over 32 003 tokens 38 and 42 us, 512 over 4 000 29 and 46, 1 000 over
-  // 1 000 30 and 50; and beyond, 100 rows over 32 003 64 and 48, 1 000 over 4 000 57
-  // and 49, 64 over 151 936 173 and 139. Tiles are as few as tokens by 256 make them,
-  // and as narrow as that leaves them: 320 rows over 151 936 by two of 160 239 us, of
-  // 256 270 us, by three of 128 295 us.
-  const int64_t streams = (a.V + kInt8BlockV - 1) / kInt8BlockV * ((a.T + 63) / 64);
-  const int64_t n_tt = (a.T + 255) / 256;
+  // Tiles are as few as tokens by 256 make them, and narrower where they would leave
+  // CUs idle; and as narrow as their number leaves them. (200 rows over 32 003, H =
+  // 4 096, by two tiles of 100 42 us, by one 61; 256 over 16 000 by four 23, by one
+  // 44; but 320 over 151 936 by two of 160 210, by three of 107 248.)
+  const int64_t n_vt = (a.V + kTileRows - 1) / kTileRows;
+  const int64_t n_tt =
+      std::max<int64_t>((a.T + 255) / 256, std::min<int64_t>(kCus / n_vt, (a.T + 63) / 64));
   const int64_t width = ((a.T + n_tt - 1) / n_tt + 31) / 32;  // of a tile, by 32 tokens
-  if (a.T <= 16) stream<1>(a, stream_);
-  else if (streams <= kCus && a.T <= 32) stream<2>(a, stream_);
-  else if (streams <= kCus) stream<4>(a, stream_);
+  // Few tokens by streams, which put twice the workgroups on the rows of W, where
+  // there is enough of it for each: up to 16, and up to 32 where all of them run at
+  // once. Streams and tiles, H = 4 096: one row over 151 936 108 and 121 us, over
+  // 32 003 32 and 38, over 8 000 20 and 18; 32 rows over 151 936 133 and 125, over
+  // 32 003 31 and 34, over 8 000 23 and 18; 64 rows over 32 003 36 and 36. H = 1 024,
+  // over 50 021: 16 and 12, 20 and 13.
+  const int64_t blocks = (a.V + kInt8BlockV - 1) / kInt8BlockV;
+  const bool streams = a.H > 15 * kInt8StageK && blocks > kCus / 4;
+  if (streams && a.T <= 16) stream<1>(a, stream_);
+  else if (streams && a.T <= 32 && blocks <= kCus) stream<2>(a, stream_);
   else if (width <= 2) tiles<2>(a, stream_);
   else if (width <= 4) tiles<4>(a, stream_);
   else if (width <= 5) tiles<5>(a, stream_);

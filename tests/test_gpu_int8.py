@@ -129,12 +129,16 @@ def codes(rng, rows, h, pad=0, lead=0, low=-127):
 SIZES = [(1, 1, 1), (1, 128, 64), (2, 127, 129), (3, 257, 33), (16, 300, 256), (17, 129, 100),
          (31, 515, 1001), (33, 1000, 384), (64, 640, 128), (65, 700, 130), (100, 1025, 640),
          (129, 384, 17), (257, 513, 256), (300, 2049, 72), (513, 1300, 200)]
-# More work than the CUs take at once by streams: tiles of 64, 128, 160, 192 and 256
-# tokens, one, two and three of them, rows of one stage and more, ends inside a tile
-# and a block.
+# Tiles of 64, 128, 160, 192 and 256 tokens, one, two and three of them, rows of one
+# stage and more, ends inside a tile and a block.
 SIZES += [(17, 33000, 33), (64, 32897, 200), (100, 17000, 129), (150, 11100, 128),
           (190, 11009, 300), (200, 8300, 16), (256, 8321, 257), (300, 6600, 385),
-          (384, 6001, 100), (513, 4000, 520), (700, 3001, 72), (2000, 1152, 500)]
+          (384, 6001, 100), (513, 4000, 520), (700, 3001, 72), (2000, 1152, 500),
+          (100, 33001, 129), (250, 40000, 130), (300, 33100, 70), (390, 32900, 40),
+          (160, 33000, 256), (180, 65700, 64), (64, 65700, 256)]
+# Streams: few tokens, rows of 16 stages and more, and enough of them.
+SIZES += [(1, 8321, 2000), (16, 8321, 2048), (5, 10001, 4100), (17, 8400, 1921), (32, 32700, 2050),
+          (9, 33000, 1930), (32, 32800, 2000)]
 
 
 @pytest.mark.parametrize("dtype", list(TYPES))
