@@ -5,10 +5,9 @@
 //
 // Two ways through a row, chosen by its settings alone:
 //
-// By a short list (top_k in [1, 420] (200 for distributions), the greedy draw, min-p
-// alone, and up to 420
-// top logits): collect_kernel reads the row once, keeps the tokens that can still
-// be among the first in a list in LDS, and sums exp(z - m) per wave and chunk for
+// By a short list (top_k in [1, 420], of distributions in [1, 200], the greedy draw,
+// a draw by min-p alone, and up to 420 top logits): collect_kernel reads the row once,
+// keeps the tokens that can still be among the first in a list in LDS, and sums exp(z - m) per wave and chunk for
 // the log-sum-exp, which log_sum corrects by the listed tokens. The list is
 // sorted; everything else is decided in it, with weights and sums in fp64. Where
 // there are few rows, a row is cut into slices, each leaves its list, and
@@ -24,6 +23,9 @@
 // slices). Prefix sums over the buckets find the bucket in which a rank or a
 // mass is reached; only that bucket's tokens are then listed, sorted and
 // summed.
+//
+// A distribution that keeps every token, or those that min-p leaves, takes neither:
+// its weights are summed as they are.
 //
 // What a kernel does it for, its Job, is a template parameter: the instances for
 // the draw and the top logits are compiled in select.hip, those for the
@@ -810,8 +812,9 @@ __device__ __forceinline__ void collect_buckets(const Row<D>& row, S& sh, int c0
 // Where every token is kept, or those that min-p leaves, nothing has to be ordered:
 // a row's weights are summed, in fp64, as what is drawn between two distributions
 // needs digits that fp32's exponentials lose (5.5e-11 of a weight are enough: a
-// random number has steps of 2^-24). An element takes 15 instructions,
-// which bounds it: rows of 151 936 bf16 logits, 1 920 of them, take 177 us.
+// random number has steps of 2^-24). An element takes 15 vector instructions and its
+// share of the rest 3 more, which bounds it: 1 920 rows of 151 936 bf16 logits take
+// 177 us, the vector units busy for 84 % of them.
 
 constexpr double kLog2E = 1.4426950408889634;
 
