@@ -54,6 +54,16 @@ def _aligned_codes(name: str, t: torch.Tensor):
     return rows, h, ld
 
 
+def _apart(out: torch.Tensor, name: str, t: torch.Tensor):
+    """Refuses an output whose rows reach into an input's."""
+    if not out.numel() or not t.numel():
+        return
+    extent = lambda m: ((m.shape[0] - 1) * m.stride(0) + m.shape[1]) * m.element_size()  # noqa: E731
+    a, b = t.data_ptr(), out.data_ptr()
+    if a < b + extent(out) and b < a + extent(t):
+        raise ValueError(f"out must lie apart from {name}")
+
+
 def quantize_int8(x: torch.Tensor, *, out: torch.Tensor | None = None,
                   scale: torch.Tensor | None = None, bad_rows: torch.Tensor | None = None,
                   check: bool = False):
@@ -78,6 +88,7 @@ def quantize_int8(x: torch.Tensor, *, out: torch.Tensor | None = None,
         if not isinstance(out, torch.Tensor) or out.device != dev or tuple(out.shape) != (r, h):
             raise ValueError(f"out must be [{r}, {h}] on x's device")
         _, _, ldq = _aligned_codes("out", out)
+        _apart(out, "x", x)
         torch.autograd.graph.increment_version(out)
     if scale is None:
         scale = torch.empty(r, dtype=torch.float32, device=dev)
@@ -132,6 +143,8 @@ def logits_int8(x: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, w_scale
         if out.requires_grad:
             raise ValueError("out must not require gradients")
         _, _, _, ld, code = _rows("out", out, None)
+        _apart(out, "x", x)
+        _apart(out, "w", w)
         torch.autograd.graph.increment_version(out)
     L = lib()
     ws = _workspace(workspace, L.lp_logits_int8_workspace_bytes(t, h), dev)

@@ -135,7 +135,7 @@ SIZES += [(17, 33000, 33), (64, 32897, 200), (100, 17000, 129), (150, 11100, 128
           (190, 11009, 300), (200, 8300, 16), (256, 8321, 257), (300, 6600, 385),
           (384, 6001, 100), (513, 4000, 520), (700, 3001, 72), (2000, 1152, 500),
           (100, 33001, 129), (250, 40000, 130), (300, 33100, 70), (390, 32900, 40),
-          (160, 33000, 256), (180, 65700, 64), (64, 65700, 256)]
+          (160, 33000, 256), (180, 65700, 64), (64, 65700, 256), (100, 140000, 64), (33, 140000, 140)]
 # Streams: few tokens, rows of 16 stages and more, and enough of them.
 SIZES += [(1, 8321, 2000), (16, 8321, 2048), (5, 10001, 4100), (17, 8400, 1921), (32, 32700, 2050),
           (9, 33000, 1930), (32, 32800, 2000)]
@@ -362,6 +362,11 @@ def test_refusals_on_the_device():
             lp.logits_int8(*args)
         with pytest.raises(ValueError, match=text):
             lp.score_int8(*args, ids)
+    wide = torch.zeros(4, 64, device=DEV)
+    with pytest.raises(ValueError, match="apart from x"):
+        lp.quantize_int8(wide, out=wide.view(torch.int8)[:, :64])
+    with pytest.raises(ValueError, match="apart from x"):
+        lp.logits_int8(wide.view(torch.int8)[:, :48], xs, w, ws, out=wide[:, 40:49])
     short = torch.zeros(33, dtype=torch.int8, device=DEV).view(1, 33)
     with pytest.raises(ValueError, match="last row"):
         lp.logits_int8(codes(rng, 4, 33)[0], xs, short, ws[:1])
