@@ -228,3 +228,55 @@ def test_verified_rows_past_32_bits(how):
         want = oracle_verify.verify(z.double().cpu().numpy(), ids.cpu().numpy(), u.cpu().numpy(),
                                     y.double().cpu().numpy(), **how)
         assert np.array_equal(got[0].cpu().numpy(), want[0])
+
+
+# ---- The most rows -----------------------------------------------------------------
+
+def test_the_most_rows_quantised():
+    x = torch.arange(16777215, device=DEV, dtype=torch.float32)[:, None] - 8e6
+    q, s = lp.quantize_int8(x)
+    assert torch.equal(s, x[:, 0].abs() * np.float32(np.float32(1) / np.float32(127)))
+    # (|x| / scale is within a rounding of 127.)
+    assert torch.equal(q[:, 0].long(), 127 * torch.sign(x[:, 0]).long())
+    with pytest.raises(lp.LpError):
+        lp.quantize_int8(torch.empty(16777216, 1, device=DEV))
+
+
+def test_hundreds_of_thousands_of_tokens():
+    t, v, h = 300001, 130, 40
+    g = torch.Generator(device=DEV).manual_seed(2)
+    w, ws = lp.quantize_int8(torch.randn(v, h, generator=g, device=DEV))
+    x, xs = lp.quantize_int8(torch.randn(t, h, generator=g, device=DEV))
+    z = lp.logits_int8(x, xs, w, ws, torch.float32)
+    want = (x.float() @ w.float().t()) * xs[:, None] * ws  # (sums below 2^24: exact)
+    assert torch.equal(z, want)
+    ids = torch.arange(t, device=DEV) % v
+    got = lp.score_int8(x, xs, w, ws, ids, check=True)
+    exact = torch.log_softmax(z.double(), dim=1).gather(1, ids[:, None])[:, 0]
+    assert (got.double() - exact).abs().max() <= 2e-5
+
+
+@pytest.mark.parametrize("how", [dict(), dict(temperature=0.0), dict(top_p=0.6)], ids=str)
+def test_the_most_sequences(how):
+    """Without drafts each draws one token: as sample() would, but in index order."""
+    b, v = 4194303, 3
+    g = torch.Generator(device=DEV).manual_seed(2)
+    z = torch.randn(b, v, generator=g, device=DEV)
+    u = torch.rand(b, 1, generator=g, device=DEV)
+    ids = torch.empty(b, 0, dtype=torch.int64, device=DEV)
+    tokens, accepted, raw, proc = lp.verify(z, ids, u, check=True, **how)
+    assert (accepted == 0).all()
+    p = torch.softmax(z.double(), dim=1)
+    if "top_p" in how:
+        top, order = p.sort(dim=1, descending=True)
+        gone = top.cumsum(dim=1) - top >= np.float64(np.float32(0.6))
+        p = p.masked_fill(torch.zeros_like(gone).scatter(1, order, gone), 0.0)
+    elif how:
+        p = torch.zeros_like(p).scatter(1, z.argmax(dim=1, keepdim=True), 1.0)
+    c = p.cumsum(dim=1)
+    want = (c <= u.double() * c[:, -1:]).sum(dim=1)
+    # (Borders within fp64's roundings of either side may fall to the other.)
+    assert (tokens[:, 0] != want).sum() <= 2
+    with pytest.raises((lp.LpError, ValueError)):
+        lp.verify(torch.empty(b + 1, 1, device=DEV), torch.empty(b + 1, 0, dtype=torch.int64, device=DEV),
+                  torch.empty(b + 1, 1, device=DEV))
