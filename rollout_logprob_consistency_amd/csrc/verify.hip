@@ -35,10 +35,11 @@ int64_t stretches_of(int64_t V, int32_t dtype) {
 // Workgroups that run at once: of residual_kernel six on each of 256 CUs, of
 // collect_kernel three.
 constexpr int64_t kVerifyPlaces = 1536;
-// Slices of all rows. More of them shorten the longest row's way (64 sequences of 4
-// drafts, settings of their own: 239 us with the draw's 512) until joining them
-// takes longer (190 us with 640, 183 with 1 280, 190 with 2 560).
-constexpr int64_t kLimitPlaces = 1280;
+// Slices of all rows. More of them shorten the longest row's way (64 sequences of up
+// to 4 drafts, settings of their own: 205 us with 768, 146 with 1 280, 141 with 2 048,
+// 142 with 3 000) until joining them takes longer (nucleus rows, 64 sequences of 4:
+// 205, 208, 214 and 224 us).
+constexpr int64_t kLimitPlaces = 2048;
 constexpr int64_t kWholePlaces = 768;
 static_assert(LP_VERIFY_MAX_DRAFTS < 64, "a wave holds a sequence's positions");
 
