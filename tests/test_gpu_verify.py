@@ -62,7 +62,9 @@ SETTINGS = [dict(), dict(temperature=0.7), dict(temperature=1.4, top_p=0.9),
             dict(top_k=20, top_p=0.8), dict(top_k=1), dict(min_p=0.05), dict(temperature=0.0),
             dict(top_k=500), dict(top_k=200), dict(top_k=201, min_p=0.01),
             dict(top_k=600, top_p=0.95, min_p=0.01), dict(top_p=0.5, min_p=0.2),
-            dict(top_p=0.0), dict(top_p=0.9, min_p=1.5), dict(temperature=0.2)]
+            dict(top_p=0.0), dict(top_p=0.9, min_p=1.5), dict(temperature=0.2),
+            dict(temperature=1e-3), dict(temperature=2.0 ** -126), dict(temperature=1e30),
+            dict(temperature=1e-30, top_p=0.9), dict(temperature=1e4, min_p=0.5)]
 
 
 @pytest.mark.parametrize("dtype", list(TYPES))
