@@ -371,8 +371,9 @@ __device__ __forceinline__ void finish(const VerifyArgs& a, const Sequence& s, F
       const int64_t row = target_row(a, s.b, tid);
       const SelectLimit l = r.limits[row];
       const double gap = ((double)logit_at<D>(r.logits, r.ld, row, t) - l.base) * s.inv_tau;
-      logprob = (float)(gap - l.ln_all);
-      processed = (float)(gap - l.ln_kept);
+      // (A token that holds all the weight: the sums' last digits may leave them below it.)
+      logprob = (float)fmin(gap - l.ln_all, 0.0);
+      processed = (float)fmin(gap - l.ln_kept, 0.0);
     }
     const int64_t out = s.b * width + tid;
     a.out_tokens[out] = t;
