@@ -147,8 +147,8 @@ lp_status lp_sample(const void* logits, int64_t ld, int32_t dtype, int64_t N,
  * gives tokens -1, NaN scores and accepted -1, and is counted in bad_rows.
  * Rows, ids and random numbers behind a sequence's drafts are not read.
  *
- * Precision: p and q in fp64, each weight to 1.1e-12 and the sum of a row that is kept
- * whole to 5.5e-11 relative, with C and the borders as lp_sample has them otherwise;
+ * Precision: p and q in fp64, each weight, and the sum of a row that is kept whole, to
+ * 1.1e-12 relative, with C and the borders as lp_sample has them otherwise;
  * acceptances, the sums over r and the last token are decided in fp64, sums in
  * an order fixed by V_true and the dtype. Scores are rounded to fp32 once.
  *

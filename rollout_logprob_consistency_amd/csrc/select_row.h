@@ -811,10 +811,10 @@ __device__ __forceinline__ void collect_buckets(const Row<D>& row, S& sh, int c0
 // ---- Rows that are summed whole (kLimit) ----------------------------------------
 // Where every token is kept, or those that min-p leaves, nothing has to be ordered:
 // a row's weights are summed, in fp64, as what is drawn between two distributions
-// needs digits that fp32's exponentials lose (5.5e-11 of a weight are enough: a
-// random number has steps of 2^-24). An element takes 15 vector instructions and its
-// share of the rest 3 more, which bounds it: 1 920 rows of 151 936 bf16 logits take
-// 177 us, the vector units busy for 84 % of them.
+// needs digits that fp32's exponentials lose, and as a near-certain token's score is
+// what they leave. An element takes 16 vector instructions and its share of the rest 3
+// more, which bounds it: 1 920 rows of 151 936 bf16 logits take 188 us, the vector units
+// busy for 84 % of them.
 
 constexpr double kLog2E = 1.4426950408889634;
 
@@ -893,7 +893,7 @@ __device__ __forceinline__ Part whole_part(Groups<D>& v, int groups, double c, b
   float most;
   const double b900 = b + kExp2From;
   p.s = sum_groups<D>(v.g, groups, most,
-                      [&](float z) LP_INLINE { return exp2_900<7>(fma((double)z, c, b900)); });
+                      [&](float z) LP_INLINE { return exp2_900(fma((double)z, c, b900)); });
   if (__ballot(!(most < INFINITY))) return {p.m, (double)NAN};
   if (__ballot(most > -INFINITY) == 0) return {-INFINITY, 0.0};
   // (b's rounding is 2^-38 at most below 2^16.)

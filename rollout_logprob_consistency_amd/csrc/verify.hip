@@ -192,11 +192,11 @@ struct Weights {
   __device__ __forceinline__ void weigh(const Loaded& l, double (&w)[D::kVec]) const {
     if (plain) {
 #pragma unroll
-      for (int i = 0; i < D::kVec; ++i) w[i] = exp2_900<8>(fma((double)l.z.get(i), p.c, p_off));
+      for (int i = 0; i < D::kVec; ++i) w[i] = exp2_900(fma((double)l.z.get(i), p.c, p_off));
       if (!draft) return;
 #pragma unroll
       for (int i = 0; i < D::kVec; ++i)
-        w[i] = fmax(w[i] - exp2_900<8>(fma((double)l.y.get(i), q.c, q_off)), 0.0);
+        w[i] = fmax(w[i] - exp2_900(fma((double)l.y.get(i), q.c, q_off)), 0.0);
       return;
     }
 #pragma unroll
