@@ -1666,8 +1666,9 @@ __device__ __forceinline__ void draw_from_buckets(const SelectArgs& a, const Set
     // (z - anchor) / tau: the logarithms below are in the anchor's units.
     const double s = ((double)z - row.anchor) / tau;
     a.out_token[n] = token_index(f.key);
-    a.out_logprob[n] = (float)(s - log(all.mass));
-    if (a.out_processed) a.out_processed[n] = (float)(s - log(mass));
+    // (A token that holds all the weight: the masses' last digits may leave them below it.)
+    a.out_logprob[n] = (float)fmin(s - log(all.mass), 0.0);
+    if (a.out_processed) a.out_processed[n] = (float)fmin(s - log(mass), 0.0);
     if (a.out_kept) a.out_kept[n] = (int32_t)kept;
   }
 }

@@ -60,3 +60,20 @@ def test_rows_summed_whole(how, v, dtype):
     assert np.array_equal(tokens, want[0]) and np.array_equal(accepted, want[1])
     for score, ref in zip(scores, want[2:]):
         assert (np.abs(score - ref) <= E * np.abs(ref) + 1.1e-12 + 2.0 ** -40).all()
+
+
+@pytest.mark.parametrize("gap", [20.0, 23.0, 26.0])
+@pytest.mark.parametrize("how", [dict(), dict(top_p=0.5), dict(top_k=500, top_p=0.5),
+                                 dict(top_p=0.5, temperature=0.8)], ids=str)
+def test_certain_tokens_of_draws(how, gap):
+    """A token so far above the others that a nucleus keeps it alone, in rows of buckets
+    whose base is another token's logit."""
+    rng = np.random.default_rng(int(gap))
+    n, v = 200, 20011
+    z = rng.normal(size=(n, v)) * 0.3
+    z[np.arange(n), rng.integers(0, v, n)] = gap + 3 * rng.random(n)
+    logits, _ = place(z)
+    _, raw, proc, kept = lp.sample(logits, dev(rng.random(n) * 0.5, torch.float32), **how)
+    assert (raw <= 0).all() and (proc <= 0).all()
+    if "top_p" in how:
+        assert (kept == 1).all() and (proc >= -1e-12).all()
