@@ -110,11 +110,12 @@ lp_status lp_logits_int8(const int8_t* x, int64_t ldx, const float* x_scale,
  * joined in a fixed order; as lp_score, within about 1e-5 nats at logits of
  * ordinary size. Logits in fp32 are taken as (S w_scale) x_scale here, so
  * |S w_scale| has to stay below fp32's largest number and
- * w_scale above its smallest normal one.
+ * w_scale above its smallest normal one. Logits over the temperature are fp32
+ * numbers too, in units of ln 2: |z| / temperature has to stay below 2.3e38.
  *
  * Layout and errors as for lp_logits_int8, target_ids [T] int64, out_logprob
- * and out_lse [T] fp32; LP_EINVAL for a temperature that is not positive and
- * finite or an unknown flag. Workspace: lp_score_int8_workspace_bytes(T, H,
+ * and out_lse [T] fp32; LP_EINVAL for a temperature that is not a positive
+ * normal number or an unknown flag. Workspace: lp_score_int8_workspace_bytes(T, H,
  * V_true).
  * ------------------------------------------------------------------------ */
 size_t lp_score_int8_workspace_bytes(int64_t T, int64_t H, int64_t V_true);

@@ -16,6 +16,9 @@ constexpr int64_t kI32Max = std::numeric_limits<int32_t>::max();
 
 bool dtype_ok(int32_t dtype) { return dtype == LP_F32 || dtype == LP_BF16 || dtype == LP_F16; }
 
+// (Below 2^-126 the kernels' fp32 scale log2(e) / t would be infinite.)
+bool temperature_ok(float t) { return isnormal(t) && t > 0.0f; }
+
 // Rows of a dispatch of one 256-thread workgroup for each, at most 2^32 - 1
 // work-items.
 constexpr int64_t kRowsMax = 16777215;
@@ -112,8 +115,7 @@ lp_status lp_score_int8(const int8_t* x, int64_t ldx, const float* x_scale, cons
                         int64_t H, int64_t V_true, float temperature, uint32_t flags,
                         float* out_logprob, float* out_lse, int32_t* bad_rows, void* workspace,
                         size_t workspace_bytes, hipStream_t stream) {
-  if (!(isfinite(temperature) && temperature > 0.0f) || (flags & ~LP_SCORE_BF16_LOGITS))
-    return LP_EINVAL;
+  if (!temperature_ok(temperature) || (flags & ~LP_SCORE_BF16_LOGITS)) return LP_EINVAL;
   lp::Int8Args a;
   bool go;
   const lp_status st = product_args(x, ldx, x_scale, w, ldw, w_scale, T, H, V_true, &a, &go);
