@@ -81,8 +81,9 @@ const char* lp_status_string(lp_status status);
  *                bytes, 256-byte aligned; contents on entry are ignored.
  *
  * Errors: LP_EINVAL for T < 0, H < 1, V_rows < 1, V_true outside
- * [1, V_rows], ldh < H, a temperature that is not finite and > 0, a NULL
- * required pointer, or a workspace that is too small or misaligned.
+ * [1, V_rows], ldh < H, a temperature that is not finite and > 0 or lies below
+ * 4.24e-39 (log2(e) over it has to be an fp32 number), a NULL required
+ * pointer, or a workspace that is too small or misaligned.
  * LP_EUNSUPPORTED for H % 64 != 0, ldh % 8 != 0 or misaligned hidden/w; for
  * sizes whose dispatches would exceed 2^32 - 1 work-items (more than
  * 16 777 215 tiles of 352 x 256, or T above 268 435 455); and for

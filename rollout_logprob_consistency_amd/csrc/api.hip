@@ -15,6 +15,13 @@ bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p
 
 constexpr int64_t kI32Max = std::numeric_limits<int32_t>::max();
 
+// The kernels' scale log2(e) / t is an fp32 number: below 4.24e-39 it would be infinite,
+// and every score NaN.
+constexpr double kLog2E = 1.4426950408889634;
+bool temperature_ok(float t) {
+  return isfinite(t) && t > 0.0f && kLog2E / (double)t <= std::numeric_limits<float>::max();
+}
+
 // The scoring kernels address a tile's rows through buffer resources with
 // 32-bit byte offsets and a range of at most kSpanMax bytes from the tile's
 // first row: a token tile reaches 255 rows of stride ldh plus one row of H
@@ -92,7 +99,7 @@ lp_status lp_score_shard(const void* hidden_bf16, int64_t ldh, const void* w_sha
   if (T < 0 || H < 1 || ldh < H || !shard_args_ok(V_true, n_shards, rank)) return LP_EINVAL;
   if (flags & ~kScoreFlags) return LP_EINVAL;
   const bool stats = (flags & LP_SCORE_STATS) != 0;
-  if (!(isfinite(temperature) && temperature > 0.0f)) return LP_EINVAL;
+  if (!temperature_ok(temperature)) return LP_EINVAL;
   if (T == 0) return LP_OK;
   const lp_vocab_shard sh = shard_of(V_true, n_shards, rank);
   const int64_t rows = sh.row_end - sh.row_begin;
@@ -122,7 +129,7 @@ lp_status lp_score_shard(const void* hidden_bf16, int64_t ldh, const void* w_sha
   a.bf16_logits = (flags & LP_SCORE_BF16_LOGITS) != 0;
   a.n_vt = (int32_t)n_vt;
   a.n_tt = (int32_t)n_tt;
-  a.scale2 = (float)(1.4426950408889634 / (double)temperature);
+  a.scale2 = (float)(kLog2E / (double)temperature);
   char* base = static_cast<char*>(workspace);
   a.part_m = reinterpret_cast<float*>(base + ws.off_m);
   a.part_s = reinterpret_cast<float*>(base + ws.off_s);
@@ -211,7 +218,7 @@ lp_status score_impl(const void* hidden_bf16, int64_t ldh, const void* w_bf16,
                      hipStream_t stream) {
   if (T < 0 || H < 1 || V_rows < 1 || V_true < 1 || V_true > V_rows || ldh < H)
     return LP_EINVAL;
-  if (!(isfinite(temperature) && temperature > 0.0f)) return LP_EINVAL;
+  if (!temperature_ok(temperature)) return LP_EINVAL;
   if (T == 0) return LP_OK;
   if (!hidden_bf16 || !w_bf16 || !target_ids || !out_logprob || !workspace) return LP_EINVAL;
   if (stats && (!out_entropy || !out_argmax)) return LP_EINVAL;
@@ -238,7 +245,7 @@ lp_status score_impl(const void* hidden_bf16, int64_t ldh, const void* w_bf16,
   a.bf16_logits = bf16;
   a.n_vt = (int32_t)n_vt;
   a.n_tt = (int32_t)n_tt;
-  a.scale2 = (float)(1.4426950408889634 / (double)temperature);
+  a.scale2 = (float)(kLog2E / (double)temperature);
   char* base = static_cast<char*>(workspace);
   a.part_m = reinterpret_cast<float*>(base + ws.off_m);
   a.part_s = reinterpret_cast<float*>(base + ws.off_s);
@@ -492,7 +499,7 @@ lp_status lp_score_noalloc(const void* hidden_bf16, int64_t ldh, const void* w_b
   // scratch limit; only then any HIP call.
   if (T < 0 || H < 1 || V_rows < 1 || V_true < 1 || V_true > V_rows || ldh < H)
     return LP_EINVAL;
-  if (!(isfinite(temperature) && temperature > 0.0f)) return LP_EINVAL;
+  if (!temperature_ok(temperature)) return LP_EINVAL;
   if (T == 0) return LP_OK;
   if (!hidden_bf16 || !w_bf16 || !target_ids || !out_logprob) return LP_EINVAL;
   if (lp::score_workspace_layout(T, V_true, false).total > (size_t)LP_NOALLOC_SCRATCH_BYTES)
