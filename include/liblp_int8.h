@@ -83,9 +83,8 @@ lp_status lp_quantize_int8(const void* x, int64_t ldx, int32_t dtype, int64_t R,
  * Errors: LP_EINVAL for T < 0, H < 1, V < 1, ldx < H, ldw < H, ld_out < V, an
  * unknown dtype, NULL or misaligned pointers, a small workspace;
  * LP_EUNSUPPORTED for H above LP_INT8_MAX_HIDDEN, ldw not a multiple of 16, ldw
- * or ld_out above 2^22, T above 4 194 240, V above 2^31 - 256, or more tiles of 128 rows
- * of w by 64 rows of x than one dispatch holds (16 777 215). T == 0 does
- * nothing.
+ * or ld_out above 2^22, T above 4 194 240, V above 2^31 - 256, or more tiles of 256
+ * rows of w by 256 rows of x than 2^31 - 513. T == 0 does nothing.
  * ------------------------------------------------------------------------ */
 size_t lp_logits_int8_workspace_bytes(int64_t T, int64_t H);
 

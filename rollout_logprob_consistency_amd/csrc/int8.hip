@@ -745,8 +745,13 @@ Int8Workspace int8_workspace_layout(int64_t T, int64_t H, int64_t V) {
 }
 
 bool int8_grid_ok(int64_t T, int64_t V) {
-  const int64_t blocks = (V + kInt8BlockV - 1) / kInt8BlockV, tiles = (T + 63) / 64;
-  return tiles <= 65535 && blocks * tiles <= kMaxDispatchItems / (64 * kStreamWaves) &&
+  // Streams have a workgroup a block, and the tile kernel counts its tiles, and the
+  // grid's stride past them, in 32 bits: ceil(T / 256) tiles along the tokens, or more
+  // of them where there are fewer than kCus in all.
+  const int64_t blocks = (V + kInt8BlockV - 1) / kInt8BlockV;
+  const int64_t tiles = (V + kTileRows - 1) / kTileRows * ((T + 255) / 256);
+  return T <= kInt8TokensMax && blocks <= kMaxDispatchItems / (64 * kStreamWaves) &&
+         tiles <= INT32_MAX - 2 * kCus &&
          (T + kMergeTokens - 1) / kMergeTokens <= kMaxDispatchItems / (64 * kMergeWaves);
 }
 

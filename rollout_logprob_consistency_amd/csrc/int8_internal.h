@@ -68,8 +68,10 @@ struct Int8Workspace {
 // V = 0: rows of logits, no partials.
 Int8Workspace int8_workspace_layout(int64_t T, int64_t H, int64_t V);
 
-// Whether every dispatch of a product of these sizes fits 2^32 - 1 work-items
-// and the grid's 65 535 rows of workgroups.
+// Most tokens of a product, as the interface names it.
+constexpr int64_t kInt8TokensMax = 4194240;
+// Whether every dispatch of a product of these sizes fits 2^32 - 1 work-items, and
+// its tiles 32 bits.
 bool int8_grid_ok(int64_t T, int64_t V);
 
 // `a.staged` is used where x is not read in place.

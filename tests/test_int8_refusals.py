@@ -26,3 +26,14 @@ def test_subnormal_temperatures_are_refused(L, t):
     """Their fp32 scale would be infinite, and every score NaN."""
     for flags in (0, 2):
         assert score(L, t=t, flags=flags) == EINVAL
+
+
+def test_sizes_that_the_kernels_take(L):
+    """A call passes the checks of its sizes if it gets as far as its workspace. The tile
+    kernel is persistent: how many tiles there are is no matter of the dispatch."""
+    for T, V in ((905000, 151936), (4194240, 151936), (4194240, 1 << 20), (33, 2 ** 31 - 256)):
+        assert score(L, T=T, V=V, wkb=0) == EINVAL
+    # More tiles than 32 bits count.
+    for T, V in ((4194240, 2 ** 25), (65281, 2 ** 31 - 256)):
+        assert score(L, T=T, V=V) == EUNSUP
+    assert score(L, T=4194241) == EUNSUP
