@@ -50,10 +50,10 @@ extern "C" {
  *
  * Layout: q [R, H] with row stride ldq, a multiple of 16, and 16-byte aligned,
  * as the products below take it; the codes behind H up to the next multiple of
- * 16 are written as zeros; q and scale lie apart from x. Errors: LP_EINVAL for R < 0, H < 1, ldx < H, ldq < H
- * or not a multiple of 16, an unknown dtype, NULL or misaligned pointers;
- * LP_EUNSUPPORTED for R or H above 2^31 - 1 or more rows than one dispatch
- * holds (16 777 215). R == 0 does nothing.
+ * 16 are written as zeros; q and scale lie apart from x and from each other.
+ * Errors: LP_EINVAL for R < 0, H < 1, ldx < H, ldq < H or not a multiple of 16,
+ * an unknown dtype, NULL or misaligned pointers; LP_EUNSUPPORTED for R or H above
+ * 2^31 - 1 or more rows than one dispatch holds (16 777 215). R == 0 does nothing.
  * ------------------------------------------------------------------------ */
 lp_status lp_quantize_int8(const void* x, int64_t ldx, int32_t dtype, int64_t R,
                            int64_t H, int8_t* q, int64_t ldq, float* scale,
@@ -113,7 +113,7 @@ lp_status lp_logits_int8(const int8_t* x, int64_t ldx, const float* x_scale,
  * numbers too, in units of ln 2: |z| / temperature has to stay below 2.3e38.
  *
  * Layout and errors as for lp_logits_int8, target_ids [T] int64, out_logprob
- * and out_lse [T] fp32; LP_EINVAL for a temperature that is not a positive
+ * and out_lse [T] fp32, apart from the inputs; LP_EINVAL for a temperature that is not a positive
  * normal number or an unknown flag. Workspace: lp_score_int8_workspace_bytes(T, H,
  * V_true).
  * ------------------------------------------------------------------------ */

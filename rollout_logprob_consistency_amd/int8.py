@@ -10,12 +10,12 @@ and every arithmetic step runs in the library's kernels.
 A matrix in 8 bits is int8 codes [rows, H] with unit column stride and one fp32
 scale per row. The head's rows start at multiples of 16 bytes, as quantize_int8
 lays them out, and its last one has room for whole groups of 16; hidden states may
-lie anywhere. Outputs lie apart from the inputs. The results carry no derivative.
-Scratch memory is allocated per call unless `workspace` is given (a uint8 tensor
-of the library's *_workspace_bytes, 256-byte aligned); calls that may overlap,
-captured graphs among them, must not share one. `bad_rows` (int32 [1]) is a
-counter that a call adds its bad rows to; with check=True a call raises for its
-own rows only.
+lie anywhere. Outputs lie apart from the inputs and from each other. The results
+carry no derivative. Scratch memory is allocated per call unless `workspace` is
+given (a uint8 tensor of the library's *_workspace_bytes, 256-byte aligned); calls
+that may overlap, captured graphs among them, must not share one. `bad_rows` (int32
+[1]) is a counter that a call adds its bad rows to; with check=True a call raises
+for its own rows only.
 """
 
 from __future__ import annotations
@@ -54,14 +54,24 @@ def _aligned_codes(name: str, t: torch.Tensor):
     return rows, h, ld
 
 
-def _apart(out: torch.Tensor, name: str, t: torch.Tensor):
-    """Refuses an output whose rows reach into an input's."""
-    if not out.numel() or not t.numel():
+def _extent(t: torch.Tensor, width: int | None = None) -> int:
+    """Bytes from the first element's to the last one's end, of rows or of a
+    contiguous vector; `width`: elements that a row takes."""
+    if t.dim() == 2:
+        return ((t.shape[0] - 1) * t.stride(0) + (width or t.shape[1])) * t.element_size()
+    return t.numel() * t.element_size()
+
+
+def _apart(name: str, out: torch.Tensor, others: dict, width: int | None = None):
+    """Refuses an output whose memory, from its first row to its last, reaches into
+    what else the call reads or writes."""
+    if not out.numel():
         return
-    extent = lambda m: ((m.shape[0] - 1) * m.stride(0) + m.shape[1]) * m.element_size()  # noqa: E731
-    a, b = t.data_ptr(), out.data_ptr()
-    if a < b + extent(out) and b < a + extent(t):
-        raise ValueError(f"out must lie apart from {name}")
+    b = out.data_ptr()
+    end = b + _extent(out, width)
+    for other, t in others.items():
+        if t.numel() and t.data_ptr() < end and b < t.data_ptr() + _extent(t):
+            raise ValueError(f"{name} must lie apart from {other}")
 
 
 def quantize_int8(x: torch.Tensor, *, out: torch.Tensor | None = None,
@@ -88,13 +98,15 @@ def quantize_int8(x: torch.Tensor, *, out: torch.Tensor | None = None,
         if not isinstance(out, torch.Tensor) or out.device != dev or tuple(out.shape) != (r, h):
             raise ValueError(f"out must be [{r}, {h}] on x's device")
         _, _, ldq = _aligned_codes("out", out)
-        _apart(out, "x", x)
+        _apart("out", out, dict(x=x), h16)
         torch.autograd.graph.increment_version(out)
     if scale is None:
         scale = torch.empty(r, dtype=torch.float32, device=dev)
         ps = scale.data_ptr()
     else:
         ps = _like("scale", scale, (r,), torch.float32, dev)
+        _apart("scale", scale, dict(x=x))
+        _apart("out", out, dict(scale=scale), h16)
         torch.autograd.graph.increment_version(scale)
     count = _bad_rows(bad_rows, check, dev)
     _call(lib().lp_quantize_int8, dev,
@@ -143,8 +155,7 @@ def logits_int8(x: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, w_scale
         if out.requires_grad:
             raise ValueError("out must not require gradients")
         _, _, _, ld, code = _rows("out", out, None)
-        _apart(out, "x", x)
-        _apart(out, "w", w)
+        _apart("out", out, dict(x=x, x_scale=x_scale, w=w, w_scale=w_scale))
         torch.autograd.graph.increment_version(out)
     L = lib()
     ws = _workspace(workspace, L.lp_logits_int8_workspace_bytes(t, h), dev)
@@ -169,15 +180,18 @@ def score_int8(x: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, w_scale:
     if not 1 <= vt <= v:
         raise ValueError(f"v_true must lie in [1, {v}]")
     pi = _like("ids", ids, (t,), torch.int64, dev)
+    inputs = dict(x=x, x_scale=x_scale, w=w, w_scale=w_scale, ids=ids)
     if out is None:
         out = torch.empty(t, dtype=torch.float32, device=dev)
         po = out.data_ptr()
     else:
         po = _like("out", out, (t,), torch.float32, dev)
+        _apart("out", out, inputs)
         torch.autograd.graph.increment_version(out)
     pl = None
     if lse is not None:
         pl = _like("lse", lse, (t,), torch.float32, dev)
+        _apart("lse", lse, dict(inputs, out=out))
         torch.autograd.graph.increment_version(lse)
     L = lib()
     ws = _workspace(workspace, L.lp_score_int8_workspace_bytes(t, h, vt), dev)
