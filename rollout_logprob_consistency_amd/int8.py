@@ -62,6 +62,14 @@ def _extent(t: torch.Tensor, width: int | None = None) -> int:
     return t.numel() * t.element_size()
 
 
+def _given(name: str, t, shape: tuple, device: torch.device) -> int:
+    """Checks a given fp32 vector that a call writes; returns its address."""
+    p = _like(name, t, shape, torch.float32, device)
+    if t.requires_grad:
+        raise ValueError(f"{name} must not require gradients")
+    return p
+
+
 def _apart(name: str, out: torch.Tensor, others: dict, width: int | None = None):
     """Refuses an output whose memory, from its first row to its last, reaches into
     what else the call reads or writes."""
@@ -104,7 +112,7 @@ def quantize_int8(x: torch.Tensor, *, out: torch.Tensor | None = None,
         scale = torch.empty(r, dtype=torch.float32, device=dev)
         ps = scale.data_ptr()
     else:
-        ps = _like("scale", scale, (r,), torch.float32, dev)
+        ps = _given("scale", scale, (r,), dev)
         _apart("scale", scale, dict(x=x))
         _apart("out", out, dict(scale=scale), h16)
         torch.autograd.graph.increment_version(scale)
@@ -185,12 +193,12 @@ def score_int8(x: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, w_scale:
         out = torch.empty(t, dtype=torch.float32, device=dev)
         po = out.data_ptr()
     else:
-        po = _like("out", out, (t,), torch.float32, dev)
+        po = _given("out", out, (t,), dev)
         _apart("out", out, inputs)
         torch.autograd.graph.increment_version(out)
     pl = None
     if lse is not None:
-        pl = _like("lse", lse, (t,), torch.float32, dev)
+        pl = _given("lse", lse, (t,), dev)
         _apart("lse", lse, dict(inputs, out=out))
         torch.autograd.graph.increment_version(lse)
     L = lib()

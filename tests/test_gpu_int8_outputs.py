@@ -77,3 +77,17 @@ def test_scores(operands):
     lse = torch.empty(6, device=DEV)
     assert torch.equal(got, lp.score_int8(x, xs, w, ws, ids, lse=lse))
     assert torch.equal(both[6:], lse)
+
+
+def test_outputs_that_require_gradients(operands):
+    """Their values would be written over behind autograd's back."""
+    x, xs, w, ws = operands
+    ids = torch.arange(6, device=DEV)
+    leaf = torch.ones(6, device=DEV, requires_grad=True)
+    for name, call in (("scale", lambda: lp.quantize_int8(torch.randn(6, 40, device=DEV), scale=leaf)),
+                       ("out", lambda: lp.score_int8(x, xs, w, ws, ids, out=leaf)),
+                       ("lse", lambda: lp.score_int8(x, xs, w, ws, ids, lse=leaf)),
+                       ("out", lambda: lp.logits_int8(x, xs, w[:1], ws[:1], out=leaf.view(6, 1)))):
+        with pytest.raises(ValueError, match=f"{name} must not require gradients"):
+            call()
+    assert (leaf == 1).all() and leaf._version == 0
