@@ -23,6 +23,7 @@ from __future__ import annotations
 import re
 
 _VREG = re.compile(r"v\[(\d+):(\d+)\]|v(\d+)\b")
+_AREG = re.compile(r"a(?:\[|\d)")
 _STORES = ("ds_write", "buffer_store", "global_store", "scratch_store", "flat_store")
 BEFORE_SLOTS = 4
 AFTER_SLOTS = 20
@@ -149,17 +150,30 @@ def check_no_bpermute(asm: str, name_part: str = "compare_kernel") -> list[str]:
 
 
 def check_no_parked_registers(asm: str, name_part: str) -> list[str]:
-    """Problems: a missing kernel, or an accumulator written by anything but an
-    MFMA (v_accvgpr_write), or scratch memory, inside it. A tile kernel's sums
-    fill the accumulators and start from an MFMA's constant 0, so such a write is
-    a register that the compiler parks; it has parked one in a region that masks
-    lanes and taken it out for all of them."""
+    """Problems: a missing kernel, or, inside it, an accumulator written by anything
+    but an MFMA (a move from a register or another accumulator, or a load from
+    memory or LDS into one), or scratch memory. A tile kernel's sums fill the
+    accumulators and start from an MFMA's constant 0, so such a write is a register
+    that the compiler parks; it has parked one in a region that masks lanes and
+    taken it out for all of them.
+
+    An instruction writes its first operand; a store has none that it writes, and
+    its first may be the accumulator that it stores."""
     bodies = kernel_bodies(asm, name_part)
     if not bodies:
         return [f"no kernel matching {name_part!r} in the assembly"]
     problems = []
     for name, body in bodies.items():
-        n = len(re.findall(r"^\s*(?:v_accvgpr_write|scratch_(?:load|store))", body, re.M))
+        n = 0
+        for line in body.split("\n"):
+            t = line.split(";")[0].strip()
+            if not t or t.startswith("."):
+                continue
+            op, ops = _split(t)
+            if op.startswith(("scratch_load", "scratch_store")):
+                n += 1
+            elif ops and _AREG.match(ops[0]) and not op.startswith(("v_mfma", *_STORES)):
+                n += 1
         if n:
             problems.append(f"{name}: {n} accumulator write(s) or scratch access(es)")
     return problems
