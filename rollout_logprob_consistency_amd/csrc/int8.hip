@@ -209,18 +209,19 @@ __device__ __forceinline__ void store_partial(const Int8Args& a, const float (&y
                                         0, 0);
 }
 
-// Rows behind the vocabulary get weight 0. Where the token's scale is 0, its factor
-// becomes the smallest one: 0 times infinity would be NaN, and |y| 2^-149 stays
-// below 2^-21.
+// Rows behind the vocabulary get weight 0. Where the token's factor is 0 (of a scale of
+// 0), it is multiplied in here, which leaves 0, or NaN beside an infinite scale of the
+// head, and becomes 1: 0 times the infinity that follows would be NaN too.
 __device__ __forceinline__ void mask_tail(const Int8Args& a, float (&y)[kPerLane], float& f, int v0,
                                           int lg) {
   if (v0 + kInt8BlockV <= a.V) return;
-  f = f == 0.0f ? 0x1p-149f : f;
+  const float g = f == 0.0f ? 0.0f : 1.0f;
+  f = f == 0.0f ? 1.0f : f;
   const float none = f < 0.0f ? INFINITY : -INFINITY;
   int left = a.V - v0 - 8 * lg;
   asm volatile("" : "+v"(left));  // (or all tokens' comparisons are made, and kept, at once)
 #pragma unroll
-  for (int k = 0; k < kPerLane; ++k) y[k] = result_row(0, k) < left ? y[k] : none;
+  for (int k = 0; k < kPerLane; ++k) y[k] = result_row(0, k) < left ? y[k] * g : none;
 }
 
 // A token's scale is left to the end (y = S w_scale, z = y x_scale), which spares
