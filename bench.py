@@ -27,7 +27,9 @@ METRIC = "scored tokens/s + % bf16 MFMA peak, H=4096 V=151936; batch-invariance 
 PEAK_BF16_TFLOPS = 2500.0          # MI355X dense bf16 MFMA, published
 PEAK_HBM_GBPS = 8000.0             # MI355X HBM3E, published
 TRAFFIC_FILE = os.path.join(ROOT, "profiles", "score_qwen8b_traffic.json")
-SCORE_SRC = os.path.join(ROOT, "rollout_logprob_consistency_amd", "csrc", "score.hip")
+# What the scoring kernels are compiled from.
+SCORE_SOURCES = [os.path.join(ROOT, "rollout_logprob_consistency_amd", "csrc", f)
+                 for f in ("score.hip", "tile_common.h", "lp_internal.h")]
 
 
 def log(*a):
@@ -35,17 +37,21 @@ def log(*a):
 
 
 def score_source_hash() -> str:
-    return hashlib.sha256(open(SCORE_SRC, "rb").read()).hexdigest()
+    h = hashlib.sha256()
+    for path in SCORE_SOURCES:
+        with open(path, "rb") as f:
+            h.update(f.read())
+    return h.hexdigest()
 
 
 def measured_traffic():
     """Per-launch HBM bytes from the committed rocprofv3 counter summary, or
-    None if there is none or the kernel source changed since it was taken."""
+    None if there is none or the kernels' sources changed since it was taken."""
     try:
         t = json.load(open(TRAFFIC_FILE))
     except (OSError, ValueError):
         return None
-    if t.get("score_hip_sha256") != score_source_hash():
+    if t.get("score_sources_sha256") != score_source_hash():
         return None
     return t.get("bytes_per_launch")
 
