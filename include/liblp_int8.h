@@ -40,7 +40,9 @@ extern "C" {
  * alignment of the element type):
  *
  *   scale[r] = max_k |x[r, k]| times the fp32 number nearest to 1/127, rounded
- *              to fp32
+ *              to fp32 (that number is off by 2^-28, so that the scale of a row
+ *              that is not tiny is max / 127 to 1.07 2^-24, where the rounded
+ *              quotient would be to 2^-24)
  *   q[r, k]  = the integer nearest to x[r, k] / scale[r] (the quotient of the
  *              real numbers, ties to even), within [-127, 127]
  *
@@ -66,8 +68,8 @@ lp_status lp_quantize_int8(const void* x, int64_t ldx, int32_t dtype, int64_t R,
  *
  * S is exact; it is rounded to fp32 (exact below 2^24) and each product is
  * rounded to fp32, then z to `dtype`: an error of at most 3 2^-24 relative
- * and, for bf16 and fp16, one rounding more. fp16 overflows to infinity
- * where |z| passes 65 504. A NaN scale gives NaN.
+ * (where neither product is subnormal) and, for bf16 and fp16, one rounding
+ * more. fp16 overflows to infinity from |z| = 65 520 on. A NaN scale gives NaN.
  *
  * Layout: x [T, H], row stride ldx, any alignment; w [V, H] 16-byte aligned
  * with row stride ldw, a multiple of 16 (what lies behind H up to the next

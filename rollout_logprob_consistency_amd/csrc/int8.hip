@@ -372,7 +372,7 @@ __global__ __launch_bounds__(64 * kStreamWaves) void stream_kernel(Int8Args a) {
 // first are copied, so that the sums' scales, roundings and stores (15 % of a tile
 // of 4 096 hidden elements) are all that the MFMAs wait for. Scores of 8 192 rows over
 // 151 936 x 4 096 take 3.7 ms: 2.7 POP/s, the matrix units busy for 69 % of the time at
-// the 1.9 GHz that the power limit leaves; logits of 320 rows 209 us (1.9 POP/s), where
+// the 1.9 GHz that the power limit leaves; logits of 320 rows 201 to 208 us (1.9 POP/s), where
 // issuing the copies and waiting for a tile's ends weigh more.
 constexpr int kTileRows = 256;                      // of W
 constexpr int kTileThreads = 256;

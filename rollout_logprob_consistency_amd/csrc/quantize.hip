@@ -2,6 +2,9 @@
 //
 //   scale = max |x| (1 / 127),   q = the integer nearest to x / scale
 //
+// (The factor is fp32's 1 / 127, which is off by 2^-28: a row's scale is max / 127 to
+// 1.07 half steps, and its largest code is 127 as it would be after a division.)
+//
 // One pass: a row's lanes hold it in registers between the maximum and the codes, so
 // it is read once (rows of more than 32 KiB are read again, from L2). Memory bounds it:
 // 151 936 rows of 4 096 bf16 take 331 us, 5.6 TB/s read and written.
