@@ -108,8 +108,8 @@ lp_status lp_logits_int8(const int8_t* x, int64_t ldx, const float* x_scale,
  * (of a NaN or infinite scale) gives NaN; -inf is a token of probability 0.
  *
  * Precision: exponentials and sums are fp32, per 128 vocabulary rows and
- * joined in a fixed order; as lp_score, within about 1e-5 nats at logits of
- * ordinary size. Logits in fp32 are taken as (S w_scale) x_scale here, so
+ * joined in a fixed order, the score is taken from them in fp64 and is at most
+ * 0; as lp_score, within about 1e-5 nats at logits of ordinary size. Logits in fp32 are taken as (S w_scale) x_scale here, so
  * |S w_scale| has to stay below fp32's largest number and
  * w_scale above its smallest normal one. Logits over the temperature are fp32
  * numbers too, in units of ln 2: |z| / temperature has to stay below 2.3e38.

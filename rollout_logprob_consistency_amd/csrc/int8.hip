@@ -31,11 +31,10 @@ typedef int i32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kTiles = 8;            // MFMA tiles of a block along the vocabulary
 constexpr int kPerLane = 4 * kTiles; // vocabulary rows of a lane
-constexpr float kLn2 = 0.693147180559945309f;
+constexpr double kLn2 = 0.693147180559945309;
 static_assert(kInt8BlockV == 16 * kTiles, "a block is one wave's");
 
 __device__ __forceinline__ float fast_exp2(float x) { return __builtin_amdgcn_exp2f(x); }
-__device__ __forceinline__ float fast_log2(float x) { return __builtin_amdgcn_logf(x); }
 
 // 16 vocabulary rows x 16 tokens x 64 hidden elements.
 __device__ __forceinline__ i32x4 mma(const i32x4& w, const i32x4& x, const i32x4& c) {
@@ -628,7 +627,7 @@ __device__ __forceinline__ int row_sum(const Int8Args& a, int64_t t, int64_t id)
 template <class Out>
 __global__ __launch_bounds__(64 * kMergeWaves) void merge_kernel(Int8Args a) {
   __shared__ float wave_m[kMergeWaves][kMergeTokens], wave_s[kMergeWaves][kMergeTokens];
-  __shared__ float target[kMergeTokens];
+  __shared__ double target[kMergeTokens];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t t0 = (int64_t)blockIdx.x * kMergeTokens, t = t0 + (lane & 15);
   static_assert(kMergeTokens == kMergeWaves, "a target for each wave");
@@ -638,7 +637,7 @@ __global__ __launch_bounds__(64 * kMergeWaves) void merge_kernel(Int8Args a) {
     if (id >= 0 && id < a.V) {
       const float xs = a.x_scale[mine];
       const float z = score_of(Out(), row_sum(a, mine, id), xs, a.w_scale[id]);
-      if (lane == 0) target[wave] = z * factor_of(Out(), xs, a.scale2);
+      if (lane == 0) target[wave] = (double)z * (double)factor_of(Out(), xs, a.scale2);
     }
   }
   const int blocks = (a.V + kInt8BlockV - 1) / kInt8BlockV;
@@ -679,9 +678,12 @@ __global__ __launch_bounds__(64 * kMergeWaves) void merge_kernel(Int8Args a) {
   for (int g = 1; g < kMergeWaves; ++g) lse_fold(M, S, wave_m[g][lane], wave_s[g][lane]);
   const int64_t id = a.ids[t];
   const bool ok = id >= 0 && id < a.V;
-  const float lse2 = M + fast_log2(S);
-  a.out_lp[t] = ok ? (target[lane] - lse2) * kLn2 : NAN;
-  if (a.out_lse) a.out_lse[t] = lse2 * kLn2;
+  // The maximum is a rounded product, the blocks' terms are of the exact one: a token that
+  // holds all the weight has S next to 2^(target - M), and no score of its own but
+  // what cancels here. (In fp32 its score was off by 2^-24 of its logit, of either sign.)
+  const double lse2 = (double)M + log2((double)S), score = (target[lane] - lse2) * kLn2;
+  a.out_lp[t] = ok ? (float)(score > 0.0 ? 0.0 : score) : NAN;
+  if (a.out_lse) a.out_lse[t] = (float)(lse2 * kLn2);
   if (!ok && a.bad_rows) atomicAdd(a.bad_rows, 1);
 }
 
