@@ -905,7 +905,9 @@ __device__ __forceinline__ void finish_row(const ScoreArgs& a, int t, float M, f
                                            int I, float tv, bool ok) {
   const float l2s = fast_log2(S);
   const float lse2 = M + l2s;
-  a.out_lp[t] = ok ? (tv - lse2) * kLn2 : __builtin_nanf("");
+  // (Of a token that holds all the weight the roundings may leave more than its logit.)
+  const float score = (tv - lse2) * kLn2;
+  a.out_lp[t] = ok ? (score > 0.f ? 0.f : score) : __builtin_nanf("");
   if (a.out_lse) a.out_lse[t] = lse2 * kLn2;
   if (kStats) {
     // H = ln 2 (log2 S - Q / S): the log-sum-exp minus the mean scaled logit.
